@@ -46,6 +46,8 @@ NWC_ERR_HIP = -6
 NWC_ERR_SCRATCH_LIMIT = -7
 NWC_OUT_BF16 = 0
 NWC_OUT_F32 = 1
+NWC_ROPE_HALF = 0
+NWC_ROPE_PAIRS = 1
 
 
 class nwc_params(ctypes.Structure):
@@ -66,6 +68,31 @@ class nwc_info(ctypes.Structure):
                 ("n_symbols", ctypes.c_uint32), ("max_chunk_bits", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32), ("payload_bits", ctypes.c_uint64),
                 ("code_len", ctypes.c_uint8 * 256)]
+
+
+class nwc_heads(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("ld_src", ctypes.c_uint64), ("ld_dst", ctypes.c_uint64), ("heads", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class nwc_rope(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("dims", ctypes.c_uint32), ("style", ctypes.c_uint32)]
+
+
+class nwc_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_uint64),
+                ("page_stride", ctypes.c_uint64), ("kv_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32),
+                ("page_len", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class nwc_page_table(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("ld", ctypes.c_uint64), ("rows", ctypes.c_uint32), ("cols", ctypes.c_uint32)]
+
+
+class nwc_groups(ctypes.Structure):
+    _fields_ = [("start", ctypes.c_void_p), ("len", ctypes.c_void_p), ("count", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
 
 
 class NwcError(RuntimeError):
@@ -105,11 +132,19 @@ _lib.nwc_read_probe.argtypes = [_vp, _sz, _vp, _u32, _i, _vp]
 _lib.nwc_noalloc_scratch_bytes.argtypes = [ctypes.POINTER(_sz)]
 _lib.nwc_gemv_noalloc.argtypes = [ctypes.POINTER(nwc_info), _vp, _vp, _vp, _i, _vp]
 _lib.nwc_set_wait_limit.argtypes = [_u32]
+_f32 = ctypes.c_float
+_lib.nwc_qk_norm_rope.argtypes = [ctypes.POINTER(nwc_heads), ctypes.POINTER(nwc_heads), _u32, _u32, _f32,
+                                  ctypes.POINTER(nwc_rope), _vp, _vp]
+_lib.nwc_kv_append.argtypes = [ctypes.POINTER(nwc_cache), ctypes.POINTER(nwc_page_table), ctypes.POINTER(nwc_heads),
+                               _vp, _u64, ctypes.POINTER(nwc_heads), _u32, _f32, ctypes.POINTER(nwc_rope), _vp, _vp, _vp]
+_lib.nwc_attend_workspace_size.argtypes = [ctypes.POINTER(nwc_cache), _u32, _u32, _u32, ctypes.POINTER(_sz)]
+_lib.nwc_attend.argtypes = [ctypes.POINTER(nwc_cache), ctypes.POINTER(nwc_page_table), ctypes.POINTER(nwc_groups), _vp,
+                            _vp, _u64, _u32, _f32, _vp, _u64, _vp, _sz, _vp]
 for _f in ("nwc_encode_bound", "nwc_encode", "nwc_inspect", "nwc_decode", "nwc_workspace_size", "nwc_gemv",
            "nwc_gemm_skinny", "nwc_bf16_workspace_size", "nwc_gemv_bf16", "nwc_gemv_batched", "nwc_decode_batched",
            "nwc_blas_create", "nwc_blas_destroy", "nwc_prefill_workspace_size", "nwc_gemm_prefill",
            "nwc_gather_rows", "nwc_read_probe", "nwc_noalloc_scratch_bytes", "nwc_gemv_noalloc",
-           "nwc_set_wait_limit"):
+           "nwc_set_wait_limit", "nwc_qk_norm_rope", "nwc_kv_append", "nwc_attend_workspace_size", "nwc_attend"):
     getattr(_lib, _f).restype = _st
 
 # the exported C symbols, for checks against include/nwc.h
@@ -117,7 +152,8 @@ EXPORTS = ("nwc_status_str", "nwc_encode_bound", "nwc_encode", "nwc_inspect", "n
            "nwc_workspace_size", "nwc_gemv", "nwc_gemm_skinny", "nwc_bf16_workspace_size", "nwc_gemv_bf16",
            "nwc_gemv_batched", "nwc_decode_batched", "nwc_blas_create", "nwc_blas_destroy",
            "nwc_prefill_workspace_size", "nwc_gemm_prefill", "nwc_gather_rows", "nwc_read_probe",
-           "nwc_noalloc_scratch_bytes", "nwc_gemv_noalloc", "nwc_set_wait_limit")
+           "nwc_noalloc_scratch_bytes", "nwc_gemv_noalloc", "nwc_set_wait_limit", "nwc_qk_norm_rope",
+           "nwc_kv_append", "nwc_attend_workspace_size", "nwc_attend")
 
 
 def _check(st: int, where: str):
@@ -385,6 +421,220 @@ def nwc_read_probe(buf_dev, sink_dev, groups: int = 0, layout: int = 1, stream=N
     of at least 4 bytes; layout 0 grid-stride, 1 one contiguous range per workgroup."""
     _check(_lib.nwc_read_probe(_dptr(buf_dev), int(buf_dev.numel() * buf_dev.element_size()), _dptr(sink_dev),
                                int(groups), int(layout), _stream(stream)), "nwc_read_probe")
+
+
+# --------------------------------------------------------- attention side ---
+
+_ROPE_STYLES = {"half": NWC_ROPE_HALF, "pairs": NWC_ROPE_PAIRS}
+
+
+class _Call:
+    """Marshalled arguments of one call, built once and reusable (for example
+    inside a captured graph): the tensors are kept alive, must be on one
+    device, and are read and written anew by every call."""
+
+    def __init__(self):
+        self.device = None
+        self._keep = []
+
+    def _tensor(self, t, name: str, dtypes, dim: Optional[int] = None):
+        if not hasattr(t, "data_ptr"):
+            raise ValueError("%s: expected a tensor" % name)
+        if not t.is_cuda:
+            raise ValueError("%s: expected a device (cuda) tensor" % name)
+        if t.dtype not in dtypes:
+            raise ValueError("%s: expected %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+        if dim is not None and t.dim() != dim:
+            raise ValueError("%s: expected %d dimensions, got %d" % (name, dim, t.dim()))
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            raise ValueError("%s: on %s, other tensors on %s" % (name, t.device, self.device))
+        self._keep.append(t)
+        return t.data_ptr()
+
+    def _vector(self, t, name: str, n: int, dtype):
+        p = self._tensor(t, name, (dtype,), 1)
+        if t.numel() != n or not t.is_contiguous():
+            raise ValueError("%s: expected %d contiguous entries" % (name, n))
+        return p
+
+    def _rows(self, t, name: str, tokens: Optional[int], head_dim: Optional[int]):
+        """Heads [tokens, heads, head_dim], a token's heads side by side: (address, token stride)."""
+        p = self._tensor(t, name, (torch.bfloat16, torch.int16), 3)
+        if (tokens is not None and t.shape[0] != tokens) or (head_dim is not None and t.shape[2] != head_dim):
+            raise ValueError("%s: unexpected shape %s" % (name, tuple(t.shape)))
+        if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise ValueError("%s: the heads of a token must be contiguous" % name)
+        # a single row has no stride of its own
+        return p, (int(t.stride(0)) if t.shape[0] > 1 else (t.shape[1] * t.shape[2] + 7) // 8 * 8)
+
+    def _heads(self, src, dst, weight, name: str, tokens: int, head_dim: int):
+        h = nwc_heads()
+        h.src, h.ld_src = self._rows(src, name, tokens, head_dim)
+        h.heads = int(src.shape[1])
+        if dst is not None:
+            if tuple(dst.shape) != tuple(src.shape):
+                raise ValueError("%s_out: expected the shape of %s" % (name, name))
+            h.dst, h.ld_dst = self._rows(dst, name + "_out", tokens, head_dim)
+        if weight is not None:
+            h.weight = self._vector(weight, name + "_weight", head_dim, torch.bfloat16)
+        return h
+
+    def _rope(self, freqs, style):
+        if style not in _ROPE_STYLES:
+            raise ValueError("style must be 'half' or 'pairs'")
+        r = nwc_rope()
+        if freqs is not None:
+            r.freqs = self._vector(freqs, "freqs", int(freqs.numel()), torch.float32)
+            r.dims = 2 * int(freqs.numel())
+        r.style = _ROPE_STYLES[style]
+        return r
+
+    def _table(self, table):
+        t = nwc_page_table()
+        t.ids = self._tensor(table, "table", (torch.int32,), 2)
+        if table.shape[1] > 1 and table.stride(1) != 1:
+            raise ValueError("table: rows must be contiguous")
+        t.rows, t.cols = int(table.shape[0]), int(table.shape[1])
+        t.ld = int(table.stride(0)) if t.rows > 1 else t.cols
+        return t
+
+    def _cache(self, cache: "PagedCache"):
+        for t, name in ((cache.k_pages, "k_pages"), (cache.v_pages, "v_pages")):
+            self._tensor(t, name, (torch.bfloat16, torch.int16), 4)
+        return cache.struct
+
+    def _run(self, fn, where: str, stream):
+        if self.device.index == torch.cuda.current_device():
+            _check(fn(*self.args, _stream(stream)), where)
+        else:   # streams and launches belong to the tensors' device
+            with torch.cuda.device(self.device):
+                _check(fn(*self.args, _stream(stream)), where)
+
+
+class PagedCache:
+    """Key and value pages of one layer: two device tensors [n_pages, kv_heads,
+    page_len, head_dim] of BF16; pages may be any distance apart, the same in
+    both (views of one allocation for all layers, for example)."""
+
+    def __init__(self, k_pages, v_pages):
+        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            if t.dim() != 4 or tuple(t.shape) != tuple(k_pages.shape):
+                raise ValueError("%s: expected [n_pages, kv_heads, page_len, head_dim], the same for keys and values" % name)
+            _, h, n, d = t.shape
+            if (t.stride(3), t.stride(2), t.stride(1)) != (1, d, n * d):
+                raise ValueError("%s: the slots of a page must be contiguous" % name)
+            if t.shape[0] > 1 and t.stride(0) != k_pages.stride(0):
+                raise ValueError("key and value pages must be the same distance apart")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        n_pages, heads, page_len, d = (int(x) for x in k_pages.shape)
+        stride = int(k_pages.stride(0)) if n_pages > 1 else heads * page_len * d
+        self.struct = nwc_cache(k_pages.data_ptr(), v_pages.data_ptr(), n_pages, stride, heads, d, page_len, 0)
+
+
+class QkNormRope(_Call):
+    """Arguments of nwc_qk_norm_rope: q [tokens, q_heads, head_dim] and / or k
+    [tokens, kv_heads, head_dim] (views into a joint projection output are
+    fine), positions int32 [tokens] (negative: padding), weights BF16
+    [head_dim] or None (no norm), freqs float32 [dims / 2] radians per position
+    or None (no rotation).  Outputs default to the inputs (in place)."""
+
+    def __init__(self, q, k, positions, q_out=None, k_out=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 freqs=None, style: str = "half"):
+        super().__init__()
+        if q is None and k is None:
+            raise ValueError("need queries or keys")
+        some = q if q is not None else k
+        tokens, d = int(some.shape[0]), int(some.shape[-1])
+        self.q = None if q is None else self._heads(q, q if q_out is None else q_out, q_weight, "q", tokens, d)
+        self.k = None if k is None else self._heads(k, k if k_out is None else k_out, k_weight, "k", tokens, d)
+        self.rope = self._rope(freqs, style)
+        pos = self._vector(positions, "positions", tokens, torch.int32)
+        self.args = (None if q is None else ctypes.byref(self.q), None if k is None else ctypes.byref(self.k), tokens, d,
+                     float(eps), ctypes.byref(self.rope), _vp(pos))
+
+
+def nwc_qk_norm_rope(call: QkNormRope, stream=None):
+    """Norm and rotation of query and key heads in one pass (see QkNormRope)."""
+    call._run(_lib.nwc_qk_norm_rope, "nwc_qk_norm_rope", stream)
+
+
+class KvAppend(_Call):
+    """Arguments of nwc_kv_append: keys (normed and turned on the way) and values
+    [tokens, kv_heads, head_dim] of the tokens to positions int32 [tokens] of
+    page table rows `rows` (int32 [tokens]; None: token t is row t); queries q,
+    if given, are normed and turned in the same launch, in place or to q_out."""
+
+    def __init__(self, cache: PagedCache, table, k, v, positions, rows=None, k_weight=None, q=None, q_out=None, q_weight=None,
+                 eps: float = 1e-6, freqs=None, style: str = "half"):
+        super().__init__()
+        c, t = self._cache(cache), self._table(table)
+        tokens, d = int(k.shape[0]), int(c.head_dim)
+        self.k = self._heads(k, None, k_weight, "k", tokens, d)
+        if tuple(v.shape) != tuple(k.shape):
+            raise ValueError("v: expected the shape of k")
+        vp, ld_v = self._rows(v, "v", tokens, d)
+        self.q = None if q is None else self._heads(q, q if q_out is None else q_out, q_weight, "q", tokens, d)
+        self.rope = self._rope(freqs, style)
+        pos = self._vector(positions, "positions", tokens, torch.int32)
+        row = None if rows is None else self._vector(rows, "rows", tokens, torch.int32)
+        self.table = t
+        self.args = (ctypes.byref(c), ctypes.byref(t), ctypes.byref(self.k), _vp(vp), ld_v,
+                     None if q is None else ctypes.byref(self.q), tokens, float(eps), ctypes.byref(self.rope), _vp(pos),
+                     _vp(row))
+
+
+def nwc_kv_append(call: KvAppend, stream=None):
+    """Keys and values into the paged cache (see KvAppend)."""
+    call._run(_lib.nwc_kv_append, "nwc_kv_append", stream)
+
+
+def nwc_attend_workspace_size(cache: PagedCache, rows: int, q_heads: int, n_groups: int = 0) -> int:
+    out = _sz(0)
+    _check(_lib.nwc_attend_workspace_size(ctypes.byref(cache.struct), rows, q_heads, n_groups, ctypes.byref(out)),
+           "nwc_attend_workspace_size")
+    return out.value
+
+
+class Attend(_Call):
+    """Arguments of nwc_attend: one query token per page table row, q and out
+    [rows, q_heads, head_dim], lengths int32 [rows] (0: zeros, negative: row
+    left as it was), ws a device byte tensor of nwc_attend_workspace_size
+    bytes.  group_start int32 [n + 1] and shared_len int32 [n]: rows
+    group_start[i] .. group_start[i + 1] - 1 share their first shared_len[i]
+    positions, which are then read once.  scale defaults to head_dim ** -0.5."""
+
+    def __init__(self, cache: PagedCache, table, lengths, q, out, ws, scale: Optional[float] = None, group_start=None,
+                 shared_len=None):
+        super().__init__()
+        c, t = self._cache(cache), self._table(table)
+        rows, d = int(t.rows), int(c.head_dim)
+        qp, ldq = self._rows(q, "q", rows, d)
+        if tuple(out.shape) != tuple(q.shape):
+            raise ValueError("out: expected the shape of q")
+        op, ldo = self._rows(out, "out", rows, d)
+        lp = self._vector(lengths, "lengths", rows, torch.int32)
+        self.groups = nwc_groups()
+        if (group_start is None) != (shared_len is None):
+            raise ValueError("group_start and shared_len come together")
+        if group_start is not None:
+            n = int(shared_len.numel())
+            self.groups.count = n
+            if n:
+                self.groups.start = self._vector(group_start, "group_start", n + 1, torch.int32)
+                self.groups.len = self._vector(shared_len, "shared_len", n, torch.int32)
+        wp = self._tensor(ws, "ws", (torch.uint8,))
+        if not ws.is_contiguous():
+            raise ValueError("ws: expected a contiguous tensor")
+        self.table = t
+        self.args = (ctypes.byref(c), ctypes.byref(t), ctypes.byref(self.groups), _vp(lp), _vp(qp), ldq, int(q.shape[1]),
+                     float(d ** -0.5 if scale is None else scale), _vp(op), ldo, _vp(wp), int(ws.numel()))
+
+
+def nwc_attend(call: Attend, stream=None):
+    """Attention of one query token per row over the paged cache (see Attend)."""
+    call._run(_lib.nwc_attend, "nwc_attend", stream)
 
 
 def info_dict(info: nwc_info) -> dict:

@@ -43,7 +43,7 @@ def _run(cmd):
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     objs = []
-    for src in ("host_codec.cpp", "kernels.hip", "prefill.cpp"):
+    for src in ("host_codec.cpp", "kernels.hip", "attention.hip", "prefill.cpp"):
         obj = os.path.join(BUILD, src + ".o")
         host = ["-x", "c++", "-I/opt/rocm/include", "-D__HIP_PLATFORM_AMD__"]  # host code (HIP runtime API only)
         cmd = [HIPCC] + COMMON + (DEVICE if src.endswith(".hip") else host) + \

@@ -1,0 +1,981 @@
+// HIP kernels of libnwc's attention side for gfx950 (CDNA4) and the C-ABI entry
+// points that launch them: norm and rotation of query and key heads, the append
+// to a paged key-value cache, attention over that cache with shared prefixes
+// read once.
+//
+//  * k_heads: one wavefront per token and group of heads; a head is head_dim / 8
+//    lanes of 8 components.  The norm's sum runs over those lanes, the rotation
+//    takes its partner from another lane (halves) or the same one (pairs), and
+//    the result goes to a row or to a slot of a page.  Bound by HBM for long
+//    inputs, by one chain of dependent loads for a single token.
+//  * k_attend: attention of all rows in one grid; see there.
+//  * k_attend_join: adds the partial results of rows whose positions several
+//    workgroups had.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <tuple>
+
+#include "nwc.h"
+
+namespace {
+
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
+
+constexpr int kWave = 64;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Two floats rounded to BF16 (nearest even), packed.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const f32x2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __builtin_bit_cast(float, v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __builtin_bit_cast(float, v & 0xFFFF0000u); }
+
+__device__ __forceinline__ float lane_xor(float v, int mask) {
+  return __builtin_bit_cast(float, __shfl_xor(__builtin_bit_cast(int, v), mask, kWave));
+}
+
+// ---------------------------------------------------------------- k_heads ---
+
+struct PageArgs {
+  const int32_t* ids;
+  uint64_t ld, n_pages, page_stride;
+  uint32_t rows, cols, shift;  // page_len = 1 << shift
+};
+
+struct HeadsArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t *q_out, *k_out, *v_out;  // k_out, v_out: rows, or with pages.ids the cache
+  const uint16_t *q_weight, *k_weight;
+  const float* freqs;
+  const int32_t *positions, *rows;
+  uint64_t ld_q, ld_k, ld_v, ld_q_out, ld_k_out;
+  PageArgs pages;
+  uint32_t hq, hk, hv;
+  uint32_t tokens, d, half;  // half: dims / 2 (0: no rotation)
+  uint32_t style;
+  float eps, inv_d;
+};
+
+// A wavefront takes U passes over one token's heads (queries, then keys, then
+// values), 64 / G heads a pass: lane c of a head's G lanes holds components
+// 8 c .. 8 c + 7 (idle if 8 c >= head_dim).  The angles of a token serve all
+// its passes: lane c turns the same components of every head.
+template <int G, int U>
+__global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
+  constexpr uint32_t kHeads = kWave / G;  // heads of a pass
+  const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave);
+  const uint32_t all = a.hq + a.hk + a.hv;
+  const uint32_t per_token = (all + kHeads * U - 1) / (kHeads * U);
+  const uint64_t n = static_cast<uint64_t>(a.tokens) * per_token;
+  const uint32_t c = lane % G, sub = lane / G;
+  const bool on = 8 * c < a.d;
+  // the rotation's components of this lane: angles 8 c' .. (halves: c' = c or c
+  // less the lanes of the first half) or 4 c .. (pairs, each twice)
+  const uint32_t hl = a.half / 8;  // lanes of a half
+  const bool turned = on && 8 * c < 2 * a.half;
+  const bool pairs = a.style == NWC_ROPE_PAIRS;
+  for (uint64_t w = static_cast<uint64_t>(blockIdx.x) * 4 + wave; w < n; w += static_cast<uint64_t>(gridDim.x) * 4) {
+    const uint32_t t = static_cast<uint32_t>(w / per_token), part = static_cast<uint32_t>(w % per_token);
+    const int32_t pos = a.positions[t];
+    if (pos < 0) continue;  // a padding token
+    u32x4_t raw[U], wt[U];
+    uint32_t head[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      head[u] = (part * U + u) * kHeads + sub;
+      const bool live = on && head[u] < all;
+      const bool is_q = head[u] < a.hq, is_k = !is_q && head[u] < a.hq + a.hk;
+      const uint16_t* src = is_q ? a.q + t * a.ld_q + static_cast<uint64_t>(head[u]) * a.d
+                            : is_k ? a.k + t * a.ld_k + static_cast<uint64_t>(head[u] - a.hq) * a.d
+                                   : a.v + t * a.ld_v + static_cast<uint64_t>(head[u] - a.hq - a.hk) * a.d;
+      const uint16_t* wsrc = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
+      raw[u] = u32x4_t{0, 0, 0, 0};
+      wt[u] = raw[u];
+      if (live) raw[u] = *reinterpret_cast<const u32x4_t*>(src + 8 * c);
+      if (live && wsrc) wt[u] = *reinterpret_cast<const u32x4_t*>(wsrc + 8 * c);
+    }
+    // angles in turns, reduced in FP64: position (31 bits) times frequency (24
+    // bits) is exact to 2^-53 of its size, so after the whole turns are gone at
+    // most 2^31 / (2 pi) 2^-52, 8e-8 turns, is lost
+    float cs[8], sn[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      cs[j] = 1.f;
+      sn[j] = 0.f;
+    }
+    if (turned) {
+      const uint32_t first = pairs ? 4 * c : 8 * (c < hl ? c : c - hl);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double turns = static_cast<double>(pos) * (static_cast<double>(a.freqs[first + (pairs ? j / 2 : j)]) *
+                                                         0.15915494309189533577);
+        const float r = static_cast<float>(turns - __builtin_rint(turns));
+        cs[j] = __builtin_amdgcn_cosf(r);  // the hardware's sine and cosine take turns
+        const float s = __builtin_amdgcn_sinf(r);
+        sn[j] = (pairs ? j % 2 == 0 : c < hl) ? -s : s;
+      }
+    }
+    uint64_t slot = 0;  // element offset of the token's slot, less the head's part
+    bool stored = true;
+    if (a.pages.ids) {
+      const uint32_t row = a.rows ? static_cast<uint32_t>(a.rows[t]) : t;
+      const uint32_t at = static_cast<uint32_t>(pos) >> a.pages.shift;
+      stored = row < a.pages.rows && at < a.pages.cols;
+      const int32_t id = stored ? a.pages.ids[row * a.pages.ld + at] : -1;
+      stored = static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages;
+      if (stored)
+        slot = id * a.pages.page_stride +
+               static_cast<uint64_t>(static_cast<uint32_t>(pos) & ((1u << a.pages.shift) - 1)) * a.d;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool is_q = head[u] < a.hq, is_k = !is_q && head[u] < a.hq + a.hk;
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[2 * j] = bf16_lo(raw[u][j]);
+        y[2 * j + 1] = bf16_hi(raw[u][j]);
+      }
+      if (is_q ? a.q_weight != nullptr : is_k && a.k_weight != nullptr) {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
+#pragma unroll
+        for (int m = 1; m < G; m *= 2) sum += lane_xor(sum, m);
+        const float r = 1.f / sqrtf(fmaf(sum, a.inv_d, a.eps));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y[2 * j] *= r * bf16_lo(wt[u][j]);
+          y[2 * j + 1] *= r * bf16_hi(wt[u][j]);
+        }
+      }
+      float z[8];
+      if (a.half) {  // the partner of every component (uniform branch: all lanes take part)
+        const int from = static_cast<int>(!turned || pairs ? lane : c < hl ? lane + hl : lane - hl);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float other = pairs ? y[j ^ 1]
+                                    : __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(
+                                                                    4 * from, __builtin_bit_cast(int, y[j])));
+          z[j] = turned ? fmaf(y[j], cs[j], other * sn[j]) : y[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = y[j];
+      }
+      u32x4_t res;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) res[j] = pack_bf16(z[2 * j], z[2 * j + 1]);
+      if (!is_q && !is_k) res = raw[u];  // values as they are
+      if (!on || head[u] >= all) continue;
+      if (is_q) {
+        *reinterpret_cast<u32x4_t*>(a.q_out + t * a.ld_q_out + static_cast<uint64_t>(head[u]) * a.d + 8 * c) = res;
+      } else {
+        const uint32_t h = is_k ? head[u] - a.hq : head[u] - a.hq - a.hk;
+        uint16_t* dst = is_k ? a.k_out : a.v_out;
+        dst += a.pages.ids ? slot + (static_cast<uint64_t>(h) << a.pages.shift) * a.d
+                           : t * a.ld_k_out + static_cast<uint64_t>(h) * a.d;
+        if (stored) *reinterpret_cast<u32x4_t*>(dst + 8 * c) = res;
+      }
+    }
+  }
+}
+
+// --------------------------------------------------------------- k_attend ---
+//
+// Work: an item is one key-value head's part of either a group's shared prefix
+// (columns: the group's rows times the query heads of that key-value head, in
+// blocks of at most kCap) or one row's own positions (columns: its query heads).
+// An item's positions count in units of 32; all units of all items in order,
+// heads outermost, are cut into equal ranges, one per workgroup, so the split
+// needs only the lengths, which every workgroup reads for itself.  An item cut
+// between workgroups, or a row with both kinds, leaves partial sums in the
+// workspace, which k_attend_join adds in the order of the positions.
+//
+// A unit is taken by one wavefront, all in registers.  S^T = K Q^T on the
+// matrix cores, the keys straight from the page (lane: one position, 8
+// components); with the positions of the two 16-row tiles interleaved (tile t,
+// row m is position 8 (m / 4) + 4 t + m % 4) the result leaves each lane the 8
+// neighbouring positions 8 g .. 8 g + 7 of one column, g = lane / 16, which is
+// just the operand that O^T = V^T P^T takes.  The values come straight from the
+// page too: a lane reads D / 16 neighbouring components of its 8 positions and
+// turns that block by one byte permute per operand register.  No value crosses
+// lanes in the loop but the column's maximum, and that only when it grows.
+
+template <int D>
+struct AttendShape {
+  static constexpr int kNtMax = D <= 128 ? 4 : 2;  // 16-column tiles of a block
+  static constexpr int kCap = 16 * kNtMax;
+  static constexpr int kDt = D / 16;                // 16-row tiles of O^T = components of a lane
+  static constexpr int kKs = D / 32;                // steps of the K Q^T product
+  static constexpr int kQLd = D + 8, kJLd = D + 4;  // padded LDS rows (banks)
+};
+
+struct AttendArgs {
+  const uint16_t *k, *v, *q;
+  uint16_t* out;
+  const int32_t *lengths, *group_start, *group_len;
+  uint64_t ldq, ldo;
+  PageArgs pages;
+  uint32_t hq, hkv, ratio, n_groups;
+  float scale2;  // scale * log2(e)
+  float* part_o;  // workspace: partial sums [column slot][D]
+  float* part_ml; // their maxima (log2 domain) and weight sums
+  uint32_t* plan; // the plan for k_attend_join
+  uint32_t min_quota;
+};
+
+constexpr int kAttendThreads = 256;
+constexpr float kNoMax = -1e30f;  // the maximum of nothing: finite, so that exp2(-inf - it) is 0
+
+// Plan in LDS and (for the join) in the workspace: u32 words
+//   [0] units per head, [1], [3] units per workgroup (low, high word), [2] units of prefixes per head
+//   row_pre[rows + 1]   units of own positions before the row
+//   row_base[rows]      first own position (the shared length where the row shares)
+//   row_end[rows]       its length, cut to what the table covers; -1 for padding
+//   row_group[rows]     its group, or count
+//   g_start[groups + 1], g_pre[groups + 1], g_units[groups], g_row[groups]
+struct Plan {
+  uint32_t *head, *row_pre, *row_base, *row_end, *row_group, *g_start, *g_pre, *g_units, *g_row;
+  __host__ __device__ static uint32_t words(uint32_t rows, uint32_t groups) { return 4 + 4 * rows + 1 + 4 * groups + 2; }
+  __device__ uint64_t quota() const { return head[1] | static_cast<uint64_t>(head[3]) << 32; }
+  __device__ Plan(uint32_t* p, uint32_t rows, uint32_t groups) {
+    head = p;
+    row_pre = head + 4;
+    row_base = row_pre + rows + 1;
+    row_end = row_base + rows;
+    row_group = row_end + rows;
+    g_start = row_group + rows;
+    g_pre = g_start + groups + 1;
+    g_units = g_pre + groups + 1;
+    g_row = g_units + groups;
+  }
+};
+
+// In-place inclusive scan (sum or maximum) of n words in LDS by the workgroup;
+// carry: 8 words of LDS.
+template <bool MAX>
+__device__ void block_scan(uint32_t* v, uint32_t n, uint32_t* carry) {
+  const uint32_t lane = __lane_id(), wave = threadIdx.x / kWave;
+  uint32_t before = 0;
+  for (uint32_t base = 0; base < n; base += kAttendThreads) {
+    const uint32_t i = base + threadIdx.x;
+    uint32_t x = i < n ? v[i] : 0;
+#pragma unroll
+    for (int s = 1; s < kWave; s *= 2) {
+      const uint32_t y = __shfl_up(x, s, kWave);
+      if (lane >= static_cast<uint32_t>(s)) x = MAX ? max(x, y) : x + y;
+    }
+    if (lane == kWave - 1) carry[wave] = x;
+    __syncthreads();
+    for (uint32_t w = 0; w < 4; ++w) {
+      const uint32_t y = carry[w];
+      if (w < wave) x = MAX ? max(x, y) : x + y;
+    }
+    x = MAX ? max(x, before) : x + before;
+    if (i < n) v[i] = x;
+    for (uint32_t w = 0; w < 4; ++w) before = MAX ? max(before, carry[w]) : before + carry[w];
+    __syncthreads();
+  }
+}
+
+// Lengths and groups (whatever they hold) into a plan whose ranges are all in
+// bounds: starts made ascending within 0..rows, lengths within 0..capacity.
+__device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t cap, uint32_t* carry) {
+  const uint32_t rows = a.pages.rows, G = a.n_groups, tid = threadIdx.x;
+  const int32_t most = static_cast<int32_t>(a.pages.cols << a.pages.shift);
+  for (uint32_t i = tid; i < G; i += kAttendThreads) {
+    p.g_start[i] = static_cast<uint32_t>(min(max(a.group_start[i], 0), static_cast<int32_t>(rows)));
+    p.g_units[i] = static_cast<uint32_t>(min(max(a.group_len[i], 0), most));  // positions, for now
+    p.g_row[i] = rows;
+  }
+  if (tid == 0) p.g_start[G] = G ? static_cast<uint32_t>(min(max(a.group_start[G], 0), static_cast<int32_t>(rows))) : 0;
+  __syncthreads();
+  if (G) block_scan<true>(p.g_start, G + 1, carry);
+  for (uint32_t r = tid; r < rows; r += kAttendThreads) {
+    const int32_t len = a.lengths[r];
+    const uint32_t end = static_cast<uint32_t>(min(len, most));
+    uint32_t g = 0, hi = G + 1;  // the last start <= r
+    while (G && g + 1 < hi) {
+      const uint32_t mid = (g + hi) / 2;
+      if (p.g_start[mid] <= r) g = mid; else hi = mid;
+    }
+    const bool in = G && g < G && p.g_start[g] <= r;
+    const uint32_t s = in ? p.g_units[g] : 0;
+    const bool shares = s > 0 && len > 0 && end >= s;
+    p.row_end[r] = len < 0 ? 0xFFFFFFFFu : end;
+    p.row_base[r] = shares ? s : 0;
+    p.row_group[r] = shares ? g : G;
+    if (shares) atomicMin(&p.g_row[g], r);
+  }
+  __syncthreads();
+  const uint32_t blocks = (a.ratio + cap - 1) / cap;  // column blocks of one row
+  for (uint32_t r = tid; r < rows; r += kAttendThreads) {
+    const int32_t end = static_cast<int32_t>(p.row_end[r]);
+    const uint32_t base = p.row_base[r];
+    const uint32_t units = end > static_cast<int32_t>(base) ? (end + 31u) / 32 - base / 32 : 0;
+    p.row_pre[r + 1] = units * blocks;
+  }
+  for (uint32_t i = tid; i < G; i += kAttendThreads) {
+    const uint32_t cols = (p.g_start[i + 1] - p.g_start[i]) * a.ratio;
+    const uint32_t units = p.g_row[i] < rows ? (p.g_units[i] + 31) / 32 : 0;
+    p.g_pre[i + 1] = units * ((cols + cap - 1) / cap);
+    // the units of one column block; the length stays the row_base of the rows
+    p.g_units[i] = units;
+  }
+  if (tid == 0) p.row_pre[0] = p.g_pre[0] = 0;
+  __syncthreads();
+  block_scan<false>(p.row_pre + 1, rows, carry);
+  if (G) block_scan<false>(p.g_pre + 1, G, carry);
+  if (tid == 0) {
+    const uint32_t units = p.g_pre[G] + p.row_pre[rows];
+    const uint64_t total = static_cast<uint64_t>(units) * a.hkv;
+    const uint64_t quota = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint64_t>(a.min_quota));
+    p.head[0] = units;
+    p.head[1] = static_cast<uint32_t>(quota);
+    p.head[2] = p.g_pre[G];
+    p.head[3] = static_cast<uint32_t>(quota >> 32);
+  }
+  __syncthreads();
+}
+
+// One workgroup's part of one item.
+struct Segment {
+  const int32_t* ids;  // the page table row
+  uint32_t head;       // key-value head
+  uint32_t row0;       // first row of the item's columns
+  uint32_t col0, cols; // columns: (row - row0) * ratio + query head of the key-value head
+  uint32_t u0, u1;     // units (position / 32)
+  uint32_t p0, p1;     // positions that the item sees
+};
+
+template <int D>
+struct Lds {
+  uint16_t q[AttendShape<D>::kCap][AttendShape<D>::kQLd];
+  float join[4][16][AttendShape<D>::kJLd];
+  float m[4][AttendShape<D>::kCap], l[4][AttendShape<D>::kCap];
+  uint32_t carry[8];
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segment& it, Lds<D>& s, bool direct,
+                                               uint64_t slot) {
+  using S = AttendShape<D>;
+  constexpr int kDt = S::kDt, kKs = S::kKs;
+  const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave), tid = threadIdx.x;
+  const uint32_t n = lane % 16, g = lane / 16;
+  // queries to LDS, columns past the last as zeros
+  for (uint32_t i = tid; i < 16 * NT * (D / 8); i += kAttendThreads) {
+    const uint32_t c = i / (D / 8), e = i % (D / 8) * 8;
+    u32x4_t x = {0, 0, 0, 0};
+    if (c < it.cols) {
+      const uint32_t col = it.col0 + c, row = it.row0 + col / a.ratio, h = it.head * a.ratio + col % a.ratio;
+      x = *reinterpret_cast<const u32x4_t*>(a.q + row * a.ldq + static_cast<uint64_t>(h) * D + e);
+    }
+    *reinterpret_cast<u32x4_t*>(&s.q[c][e]) = x;
+  }
+  __syncthreads();
+
+  f32x4_t o[kDt][NT];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = kNoMax;
+    l[t] = 0.f;
+#pragma unroll
+    for (int d = 0; d < kDt; ++d) o[d][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const uint32_t mask = (1u << a.pages.shift) - 1;
+  const uint64_t head_off = (static_cast<uint64_t>(it.head) << a.pages.shift) * D;
+  // this lane's key positions (tile 0) and block of 8 value positions in a unit
+  const uint32_t kpos = 8 * (n / 4) + n % 4, vpos = 8 * g;
+  auto page_of = [&](uint32_t pos) -> int32_t {
+    const uint32_t at = pos >> a.pages.shift;
+    return at < a.pages.cols ? it.ids[at] : -1;
+  };
+  auto known = [&](int32_t id) { return static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages; };
+  auto offset = [&](int32_t id, uint32_t pos) {
+    return (known(id) ? static_cast<uint64_t>(id) : 0) * a.pages.page_stride + head_off +
+           static_cast<uint64_t>(pos & mask) * D;
+  };
+  u32x4_t kf[2][kKs];
+  uint32_t vr[8][kDt / 2];
+  auto load_k = [&](int32_t id, uint32_t u) {
+    const uint16_t* p = a.k + offset(id, 32 * u + kpos) + 8 * g;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int k = 0; k < kKs; ++k) kf[t][k] = *reinterpret_cast<const u32x4_t*>(p + 4 * t * D + 32 * k);
+  };
+  auto load_v = [&](int32_t id, uint32_t u) {
+    const uint16_t* p = a.v + offset(id, 32 * u + vpos) + kDt * n;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) __builtin_memcpy(vr[j], p + j * D, 2 * kDt);
+  };
+
+  uint32_t u = it.u0 + wave;
+  if (u < it.u1) {
+    int32_t kid = page_of(32 * u + kpos), vid = page_of(32 * u + vpos);
+    load_k(kid, u);
+    for (;;) {
+      load_v(vid, u);
+      const bool good = known(vid);
+      const uint32_t next = u + 4;
+      const bool more = next < it.u1;
+      if (more) {
+        kid = page_of(32 * next + kpos);
+        vid = page_of(32 * next + vpos);
+      }
+      f32x4_t sc[2][NT];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < NT; ++c) sc[t][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < kKs; ++k) {
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          const bf16x8_t qf = *reinterpret_cast<const bf16x8_t*>(&s.q[16 * c + n][32 * k + 8 * g]);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            sc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kf[t][k]), qf, sc[t][c], 0, 0, 0);
+        }
+      }
+      if (more) load_k(kid, next);
+      const uint32_t first = 32 * u;
+      if (first < it.p0 || first + 32 > it.p1 || !__all(good)) {  // an edge of the item, or a page that is none
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t pos = first + vpos + j;
+          const bool seen = good && pos >= it.p0 && pos < it.p1;
+#pragma unroll
+          for (int c = 0; c < NT; ++c)
+            if (!seen) sc[j / 4][c][j % 4] = -INFINITY;
+          // a slot that is not seen may hold anything, and 0 times NaN is NaN
+#pragma unroll
+          for (int d = 0; d < kDt / 2; ++d)
+            if (!seen) vr[j][d] = 0;
+        }
+      }
+      float mx[NT];
+      bool grow = false;
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        float x = fmaxf(fmaxf(sc[0][c][0], sc[0][c][1]), fmaxf(sc[0][c][2], sc[0][c][3]));
+        x = fmaxf(x, fmaxf(fmaxf(sc[1][c][0], sc[1][c][1]), fmaxf(sc[1][c][2], sc[1][c][3])));
+        mx[c] = x * a.scale2;
+        grow |= mx[c] > m[c] + 8.f;  // weights up to 2^8 lose nothing: BF16 and FP32 keep their relative precision
+      }
+      if (__any(grow)) {
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          float x = mx[c];
+          x = fmaxf(x, lane_xor(x, 16));
+          x = fmaxf(x, lane_xor(x, 32));
+          x = fmaxf(x, m[c]);
+          const float f = __builtin_amdgcn_exp2f(m[c] - x);
+          m[c] = x;
+          l[c] *= f;
+#pragma unroll
+          for (int d = 0; d < kDt; ++d) o[d][c] *= f;
+        }
+      }
+      bf16x8_t pf[NT];
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        float p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          p[j] = __builtin_amdgcn_exp2f(fmaf(sc[j / 4][c][j % 4], a.scale2, -m[c]));
+          l[c] += p[j];
+        }
+        u32x4_t w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
+        pf[c] = __builtin_bit_cast(bf16x8_t, w);
+      }
+#pragma unroll
+      for (int d = 0; d < kDt; ++d) {
+        u32x4_t w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = __builtin_amdgcn_perm(vr[2 * j + 1][d / 2], vr[2 * j][d / 2], d % 2 ? 0x07060302 : 0x05040100);
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+          o[d][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w), pf[c], o[d][c], 0, 0, 0);
+      }
+      if (!more) break;
+      u = next;
+    }
+  }
+
+  // the four wavefronts' sums, brought to one maximum and added in order
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    l[c] += lane_xor(l[c], 16);
+    l[c] += lane_xor(l[c], 32);
+    if (g == 0) {
+      s.m[wave][16 * c + n] = m[c];
+      s.l[wave][16 * c + n] = l[c];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    float top = s.m[0][16 * c + n];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, s.m[w][16 * c + n]);
+    const float f = __builtin_amdgcn_exp2f(m[c] - top);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float* dst = &s.join[wave][n][kDt * (4 * g + i)];  // O^T tile t, row 4 g + i: component kDt (4 g + i) + t
+#pragma unroll
+      for (int d = 0; d < kDt; ++d) dst[d] = o[d][c][i] * f;
+    }
+    __syncthreads();
+    for (uint32_t i = tid; i < 16 * (D / 4); i += kAttendThreads) {
+      const uint32_t col = i / (D / 4), e = i % (D / 4) * 4, cc = 16 * c + col;
+      if (cc < it.cols) {
+        f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+        float total = 0.f, best = s.m[0][cc];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) best = fmaxf(best, s.m[w][cc]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          sum += *reinterpret_cast<const f32x4_t*>(&s.join[w][col][e]);
+          total += s.l[w][cc] * __builtin_amdgcn_exp2f(s.m[w][cc] - best);
+        }
+        if (direct) {
+          const float r = total == 0.f ? 0.f : 1.f / total;
+          const uint32_t cl = it.col0 + cc, row = it.row0 + cl / a.ratio, h = it.head * a.ratio + cl % a.ratio;
+          uint2 w;
+          w.x = pack_bf16(sum[0] * r, sum[1] * r);
+          w.y = pack_bf16(sum[2] * r, sum[3] * r);
+          *reinterpret_cast<uint2*>(a.out + row * a.ldo + static_cast<uint64_t>(h) * D + e) = w;
+        } else {
+          *reinterpret_cast<f32x4_t*>(a.part_o + (slot + cc) * D + e) = sum;
+          if (e == 0) {
+            a.part_ml[2 * (slot + cc)] = best;
+            a.part_ml[2 * (slot + cc) + 1] = total;
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Column slot of a workgroup's partial sums: columns of all items before the
+// item, and a full block for each workgroup before this one.  Items and
+// workgroups that meet follow each other (either the item or the workgroup
+// steps on), so no two overlap.
+__device__ __forceinline__ uint64_t part_slot(const AttendArgs& a, uint32_t head, bool prefix, uint32_t row, uint32_t col0,
+                                              uint64_t wg, uint32_t cap) {
+  const uint64_t cols = static_cast<uint64_t>(a.pages.rows) * a.ratio;
+  return (2 * head + (prefix ? 0 : 1)) * cols + static_cast<uint64_t>(row) * a.ratio + col0 + wg * cap;
+}
+
+// Largest i in [0, n) with pre[i] <= x (pre ascending, pre[0] = 0).
+__device__ __forceinline__ uint32_t find_last(const uint32_t* pre, uint32_t n, uint32_t x) {
+  uint32_t lo = 0, hi = n;
+  while (lo + 1 < hi) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (pre[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+template <int D>
+__global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(const AttendArgs a) {
+  using S = AttendShape<D>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  Lds<D>& s = *reinterpret_cast<Lds<D>*>(lds);
+  const uint32_t rows = a.pages.rows, G = a.n_groups;
+  const Plan p(reinterpret_cast<uint32_t*>(lds + sizeof(Lds<D>)), rows, G);
+  make_plan(a, p, S::kCap, s.carry);
+  if (blockIdx.x == 0)
+    for (uint32_t i = threadIdx.x; i < Plan::words(rows, G); i += kAttendThreads) a.plan[i] = p.head[i];
+  const uint32_t units = p.head[0], prefix_units = p.head[2];
+  const uint64_t quota = p.quota();
+  // workgroups go round the 8 XCDs in turn: neighbours in the order of the
+  // units, which share a head's pages, on one XCD
+  const uint32_t per_xcd = gridDim.x / 8;
+  const uint64_t wg = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * per_xcd + blockIdx.x / 8;
+  uint64_t at = wg * quota;
+  const uint64_t total = static_cast<uint64_t>(units) * a.hkv, end = min(at + quota, total);
+  while (at < end) {
+    Segment it;
+    it.head = static_cast<uint32_t>(at / units);
+    const uint32_t rem = static_cast<uint32_t>(at % units);
+    const bool prefix = rem < prefix_units;
+    uint32_t done, n_units, first;  // units of the item before this range, all its units, its first unit's position / 32
+    uint32_t item_row;
+    if (prefix) {
+      const uint32_t i = find_last(p.g_pre, G, rem);
+      n_units = p.g_units[i];
+      const uint32_t in = rem - p.g_pre[i], block = in / n_units;
+      done = in - block * n_units;
+      first = 0;
+      item_row = p.g_start[i];
+      it.col0 = block * S::kCap;
+      it.cols = (p.g_start[i + 1] - item_row) * a.ratio - it.col0;
+      it.ids = a.pages.ids + p.g_row[i] * a.pages.ld;
+      it.p0 = 0;
+      it.p1 = p.row_base[p.g_row[i]];
+    } else {
+      const uint32_t own = rem - prefix_units, r = find_last(p.row_pre, rows, own);
+      const uint32_t base = p.row_base[r], stop = p.row_end[r];
+      first = base / 32;
+      n_units = (stop + 31) / 32 - first;
+      const uint32_t in = own - p.row_pre[r], block = in / n_units;
+      done = in - block * n_units;
+      item_row = r;
+      it.col0 = block * S::kCap;
+      it.cols = a.ratio - it.col0;
+      it.ids = a.pages.ids + r * a.pages.ld;
+      it.p0 = base;
+      it.p1 = stop;
+    }
+    it.row0 = item_row;
+    it.cols = min(it.cols, static_cast<uint32_t>(S::kCap));
+    const uint32_t take = static_cast<uint32_t>(min(static_cast<uint64_t>(n_units - done), end - at));
+    it.u0 = first + done;
+    it.u1 = it.u0 + take;
+    const bool direct = !prefix && it.p0 == 0 && take == n_units;
+    const uint64_t slot = part_slot(a, it.head, prefix, item_row, it.col0, wg, S::kCap);
+    if (it.cols <= 16)
+      attend_segment<D, 1>(a, it, s, direct, slot);
+    else if (S::kNtMax == 2 || it.cols <= 32)
+      attend_segment<D, 2>(a, it, s, direct, slot);
+    else
+      attend_segment<D, S::kNtMax>(a, it, s, direct, slot);
+    at += take;
+  }
+}
+
+// One workgroup per row and key-value head: the partial sums of its columns,
+// prefix first, in the order of the positions.
+template <int D>
+__global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs a) {
+  constexpr uint32_t kCap = AttendShape<D>::kCap;
+  const uint32_t rows = a.pages.rows, r = blockIdx.x / a.hkv, head = blockIdx.x % a.hkv;
+  const Plan p(a.plan, rows, a.n_groups);
+  const uint32_t units = p.head[0], prefix_units = p.head[2];
+  const uint64_t quota = p.quota();
+  const uint32_t base = p.row_base[r], g = p.row_group[r];
+  const int32_t stop = static_cast<int32_t>(p.row_end[r]);
+  if (stop < 0) return;  // padding
+  const uint32_t own_units = stop > static_cast<int32_t>(base) ? (stop + 31u) / 32 - base / 32 : 0;
+  for (uint32_t i = threadIdx.x; i < a.ratio * (D / 4); i += kAttendThreads) {
+    const uint32_t j = i / (D / 4), e = i % (D / 4) * 4;
+    uint64_t w0[2] = {1, 1}, w1[2] = {0, 0}, slot[2] = {0, 0};  // workgroups of the prefix and of the own positions
+    if (base) {
+      const uint32_t col = (r - p.g_start[g]) * a.ratio + j, block = col / kCap, n = p.g_units[g];
+      const uint64_t first = static_cast<uint64_t>(units) * head + p.g_pre[g] + static_cast<uint64_t>(block) * n;
+      w0[0] = first / quota;
+      w1[0] = (first + n - 1) / quota;
+      slot[0] = part_slot(a, head, true, p.g_start[g], block * kCap, 0, kCap) + col % kCap;
+    }
+    if (own_units) {
+      const uint32_t block = j / kCap;
+      const uint64_t first = static_cast<uint64_t>(units) * head + prefix_units + p.row_pre[r] +
+                             static_cast<uint64_t>(block) * own_units;
+      w0[1] = first / quota;
+      w1[1] = (first + own_units - 1) / quota;
+      slot[1] = part_slot(a, head, false, r, block * kCap, 0, kCap) + j % kCap;
+      if (!base && w0[1] == w1[1]) continue;  // k_attend wrote the output itself
+    }
+    float best = kNoMax;
+    for (int k = 0; k < 2; ++k)
+      for (uint64_t w = w0[k]; w <= w1[k] && w0[k] <= w1[k]; ++w) best = fmaxf(best, a.part_ml[2 * (slot[k] + w * kCap)]);
+    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+    float total = 0.f;
+    for (int k = 0; k < 2; ++k)
+      for (uint64_t w = w0[k]; w <= w1[k] && w0[k] <= w1[k]; ++w) {
+        const uint64_t at = slot[k] + w * kCap;
+        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - best);
+        total += a.part_ml[2 * at + 1] * f;
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part_o + at * D + e);
+        sum += x * f;
+      }
+    const float f = total == 0.f ? 0.f : 1.f / total;
+    uint2 w;
+    w.x = pack_bf16(sum[0] * f, sum[1] * f);
+    w.y = pack_bf16(sum[2] * f, sum[3] * f);
+    *reinterpret_cast<uint2*>(a.out + r * a.ldo + static_cast<uint64_t>(head * a.ratio + j) * D + e) = w;
+  }
+}
+
+// ------------------------------------------------------------------- host ---
+
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Launch a kernel and report that launch's own status.
+template <typename... P, typename... A>
+nwc_status launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t s, const A&... a) {
+  static_assert(sizeof...(P) == sizeof...(A), "argument count");
+  std::tuple<P...> args{static_cast<P>(a)...};
+  void* argv[sizeof...(P)];
+  std::apply([&](auto&... e) {
+    int i = 0;
+    ((argv[i++] = const_cast<void*>(static_cast<const void*>(&e))), ...);
+  }, args);
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, argv, lds, s) == hipSuccess
+             ? NWC_OK
+             : NWC_ERR_HIP;
+}
+
+uint32_t cu_count() {
+  int dev = 0, n = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1)
+    return 0;
+  return static_cast<uint32_t>(n);
+}
+
+// Most heads of one tensor and elements of a page: products of sizes stay far
+// below 2^63 with strides below 2^40.
+constexpr uint32_t kMaxHeads = 65536;
+constexpr uint64_t kMaxStride = uint64_t{1} << 40;
+
+nwc_status check_rope(const nwc_rope* rope, uint32_t d) {
+  if (!rope || rope->dims == 0) return NWC_OK;
+  if (!rope->freqs || rope->dims > d || rope->style > NWC_ROPE_PAIRS) return NWC_ERR_INVALID_ARG;
+  if (rope->dims % 16) return NWC_ERR_UNSUPPORTED;
+  return aligned(rope->freqs, 4) ? NWC_OK : NWC_ERR_ALIGNMENT;
+}
+
+nwc_status check_heads(const nwc_heads* h, uint32_t d, bool to_rows) {
+  if (!h->src || h->heads == 0 || h->heads > kMaxHeads || h->reserved || (to_rows && !h->dst)) return NWC_ERR_INVALID_ARG;
+  const uint64_t row = static_cast<uint64_t>(h->heads) * d;
+  if (h->ld_src < row || h->ld_src > kMaxStride || (to_rows && (h->ld_dst < row || h->ld_dst > kMaxStride)))
+    return NWC_ERR_INVALID_ARG;
+  if (!aligned(h->src, 16) || !aligned(h->weight, 16) || h->ld_src % 8) return NWC_ERR_ALIGNMENT;
+  if (to_rows && (!aligned(h->dst, 16) || h->ld_dst % 8)) return NWC_ERR_ALIGNMENT;
+  if (to_rows && h->dst == h->src && h->ld_dst != h->ld_src) return NWC_ERR_INVALID_ARG;
+  return NWC_OK;
+}
+
+nwc_status check_cache(const nwc_cache* c, const nwc_page_table* t, PageArgs* p) {
+  if (!c || !c->k || !c->v || c->n_pages == 0 || c->n_pages > 0x7FFFFFFF || c->kv_heads == 0 || c->kv_heads > kMaxHeads ||
+      c->page_len == 0 || c->reserved)
+    return NWC_ERR_INVALID_ARG;
+  if (c->page_len < 16 || c->page_len > 1024 || (c->page_len & (c->page_len - 1))) return NWC_ERR_UNSUPPORTED;
+  if (c->page_stride < static_cast<uint64_t>(c->kv_heads) * c->page_len * c->head_dim || c->page_stride > kMaxStride)
+    return NWC_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % 8) return NWC_ERR_ALIGNMENT;
+  p->n_pages = c->n_pages;
+  p->page_stride = c->page_stride;
+  p->shift = static_cast<uint32_t>(__builtin_ctz(c->page_len));
+  if (t) {
+    if (!t->ids || t->rows == 0 || t->cols == 0 || t->ld < t->cols || t->ld > kMaxStride) return NWC_ERR_INVALID_ARG;
+    if (!aligned(t->ids, 4)) return NWC_ERR_ALIGNMENT;
+    p->ids = t->ids;
+    p->ld = t->ld;
+    p->rows = t->rows;
+    p->cols = t->cols;
+  }
+  return NWC_OK;
+}
+
+nwc_status launch_heads(HeadsArgs& a, hipStream_t s) {
+  const uint32_t all = a.hq + a.hk + a.hv, lanes = a.d / 8;
+  a.inv_d = 1.f / static_cast<float>(a.d);
+  const uint32_t cus = cu_count();
+  if (cus == 0) return NWC_ERR_HIP;
+  const uint32_t g = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
+  const uint32_t passes = (all + kWave / g - 1) / (kWave / g);
+  // one pass per wavefront while that leaves compute units idle, else four
+  const bool few = static_cast<uint64_t>(a.tokens) * passes < static_cast<uint64_t>(cus) * 16;
+  const uint64_t waves = static_cast<uint64_t>(a.tokens) * (few ? passes : (passes + 3) / 4);
+  const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>((waves + 3) / 4, uint64_t{1} << 24));
+  auto go = [&](auto one, auto four) { return launch(few ? one : four, dim3(grid), dim3(256), 0, s, a); };
+  if (g == 8) return go(k_heads<8, 1>, k_heads<8, 4>);
+  if (g == 16) return go(k_heads<16, 1>, k_heads<16, 4>);
+  return go(k_heads<32, 1>, k_heads<32, 4>);
+}
+
+bool heads_dim_ok(uint32_t d) { return d >= 8 && d <= 256 && d % 8 == 0; }
+
+void set_rope(HeadsArgs* a, const nwc_rope* rope) {
+  if (rope && rope->dims) {
+    a->freqs = rope->freqs;
+    a->half = rope->dims / 2;
+    a->style = rope->style;
+  }
+}
+
+// Workspace of nwc_attend: partial sums, maxima and sums, the plan.
+constexpr uint32_t kAttendMaxRows = 4096, kAttendMaxRatio = 64, kAttendMaxLen = 1u << 22;
+struct AttendLayout {
+  uint64_t ml, plan, bytes;
+};
+AttendLayout attend_layout(uint32_t rows, uint32_t q_heads, uint32_t groups, uint32_t d, uint32_t grid) {
+  const uint64_t cap = d <= 128 ? 64 : 32;
+  const uint64_t slots = 2 * static_cast<uint64_t>(rows) * q_heads + grid * cap;
+  auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
+  AttendLayout L;
+  L.ml = up(slots * d * 4);
+  L.plan = L.ml + up(slots * 8);
+  L.bytes = L.plan + up(static_cast<uint64_t>(Plan::words(rows, groups)) * 4);
+  return L;
+}
+
+nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uint32_t groups) {
+  if (!c || rows == 0 || q_heads == 0 || c->kv_heads == 0) return NWC_ERR_INVALID_ARG;
+  const uint32_t d = c->head_dim;
+  if (d != 64 && d != 96 && d != 128 && d != 192 && d != 256) return NWC_ERR_UNSUPPORTED;
+  if (q_heads % c->kv_heads) return NWC_ERR_INVALID_ARG;
+  if (rows > kAttendMaxRows || groups > kAttendMaxRows || q_heads / c->kv_heads > kAttendMaxRatio || q_heads > kMaxHeads)
+    return NWC_ERR_UNSUPPORTED;
+  return NWC_OK;
+}
+
+uint32_t attend_grid(uint32_t cus, uint32_t d) { return cus * (d <= 128 ? 2 : 1); }
+
+template <int D>
+nwc_status launch_attend(const AttendArgs& a, uint32_t grid, hipStream_t s) {
+  const size_t lds = sizeof(Lds<D>) + static_cast<size_t>(Plan::words(a.pages.rows, a.n_groups)) * 4;
+  if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<D>), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(lds)) != hipSuccess)
+    return NWC_ERR_HIP;
+  const nwc_status st = launch(k_attend<D>, dim3(grid), dim3(kAttendThreads), lds, s, a);
+  if (st) return st;
+  return launch(k_attend_join<D>, dim3(a.pages.rows * a.hkv), dim3(kAttendThreads), 0, s, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+nwc_status nwc_qk_norm_rope(const nwc_heads* q, const nwc_heads* k, uint32_t tokens, uint32_t head_dim, float eps,
+                            const nwc_rope* rope, const int32_t* positions_dev, void* stream) {
+  if ((!q && !k) || tokens == 0 || !positions_dev || !(eps >= 0.f) || !std::isfinite(eps) || head_dim == 0)
+    return NWC_ERR_INVALID_ARG;
+  if (!heads_dim_ok(head_dim)) return NWC_ERR_UNSUPPORTED;
+  if (!aligned(positions_dev, 4)) return NWC_ERR_ALIGNMENT;
+  nwc_status st = check_rope(rope, head_dim);
+  if (!st && q) st = check_heads(q, head_dim, true);
+  if (!st && k) st = check_heads(k, head_dim, true);
+  if (st) return st;
+  HeadsArgs a = {};
+  if (q) {
+    a.q = q->src; a.q_out = q->dst; a.q_weight = q->weight; a.ld_q = q->ld_src; a.ld_q_out = q->ld_dst; a.hq = q->heads;
+  }
+  if (k) {
+    a.k = k->src; a.k_out = k->dst; a.k_weight = k->weight; a.ld_k = k->ld_src; a.ld_k_out = k->ld_dst; a.hk = k->heads;
+  }
+  set_rope(&a, rope);
+  a.positions = positions_dev;
+  a.tokens = tokens;
+  a.d = head_dim;
+  a.eps = eps;
+  return launch_heads(a, static_cast<hipStream_t>(stream));
+}
+
+nwc_status nwc_kv_append(const nwc_cache* cache, const nwc_page_table* table, const nwc_heads* k, const uint16_t* v_dev,
+                         uint64_t ld_v, const nwc_heads* q, uint32_t tokens, float eps, const nwc_rope* rope,
+                         const int32_t* positions_dev, const int32_t* rows_dev, void* stream) {
+  if (!cache || !table || !k || !v_dev || tokens == 0 || !positions_dev || !(eps >= 0.f) || !std::isfinite(eps) ||
+      cache->head_dim == 0)
+    return NWC_ERR_INVALID_ARG;
+  const uint32_t d = cache->head_dim;
+  if (!heads_dim_ok(d)) return NWC_ERR_UNSUPPORTED;
+  HeadsArgs a = {};
+  nwc_status st = check_cache(cache, table, &a.pages);
+  if (!st) st = check_rope(rope, d);
+  if (!st) st = check_heads(k, d, false);
+  if (!st && q) st = check_heads(q, d, true);
+  if (st) return st;
+  if (k->heads != cache->kv_heads || ld_v < static_cast<uint64_t>(k->heads) * d || ld_v > kMaxStride) return NWC_ERR_INVALID_ARG;
+  if (!rows_dev && tokens > table->rows) return NWC_ERR_INVALID_ARG;  // token t is row t
+  if (!aligned(v_dev, 16) || ld_v % 8 || !aligned(positions_dev, 4) || !aligned(rows_dev, 4)) return NWC_ERR_ALIGNMENT;
+  if (q) {
+    a.q = q->src; a.q_out = q->dst; a.q_weight = q->weight; a.ld_q = q->ld_src; a.ld_q_out = q->ld_dst; a.hq = q->heads;
+  }
+  a.k = k->src; a.k_out = cache->k; a.k_weight = k->weight; a.ld_k = k->ld_src; a.hk = k->heads;
+  a.v = v_dev; a.v_out = cache->v; a.ld_v = ld_v; a.hv = k->heads;
+  set_rope(&a, rope);
+  a.positions = positions_dev;
+  a.rows = rows_dev;
+  a.tokens = tokens;
+  a.d = d;
+  a.eps = eps;
+  return launch_heads(a, static_cast<hipStream_t>(stream));
+}
+
+nwc_status nwc_attend_workspace_size(const nwc_cache* cache, uint32_t rows, uint32_t q_heads, uint32_t n_groups, size_t* bytes) {
+  if (!bytes) return NWC_ERR_INVALID_ARG;
+  const nwc_status st = attend_shape(cache, rows, q_heads, n_groups);
+  if (st) return st;
+  *bytes = attend_layout(rows, q_heads, n_groups, cache->head_dim, attend_grid(256, cache->head_dim)).bytes;
+  return NWC_OK;
+}
+
+nwc_status nwc_attend(const nwc_cache* cache, const nwc_page_table* table, const nwc_groups* groups, const int32_t* lengths_dev,
+                      const uint16_t* q_dev, uint64_t ldq, uint32_t q_heads, float scale, uint16_t* out_dev, uint64_t ldo,
+                      void* ws, size_t ws_bytes, void* stream) {
+  if (!cache || !table || !lengths_dev || !q_dev || !out_dev || !ws || !std::isfinite(scale) || scale <= 0.f)
+    return NWC_ERR_INVALID_ARG;
+  const uint32_t n_groups = groups ? groups->count : 0;
+  if (groups && (groups->reserved || (n_groups && (!groups->start || !groups->len)))) return NWC_ERR_INVALID_ARG;
+  AttendArgs a = {};
+  nwc_status st = attend_shape(cache, table->rows, q_heads, n_groups);
+  if (!st) st = check_cache(cache, table, &a.pages);
+  if (st) return st;
+  const uint32_t d = cache->head_dim, rows = table->rows;
+  const uint64_t row = static_cast<uint64_t>(q_heads) * d;
+  if (ldq < row || ldo < row || ldq > kMaxStride || ldo > kMaxStride) return NWC_ERR_INVALID_ARG;
+  if ((static_cast<uint64_t>(table->cols) << a.pages.shift) > kAttendMaxLen) return NWC_ERR_UNSUPPORTED;
+  if (!aligned(q_dev, 16) || !aligned(out_dev, 16) || ldq % 8 || ldo % 8 || !aligned(lengths_dev, 4) || !aligned(ws, 256) ||
+      (n_groups && (!aligned(groups->start, 4) || !aligned(groups->len, 4))))
+    return NWC_ERR_ALIGNMENT;
+  if (ws_bytes < attend_layout(rows, q_heads, n_groups, d, attend_grid(256, d)).bytes) return NWC_ERR_BUFFER_TOO_SMALL;
+  const uint32_t cus = std::min(cu_count(), 256u);
+  if (cus == 0) return NWC_ERR_HIP;
+  const uint32_t grid = attend_grid(cus, d);
+  const AttendLayout L = attend_layout(rows, q_heads, n_groups, d, grid);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  a.k = cache->k;
+  a.v = cache->v;
+  a.q = q_dev;
+  a.out = out_dev;
+  a.lengths = lengths_dev;
+  if (n_groups) {
+    a.group_start = groups->start;
+    a.group_len = groups->len;
+  }
+  a.ldq = ldq;
+  a.ldo = ldo;
+  a.hq = q_heads;
+  a.hkv = cache->kv_heads;
+  a.ratio = q_heads / cache->kv_heads;
+  a.n_groups = n_groups;
+  a.scale2 = scale * kLog2e;
+  a.part_o = reinterpret_cast<float*>(w);
+  a.part_ml = reinterpret_cast<float*>(w + L.ml);
+  a.plan = reinterpret_cast<uint32_t*>(w + L.plan);
+  a.min_quota = 1;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (d) {
+    case 64: return launch_attend<64>(a, grid, s);
+    case 96: return launch_attend<96>(a, grid, s);
+    case 128: return launch_attend<128>(a, grid, s);
+    case 192: return launch_attend<192>(a, grid, s);
+    default: return launch_attend<256>(a, grid, s);
+  }
+}
+
+}  // extern "C"

@@ -346,6 +346,136 @@ nwc_status nwc_gemv_bf16(const uint16_t *w_dev, uint64_t rows, uint64_t cols, ui
 nwc_status nwc_read_probe(const void *buf_dev, size_t bytes, uint32_t *sink_dev, uint32_t groups,
                           int layout, void *stream);
 
+/* ------------------------------------------------ the attention side ---
+ * What a decode step does between its projections ("NWC -- Neural Weight
+ * Compression", results table: greedy decoding, whole tokens): queries and
+ * keys normed and turned by their position, keys and values appended to a
+ * paged cache, attention over that cache.  All data BF16, all arithmetic
+ * FP32 (angles FP64), one rounding to BF16 per output value.
+ *
+ * Positions, lengths and page tables live on the device: one captured graph
+ * serves a growing cache.  The host checks what it can see (pointers, sizes,
+ * alignment); the kernels check every position, row and page number before
+ * they use it, so a wrong one leaves data out and never reads or writes
+ * outside the described memory. */
+
+/* Heads of one tensor: [tokens, heads, head_dim], a token's heads side by
+ * side, tokens ld elements apart (ld % 8 == 0, pointers 16-byte aligned).
+ * weight (device, head_dim BF16, 16-byte aligned): each head is divided by
+ * the root of its mean square (+ eps) and multiplied by it; NULL: no norm.
+ * dst may be src itself with the same ld (each head is read before it is
+ * written); any other overlap is an error the library does not see. */
+typedef struct {
+  const uint16_t *src;
+  uint16_t *dst;
+  const uint16_t *weight;
+  uint64_t ld_src, ld_dst;
+  uint32_t heads;
+  uint32_t reserved;               /* 0 */
+} nwc_heads;
+
+/* Rotation by position: pair i of a head's first `dims` components turns by
+ * position * freqs[i] radians (freqs: device, dims / 2 floats, 4-byte
+ * aligned; the product and its reduction to one turn in FP64, so far
+ * positions keep their angle).  style NWC_ROPE_HALF: pair i is (i, i + dims
+ * / 2); NWC_ROPE_PAIRS: (2 i, 2 i + 1).  dims a multiple of 16, at most
+ * head_dim; 0 (freqs may be NULL): no rotation. */
+typedef enum { NWC_ROPE_HALF = 0, NWC_ROPE_PAIRS = 1 } nwc_rope_style;
+typedef struct {
+  const float *freqs;
+  uint32_t dims;
+  uint32_t style;
+} nwc_rope;
+
+/* Norm and rotation of query and key heads in one pass: token t of q and k
+ * (either may be NULL, not both) by its position positions_dev[t] (device,
+ * int32).  A token of negative position is padding: its dst rows are left as
+ * they were.  head_dim a multiple of 8, 8..256.  Async.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (head_dim, rope), HIP. */
+nwc_status nwc_qk_norm_rope(const nwc_heads *q, const nwc_heads *k, uint32_t tokens, uint32_t head_dim,
+                            float eps, const nwc_rope *rope, const int32_t *positions_dev, void *stream);
+
+/* A paged cache of one layer: page p of the keys is kv_heads x page_len x
+ * head_dim BF16 values at k + p * page_stride, of the values the same at v
+ * (page_stride >= kv_heads * page_len * head_dim elements, a multiple of 8, so
+ * keys, values and layers may interleave in one allocation; 16-byte aligned
+ * pointers).  page_len a power of two, 16..1024. */
+typedef struct {
+  uint16_t *k, *v;
+  uint64_t n_pages, page_stride;
+  uint32_t kv_heads, head_dim, page_len;
+  uint32_t reserved;               /* 0 */
+} nwc_cache;
+
+/* Page tables: position p of row r is slot p % page_len of page
+ * ids[r * ld + p / page_len] (device, int32).  rows x cols entries, ld >=
+ * cols.  Entries past a row's length are never used; an entry outside
+ * 0..n_pages-1 within it names no page: nothing is stored there and
+ * attention does not see those positions. */
+typedef struct {
+  const int32_t *ids;
+  uint64_t ld;
+  uint32_t rows, cols;
+} nwc_page_table;
+
+/* Append to the cache: for each token t the keys k->src, normed and turned
+ * as by nwc_qk_norm_rope, and the values v_dev [tokens, kv_heads, head_dim]
+ * (token stride ld_v), both to position positions_dev[t] of table row
+ * rows_dev[t] (device, int32; NULL: token t is row t, so one token per
+ * sequence).  k->dst and k->ld_dst are not used.  q, if not NULL, is normed
+ * and turned in the same launch.  A token of negative position is skipped,
+ * its queries too; one whose row or page does not exist is not stored.  Two
+ * tokens of one call must not name one slot (its content would be either's,
+ * key and value perhaps not the same one's); a page shared by several rows
+ * is the caller's to copy before a row writes to it.  head_dim a multiple of
+ * 8, 8..256.  Async.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (head_dim, page_len, rope), HIP. */
+nwc_status nwc_kv_append(const nwc_cache *cache, const nwc_page_table *table, const nwc_heads *k,
+                         const uint16_t *v_dev, uint64_t ld_v, const nwc_heads *q, uint32_t tokens,
+                         float eps, const nwc_rope *rope, const int32_t *positions_dev,
+                         const int32_t *rows_dev, void *stream);
+
+/* Rows that share a prefix: group i is rows start[i] .. start[i + 1] - 1,
+ * whose first len[i] positions hold the same tokens (start: device, count + 1
+ * int32, ascending; len: device, count int32).  The positions are read once
+ * for the whole group, through the table row of the group's first row that is
+ * long enough; a row shorter than len[i] takes no part and is read alone, as
+ * is a row of no group.  len need not be a multiple of page_len.  Groups
+ * only say what may be read once: where the tables agree the result is that
+ * of no groups, up to rounding. */
+typedef struct {
+  const int32_t *start;
+  const int32_t *len;
+  uint32_t count;
+  uint32_t reserved;               /* 0 */
+} nwc_groups;
+
+/* Attention of one query token per row over the paged cache:
+ * out[r, h] = sum_p w_p v[p], w = softmax_p(scale q[r, h] . k[p]), over the
+ * positions p < lengths_dev[r] (device, int32) of key-value head
+ * h / (q_heads / kv_heads).  q_dev and out_dev [rows, q_heads, head_dim],
+ * rows ldq / ldo elements apart (multiples of 8, 16-byte aligned), rows =
+ * table->rows.  Length 0 gives zeros; a negative length marks a padding row,
+ * whose output is left as it was; a length past the table's cols *
+ * page_len is cut to it.  Several tokens of one sequence are several rows
+ * with the same pages and lengths one apart, in one group.  groups NULL or
+ * count 0: nothing shared.
+ * scale finite and > 0.  head_dim 64, 96, 128, 192 or 256; q_heads a multiple of kv_heads, at most
+ * 64 times it; at most 4096 rows; cols * page_len <= 2^22.
+ * Softmax statistics and sums in FP32; the weights w are rounded to BF16 for
+ * the matrix cores (relative error 2^-9 each, the size of the output's own
+ * rounding).  Repeated calls give the same bits.  ws (device, 256-byte
+ * aligned, at least nwc_attend_workspace_size bytes for these rows, q_heads
+ * and group count; no initial content needed); calls that share it must not
+ * run concurrently.  Async.
+ * Errors: INVALID_ARG, BUFFER_TOO_SMALL (ws), ALIGNMENT, UNSUPPORTED, HIP. */
+nwc_status nwc_attend_workspace_size(const nwc_cache *cache, uint32_t rows, uint32_t q_heads,
+                                     uint32_t n_groups, size_t *bytes);
+nwc_status nwc_attend(const nwc_cache *cache, const nwc_page_table *table, const nwc_groups *groups,
+                      const int32_t *lengths_dev, const uint16_t *q_dev, uint64_t ldq, uint32_t q_heads,
+                      float scale, uint16_t *out_dev, uint64_t ldo, void *ws, size_t ws_bytes,
+                      void *stream);
+
 /* Test hook for the bounded waits of nwc_gemm_skinny's matrix-core kernel
  * (batch >= 5, 8-row tiles), whose decoding and matrix-core wavefronts wait
  * for each other through flags in LDS.  Every such wait gives up after
