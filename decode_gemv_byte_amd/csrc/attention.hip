@@ -213,13 +213,13 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
 // turns that block by one byte permute per operand register.  No value crosses
 // lanes in the loop but the column's maximum, and that only when it grows.
 
+constexpr uint32_t kCap = 128;  // columns of a block: 4 wavefronts of 2 16-column tiles
+
 template <int D>
 struct AttendShape {
-  static constexpr int kNtMax = D <= 128 ? 4 : 2;  // 16-column tiles of a block
-  static constexpr int kCap = 16 * kNtMax;
-  static constexpr int kDt = D / 16;                // 16-row tiles of O^T = components of a lane
-  static constexpr int kKs = D / 32;                // steps of the K Q^T product
-  static constexpr int kQLd = D + 8, kJLd = D + 4;  // padded LDS rows (banks)
+  static constexpr int kDt = D / 16;    // 16-row tiles of O^T = components of a lane
+  static constexpr int kKs = D / 32;    // steps of the K Q^T product
+  static constexpr int kJLd = D + 4;    // padded LDS rows (banks)
 };
 
 struct AttendArgs {
@@ -292,7 +292,7 @@ __device__ void block_scan(uint32_t* v, uint32_t n, uint32_t* carry) {
 
 // Lengths and groups (whatever they hold) into a plan whose ranges are all in
 // bounds: starts made ascending within 0..rows, lengths within 0..capacity.
-__device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t cap, uint32_t* carry) {
+__device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t* carry) {
   const uint32_t rows = a.pages.rows, G = a.n_groups, tid = threadIdx.x;
   const int32_t most = static_cast<int32_t>(a.pages.cols << a.pages.shift);
   for (uint32_t i = tid; i < G; i += kAttendThreads) {
@@ -320,7 +320,7 @@ __device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t cap, uint
     if (shares) atomicMin(&p.g_row[g], r);
   }
   __syncthreads();
-  const uint32_t blocks = (a.ratio + cap - 1) / cap;  // column blocks of one row
+  const uint32_t blocks = (a.ratio + kCap - 1) / kCap;  // column blocks of one row
   for (uint32_t r = tid; r < rows; r += kAttendThreads) {
     const int32_t end = static_cast<int32_t>(p.row_end[r]);
     const uint32_t base = p.row_base[r];
@@ -330,7 +330,7 @@ __device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t cap, uint
   for (uint32_t i = tid; i < G; i += kAttendThreads) {
     const uint32_t cols = (p.g_start[i + 1] - p.g_start[i]) * a.ratio;
     const uint32_t units = p.g_row[i] < rows ? (p.g_units[i] + 31) / 32 : 0;
-    p.g_pre[i + 1] = units * ((cols + cap - 1) / cap);
+    p.g_pre[i + 1] = units * ((cols + kCap - 1) / kCap);
     // the units of one column block; the length stays the row_base of the rows
     p.g_units[i] = units;
   }
@@ -362,41 +362,23 @@ struct Segment {
 
 template <int D>
 struct Lds {
-  uint16_t q[AttendShape<D>::kCap][AttendShape<D>::kQLd];
   float join[4][16][AttendShape<D>::kJLd];
-  float m[4][AttendShape<D>::kCap], l[4][AttendShape<D>::kCap];
+  float m[4][32], l[4][32];  // [wavefront][column of the wavefront]
   uint32_t carry[8];
 };
 
-template <int D, int NT>
+// The workgroup's part of an item: CW wavefronts side by side take 16 NT columns
+// each of the same units (one read from HBM, the others find them in the
+// caches), 4 / CW in turn take different units.
+template <int D, int NT, int CW>
 __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segment& it, Lds<D>& s, bool direct,
                                                uint64_t slot) {
   using S = AttendShape<D>;
   constexpr int kDt = S::kDt, kKs = S::kKs;
+  constexpr uint32_t kTurns = 4 / CW;
   const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave), tid = threadIdx.x;
   const uint32_t n = lane % 16, g = lane / 16;
-  // queries to LDS, columns past the last as zeros
-  for (uint32_t i = tid; i < 16 * NT * (D / 8); i += kAttendThreads) {
-    const uint32_t c = i / (D / 8), e = i % (D / 8) * 8;
-    u32x4_t x = {0, 0, 0, 0};
-    if (c < it.cols) {
-      const uint32_t col = it.col0 + c, row = it.row0 + col / a.ratio, h = it.head * a.ratio + col % a.ratio;
-      x = *reinterpret_cast<const u32x4_t*>(a.q + row * a.ldq + static_cast<uint64_t>(h) * D + e);
-    }
-    *reinterpret_cast<u32x4_t*>(&s.q[c][e]) = x;
-  }
-  __syncthreads();
-
-  f32x4_t o[kDt][NT];
-  float m[NT], l[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    m[t] = kNoMax;
-    l[t] = 0.f;
-#pragma unroll
-    for (int d = 0; d < kDt; ++d) o[d][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  }
-
+  const uint32_t wcol = wave % CW * (16 * NT), turn = wave / CW;
   const uint32_t mask = (1u << a.pages.shift) - 1;
   const uint64_t head_off = (static_cast<uint64_t>(it.head) << a.pages.shift) * D;
   // this lane's key positions (tile 0) and block of 8 value positions in a unit
@@ -425,14 +407,38 @@ __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segmen
     for (int j = 0; j < 8; ++j) __builtin_memcpy(vr[j], p + j * D, 2 * kDt);
   };
 
-  uint32_t u = it.u0 + wave;
+  f32x4_t o[kDt][NT];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = kNoMax;
+    l[t] = 0.f;
+#pragma unroll
+    for (int d = 0; d < kDt; ++d) o[d][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+
+  uint32_t u = it.u0 + turn;
   if (u < it.u1) {
     int32_t kid = page_of(32 * u + kpos), vid = page_of(32 * u + vpos);
+    // queries: this lane's column of each tile, 8 components a step; zeros past the last column
+    u32x4_t qf[kKs][NT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      const uint32_t col = wcol + 16 * c + n;
+      const bool live = col < it.cols;
+      const uint32_t at = it.col0 + (live ? col : 0), row = it.row0 + at / a.ratio, h = it.head * a.ratio + at % a.ratio;
+      const uint16_t* p = a.q + row * a.ldq + static_cast<uint64_t>(h) * D + 8 * g;
+#pragma unroll
+      for (int k = 0; k < kKs; ++k) {
+        qf[k][c] = u32x4_t{0, 0, 0, 0};
+        if (live) qf[k][c] = *reinterpret_cast<const u32x4_t*>(p + 32 * k);
+      }
+    }
     load_k(kid, u);
     for (;;) {
       load_v(vid, u);
       const bool good = known(vid);
-      const uint32_t next = u + 4;
+      const uint32_t next = u + kTurns;
       const bool more = next < it.u1;
       if (more) {
         kid = page_of(32 * next + kpos);
@@ -444,15 +450,13 @@ __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segmen
 #pragma unroll
         for (int c = 0; c < NT; ++c) sc[t][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < kKs; ++k) {
+      for (int k = 0; k < kKs; ++k)
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          const bf16x8_t qf = *reinterpret_cast<const bf16x8_t*>(&s.q[16 * c + n][32 * k + 8 * g]);
+        for (int c = 0; c < NT; ++c)
 #pragma unroll
           for (int t = 0; t < 2; ++t)
-            sc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kf[t][k]), qf, sc[t][c], 0, 0, 0);
-        }
-      }
+            sc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kf[t][k]),
+                                                               __builtin_bit_cast(bf16x8_t, qf[k][c]), sc[t][c], 0, 0, 0);
       if (more) load_k(kid, next);
       const uint32_t first = 32 * u;
       if (first < it.p0 || first + 32 > it.p1 || !__all(good)) {  // an edge of the item, or a page that is none
@@ -521,7 +525,7 @@ __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segmen
     }
   }
 
-  // the four wavefronts' sums, brought to one maximum and added in order
+  // the sums of wavefronts with the same columns, brought to one maximum and added in order
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
     l[c] += lane_xor(l[c], 16);
@@ -534,9 +538,9 @@ __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segmen
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
-    float top = s.m[0][16 * c + n];
+    float top = m[c];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) top = fmaxf(top, s.m[w][16 * c + n]);
+    for (uint32_t w = 0; w < kTurns; ++w) top = fmaxf(top, s.m[w * CW + wave % CW][16 * c + n]);
     const float f = __builtin_amdgcn_exp2f(m[c] - top);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -545,17 +549,18 @@ __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segmen
       for (int d = 0; d < kDt; ++d) dst[d] = o[d][c][i] * f;
     }
     __syncthreads();
-    for (uint32_t i = tid; i < 16 * (D / 4); i += kAttendThreads) {
-      const uint32_t col = i / (D / 4), e = i % (D / 4) * 4, cc = 16 * c + col;
+    for (uint32_t i = tid; i < CW * 16 * (D / 4); i += kAttendThreads) {
+      const uint32_t col = i / (D / 4) % 16, cw = i / (D / 4) / 16, e = i % (D / 4) * 4;
+      const uint32_t cc = cw * (16 * NT) + 16 * c + col;
       if (cc < it.cols) {
         f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-        float total = 0.f, best = s.m[0][cc];
+        float total = 0.f, best = s.m[cw][16 * c + col];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) best = fmaxf(best, s.m[w][cc]);
+        for (uint32_t w = 1; w < kTurns; ++w) best = fmaxf(best, s.m[w * CW + cw][16 * c + col]);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          sum += *reinterpret_cast<const f32x4_t*>(&s.join[w][col][e]);
-          total += s.l[w][cc] * __builtin_amdgcn_exp2f(s.m[w][cc] - best);
+        for (uint32_t w = 0; w < kTurns; ++w) {
+          sum += *reinterpret_cast<const f32x4_t*>(&s.join[w * CW + cw][col][e]);
+          total += s.l[w * CW + cw][16 * c + col] * __builtin_amdgcn_exp2f(s.m[w * CW + cw][16 * c + col] - best);
         }
         if (direct) {
           const float r = total == 0.f ? 0.f : 1.f / total;
@@ -582,9 +587,9 @@ __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segmen
 // workgroups that meet follow each other (either the item or the workgroup
 // steps on), so no two overlap.
 __device__ __forceinline__ uint64_t part_slot(const AttendArgs& a, uint32_t head, bool prefix, uint32_t row, uint32_t col0,
-                                              uint64_t wg, uint32_t cap) {
+                                              uint64_t wg) {
   const uint64_t cols = static_cast<uint64_t>(a.pages.rows) * a.ratio;
-  return (2 * head + (prefix ? 0 : 1)) * cols + static_cast<uint64_t>(row) * a.ratio + col0 + wg * cap;
+  return (2 * head + (prefix ? 0 : 1)) * cols + static_cast<uint64_t>(row) * a.ratio + col0 + wg * kCap;
 }
 
 // Largest i in [0, n) with pre[i] <= x (pre ascending, pre[0] = 0).
@@ -599,12 +604,11 @@ __device__ __forceinline__ uint32_t find_last(const uint32_t* pre, uint32_t n, u
 
 template <int D>
 __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(const AttendArgs a) {
-  using S = AttendShape<D>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   Lds<D>& s = *reinterpret_cast<Lds<D>*>(lds);
   const uint32_t rows = a.pages.rows, G = a.n_groups;
   const Plan p(reinterpret_cast<uint32_t*>(lds + sizeof(Lds<D>)), rows, G);
-  make_plan(a, p, S::kCap, s.carry);
+  make_plan(a, p, s.carry);
   if (blockIdx.x == 0)
     for (uint32_t i = threadIdx.x; i < Plan::words(rows, G); i += kAttendThreads) a.plan[i] = p.head[i];
   const uint32_t units = p.head[0], prefix_units = p.head[2];
@@ -629,7 +633,7 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
       done = in - block * n_units;
       first = 0;
       item_row = p.g_start[i];
-      it.col0 = block * S::kCap;
+      it.col0 = block * kCap;
       it.cols = (p.g_start[i + 1] - item_row) * a.ratio - it.col0;
       it.ids = a.pages.ids + p.g_row[i] * a.pages.ld;
       it.p0 = 0;
@@ -642,80 +646,103 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
       const uint32_t in = own - p.row_pre[r], block = in / n_units;
       done = in - block * n_units;
       item_row = r;
-      it.col0 = block * S::kCap;
+      it.col0 = block * kCap;
       it.cols = a.ratio - it.col0;
       it.ids = a.pages.ids + r * a.pages.ld;
       it.p0 = base;
       it.p1 = stop;
     }
     it.row0 = item_row;
-    it.cols = min(it.cols, static_cast<uint32_t>(S::kCap));
+    it.cols = min(it.cols, kCap);
     const uint32_t take = static_cast<uint32_t>(min(static_cast<uint64_t>(n_units - done), end - at));
     it.u0 = first + done;
     it.u1 = it.u0 + take;
     const bool direct = !prefix && it.p0 == 0 && take == n_units;
-    const uint64_t slot = part_slot(a, it.head, prefix, item_row, it.col0, wg, S::kCap);
+    const uint64_t slot = part_slot(a, it.head, prefix, item_row, it.col0, wg);
     if (it.cols <= 16)
-      attend_segment<D, 1>(a, it, s, direct, slot);
-    else if (S::kNtMax == 2 || it.cols <= 32)
-      attend_segment<D, 2>(a, it, s, direct, slot);
+      attend_segment<D, 1, 1>(a, it, s, direct, slot);
+    else if (it.cols <= 32)
+      attend_segment<D, 2, 1>(a, it, s, direct, slot);
+    else if (it.cols <= 64)
+      attend_segment<D, 2, 2>(a, it, s, direct, slot);
     else
-      attend_segment<D, S::kNtMax>(a, it, s, direct, slot);
+      attend_segment<D, 2, 4>(a, it, s, direct, slot);
     at += take;
   }
 }
 
-// One workgroup per row and key-value head: the partial sums of its columns,
-// prefix first, in the order of the positions.
+// One workgroup per row and query head: the partial sums of its column, prefix
+// first.  D / 4 threads hold a column's components; the parts go round kLines
+// such lines, each keeps a running maximum, and the lines are added in order.
 template <int D>
 __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs a) {
-  constexpr uint32_t kCap = AttendShape<D>::kCap;
-  const uint32_t rows = a.pages.rows, r = blockIdx.x / a.hkv, head = blockIdx.x % a.hkv;
+  constexpr uint32_t kLine = D / 4, kLines = kAttendThreads / kLine;
+  __shared__ f32x4_t sums[kLines][kLine];
+  __shared__ float ms[kLines], ls[kLines];
+  const uint32_t rows = a.pages.rows, r = blockIdx.x / a.hq, h = blockIdx.x % a.hq, head = h / a.ratio, j = h % a.ratio;
   const Plan p(a.plan, rows, a.n_groups);
   const uint32_t units = p.head[0], prefix_units = p.head[2];
   const uint64_t quota = p.quota();
-  const uint32_t base = p.row_base[r], g = p.row_group[r];
+  const uint32_t base = p.row_base[r], g = p.row_group[r], own_pre = p.row_pre[r];
   const int32_t stop = static_cast<int32_t>(p.row_end[r]);
   if (stop < 0) return;  // padding
   const uint32_t own_units = stop > static_cast<int32_t>(base) ? (stop + 31u) / 32 - base / 32 : 0;
-  for (uint32_t i = threadIdx.x; i < a.ratio * (D / 4); i += kAttendThreads) {
-    const uint32_t j = i / (D / 4), e = i % (D / 4) * 4;
-    uint64_t w0[2] = {1, 1}, w1[2] = {0, 0}, slot[2] = {0, 0};  // workgroups of the prefix and of the own positions
-    if (base) {
-      const uint32_t col = (r - p.g_start[g]) * a.ratio + j, block = col / kCap, n = p.g_units[g];
-      const uint64_t first = static_cast<uint64_t>(units) * head + p.g_pre[g] + static_cast<uint64_t>(block) * n;
-      w0[0] = first / quota;
-      w1[0] = (first + n - 1) / quota;
-      slot[0] = part_slot(a, head, true, p.g_start[g], block * kCap, 0, kCap) + col % kCap;
-    }
-    if (own_units) {
-      const uint32_t block = j / kCap;
-      const uint64_t first = static_cast<uint64_t>(units) * head + prefix_units + p.row_pre[r] +
-                             static_cast<uint64_t>(block) * own_units;
-      w0[1] = first / quota;
-      w1[1] = (first + own_units - 1) / quota;
-      slot[1] = part_slot(a, head, false, r, block * kCap, 0, kCap) + j % kCap;
-      if (!base && w0[1] == w1[1]) continue;  // k_attend wrote the output itself
-    }
-    float best = kNoMax;
-    for (int k = 0; k < 2; ++k)
-      for (uint64_t w = w0[k]; w <= w1[k] && w0[k] <= w1[k]; ++w) best = fmaxf(best, a.part_ml[2 * (slot[k] + w * kCap)]);
-    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-    float total = 0.f;
-    for (int k = 0; k < 2; ++k)
-      for (uint64_t w = w0[k]; w <= w1[k] && w0[k] <= w1[k]; ++w) {
-        const uint64_t at = slot[k] + w * kCap;
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - best);
-        total += a.part_ml[2 * at + 1] * f;
-        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part_o + at * D + e);
-        sum += x * f;
-      }
-    const float f = total == 0.f ? 0.f : 1.f / total;
-    uint2 w;
-    w.x = pack_bf16(sum[0] * f, sum[1] * f);
-    w.y = pack_bf16(sum[2] * f, sum[3] * f);
-    *reinterpret_cast<uint2*>(a.out + r * a.ldo + static_cast<uint64_t>(head * a.ratio + j) * D + e) = w;
+  // the workgroup that has a unit (32-bit division where the numbers allow)
+  auto owner = [&](uint64_t x) -> uint32_t {
+    return static_cast<uint32_t>((x | quota) >> 32 ? x / quota : static_cast<uint32_t>(x) / static_cast<uint32_t>(quota));
+  };
+  uint32_t w0 = 0, n0 = 0, w1 = 0, n1 = 0;  // first workgroup and number of parts: of the prefix, of the own positions
+  uint64_t slot0 = 0, slot1 = 0;
+  if (base) {
+    const uint32_t first_row = p.g_start[g], col = (r - first_row) * a.ratio + j, block = col / kCap, n = p.g_units[g];
+    const uint64_t first = static_cast<uint64_t>(units) * head + p.g_pre[g] + static_cast<uint64_t>(block) * n;
+    w0 = owner(first);
+    n0 = owner(first + n - 1) - w0 + 1;
+    slot0 = part_slot(a, head, true, first_row, block * kCap, w0) + col % kCap;
   }
+  if (own_units) {
+    const uint64_t first = static_cast<uint64_t>(units) * head + prefix_units + own_pre;
+    w1 = owner(first);
+    n1 = owner(first + own_units - 1) - w1 + 1;
+    slot1 = part_slot(a, head, false, r, 0, w1) + j;
+    if (!base && n1 == 1) return;  // k_attend wrote the output itself
+  }
+  const uint32_t line = threadIdx.x / kLine, e = threadIdx.x % kLine * 4, parts = n0 + n1;
+  f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+  float best = kNoMax, total = 0.f;
+  if (line < kLines) {
+#pragma unroll 4
+    for (uint32_t i = line; i < parts; i += kLines) {
+      const uint64_t at = i < n0 ? slot0 + static_cast<uint64_t>(i) * kCap : slot1 + static_cast<uint64_t>(i - n0) * kCap;
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
+      const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part_o + at * D + e);
+      const float top = fmaxf(best, ml.x), f = __builtin_amdgcn_exp2f(best - top), f2 = __builtin_amdgcn_exp2f(ml.x - top);
+      sum = sum * f + x * f2;
+      total = total * f + ml.y * f2;
+      best = top;
+    }
+    sums[line][e / 4] = sum;
+    if (e == 0) {
+      ms[line] = best;
+      ls[line] = total;
+    }
+  }
+  __syncthreads();
+  if (line != 0) return;
+  for (uint32_t i = 1; i < kLines; ++i) best = fmaxf(best, ms[i]);
+  sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  total = 0.f;
+#pragma unroll
+  for (uint32_t i = 0; i < kLines; ++i) {
+    const float f = __builtin_amdgcn_exp2f(ms[i] - best);
+    sum += sums[i][e / 4] * f;
+    total += ls[i] * f;
+  }
+  const float f = total == 0.f ? 0.f : 1.f / total;
+  uint2 w;
+  w.x = pack_bf16(sum[0] * f, sum[1] * f);
+  w.y = pack_bf16(sum[2] * f, sum[3] * f);
+  *reinterpret_cast<uint2*>(a.out + r * a.ldo + static_cast<uint64_t>(h) * D + e) = w;
 }
 
 // ------------------------------------------------------------------- host ---
@@ -818,13 +845,12 @@ void set_rope(HeadsArgs* a, const nwc_rope* rope) {
 }
 
 // Workspace of nwc_attend: partial sums, maxima and sums, the plan.
-constexpr uint32_t kAttendMaxRows = 4096, kAttendMaxRatio = 64, kAttendMaxLen = 1u << 22;
+constexpr uint32_t kAttendMaxRows = 4096, kAttendMaxGroups = 1024, kAttendMaxRatio = 64, kAttendMaxLen = 1u << 22;
 struct AttendLayout {
   uint64_t ml, plan, bytes;
 };
 AttendLayout attend_layout(uint32_t rows, uint32_t q_heads, uint32_t groups, uint32_t d, uint32_t grid) {
-  const uint64_t cap = d <= 128 ? 64 : 32;
-  const uint64_t slots = 2 * static_cast<uint64_t>(rows) * q_heads + grid * cap;
+  const uint64_t slots = 2 * static_cast<uint64_t>(rows) * q_heads + static_cast<uint64_t>(grid) * kCap;
   auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
   AttendLayout L;
   L.ml = up(slots * d * 4);
@@ -838,7 +864,7 @@ nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uin
   const uint32_t d = c->head_dim;
   if (d != 64 && d != 96 && d != 128 && d != 192 && d != 256) return NWC_ERR_UNSUPPORTED;
   if (q_heads % c->kv_heads) return NWC_ERR_INVALID_ARG;
-  if (rows > kAttendMaxRows || groups > kAttendMaxRows || q_heads / c->kv_heads > kAttendMaxRatio || q_heads > kMaxHeads)
+  if (rows > kAttendMaxRows || groups > kAttendMaxGroups || q_heads / c->kv_heads > kAttendMaxRatio || q_heads > kMaxHeads)
     return NWC_ERR_UNSUPPORTED;
   return NWC_OK;
 }
@@ -853,7 +879,7 @@ nwc_status launch_attend(const AttendArgs& a, uint32_t grid, hipStream_t s) {
     return NWC_ERR_HIP;
   const nwc_status st = launch(k_attend<D>, dim3(grid), dim3(kAttendThreads), lds, s, a);
   if (st) return st;
-  return launch(k_attend_join<D>, dim3(a.pages.rows * a.hkv), dim3(kAttendThreads), 0, s, a);
+  return launch(k_attend_join<D>, dim3(a.pages.rows * a.hq), dim3(kAttendThreads), 0, s, a);
 }
 
 }  // namespace
