@@ -233,7 +233,7 @@ struct AttendArgs {
   float* part_o;  // workspace: partial sums [column slot][D]
   float* part_ml; // their maxima (log2 domain) and weight sums
   uint32_t* plan; // the plan for k_attend_join
-  uint32_t min_quota;
+  uint32_t min_quota, ring;  // least units of a workgroup; slots of the ring
 };
 
 constexpr int kAttendThreads = 256;
@@ -360,25 +360,106 @@ struct Segment {
   uint32_t p0, p1;     // positions that the item sees
 };
 
-template <int D>
-struct Lds {
-  float join[4][16][AttendShape<D>::kJLd];
-  float m[4][32], l[4][32];  // [wavefront][column of the wavefront]
-  uint32_t carry[8];
+// A wavefront's running sums for NT tiles of 16 columns: lane (n, g) holds column
+// n, components kDt (4 g + i) + t of O (tile t, i = 0 .. 3), the maximum of the
+// scores so far (log2 domain, the same in a column's four lanes) and its own
+// part of the sum of the weights.
+template <int D, int NT>
+struct Sums {
+  static constexpr int kDt = AttendShape<D>::kDt;
+  f32x4_t o[kDt][NT];
+  float m[NT], l[NT];
+  __device__ Sums() {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t] = kNoMax;
+      l[t] = 0.f;
+#pragma unroll
+      for (int d = 0; d < kDt; ++d) o[d][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+  // Weights of one unit's scores (lane: positions 8 g .. 8 g + 7 of its column),
+  // rounded to BF16 as the matrix cores take them; their sum is of the unrounded
+  // ones.
+  __device__ __forceinline__ void weigh(const f32x4_t (&sc)[2][NT], float scale2, bf16x8_t (&pf)[NT]) {
+    float mx[NT];
+    bool grow = false;
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      float x = fmaxf(fmaxf(sc[0][c][0], sc[0][c][1]), fmaxf(sc[0][c][2], sc[0][c][3]));
+      x = fmaxf(x, fmaxf(fmaxf(sc[1][c][0], sc[1][c][1]), fmaxf(sc[1][c][2], sc[1][c][3])));
+      mx[c] = x * scale2;
+      grow |= mx[c] > m[c] + 8.f;  // weights up to 2^8 lose nothing: BF16 and FP32 keep their relative precision
+    }
+    if (__any(grow)) {
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        float x = mx[c];
+        x = fmaxf(x, lane_xor(x, 16));
+        x = fmaxf(x, lane_xor(x, 32));
+        x = fmaxf(x, m[c]);
+        const float f = __builtin_amdgcn_exp2f(m[c] - x);
+        m[c] = x;
+        l[c] *= f;
+#pragma unroll
+        for (int d = 0; d < kDt; ++d) o[d][c] *= f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      float p[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p[j] = __builtin_amdgcn_exp2f(fmaf(sc[j / 4][c][j % 4], scale2, -m[c]));
+        l[c] += p[j];
+      }
+      u32x4_t w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
+      pf[c] = __builtin_bit_cast(bf16x8_t, w);
+    }
+  }
+  // o += V^T P^T for one unit: vr[j] are the lane's components of position 8 g + j.
+  __device__ __forceinline__ void add(const uint32_t (&vr)[8][kDt / 2], const bf16x8_t (&pf)[NT]) {
+#pragma unroll
+    for (int d = 0; d < kDt; ++d) {
+      u32x4_t w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = __builtin_amdgcn_perm(vr[2 * j + 1][d / 2], vr[2 * j][d / 2], d % 2 ? 0x07060302 : 0x05040100);
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+        o[d][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w), pf[c], o[d][c], 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      l[c] += lane_xor(l[c], 16);
+      l[c] += lane_xor(l[c], 32);
+    }
+  }
 };
 
-// The workgroup's part of an item: CW wavefronts side by side take 16 NT columns
-// each of the same units (one read from HBM, the others find them in the
-// caches), 4 / CW in turn take different units.
-template <int D, int NT, int CW>
-__device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segment& it, Lds<D>& s, bool direct,
+// LDS of a workgroup: the fixed part, then the plan, then the ring of slots or
+// the sums that the wavefronts exchange (never both).
+struct LdsFixed {
+  float m[4][32], l[4][32];  // [wavefront][column]
+  uint32_t good[4][4];       // [slot][wavefront]: the page exists
+  uint32_t carry[8];
+};
+template <int D>
+using Join = float[4][16][AttendShape<D>::kJLd];
+
+// The workgroup's part of an item of at most 16 NT columns: the wavefronts take
+// its units in turn.
+template <int D, int NT>
+__device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segment& it, LdsFixed& s, Join<D>& join, bool direct,
                                                uint64_t slot) {
   using S = AttendShape<D>;
   constexpr int kDt = S::kDt, kKs = S::kKs;
-  constexpr uint32_t kTurns = 4 / CW;
   const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave), tid = threadIdx.x;
   const uint32_t n = lane % 16, g = lane / 16;
-  const uint32_t wcol = wave % CW * (16 * NT), turn = wave / CW;
   const uint32_t mask = (1u << a.pages.shift) - 1;
   const uint64_t head_off = (static_cast<uint64_t>(it.head) << a.pages.shift) * D;
   // this lane's key positions (tile 0) and block of 8 value positions in a unit
@@ -407,24 +488,16 @@ __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segmen
     for (int j = 0; j < 8; ++j) __builtin_memcpy(vr[j], p + j * D, 2 * kDt);
   };
 
-  f32x4_t o[kDt][NT];
-  float m[NT], l[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    m[t] = kNoMax;
-    l[t] = 0.f;
-#pragma unroll
-    for (int d = 0; d < kDt; ++d) o[d][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  }
+  Sums<D, NT> acc;
 
-  uint32_t u = it.u0 + turn;
+  uint32_t u = it.u0 + wave;
   if (u < it.u1) {
     int32_t kid = page_of(32 * u + kpos), vid = page_of(32 * u + vpos);
     // queries: this lane's column of each tile, 8 components a step; zeros past the last column
     u32x4_t qf[kKs][NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
-      const uint32_t col = wcol + 16 * c + n;
+      const uint32_t col = 16 * c + n;
       const bool live = col < it.cols;
       const uint32_t at = it.col0 + (live ? col : 0), row = it.row0 + at / a.ratio, h = it.head * a.ratio + at % a.ratio;
       const uint16_t* p = a.q + row * a.ldq + static_cast<uint64_t>(h) * D + 8 * g;
@@ -438,7 +511,7 @@ __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segmen
     for (;;) {
       load_v(vid, u);
       const bool good = known(vid);
-      const uint32_t next = u + kTurns;
+      const uint32_t next = u + 4;
       const bool more = next < it.u1;
       if (more) {
         kid = page_of(32 * next + kpos);
@@ -473,94 +546,47 @@ __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segmen
             if (!seen) vr[j][d] = 0;
         }
       }
-      float mx[NT];
-      bool grow = false;
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        float x = fmaxf(fmaxf(sc[0][c][0], sc[0][c][1]), fmaxf(sc[0][c][2], sc[0][c][3]));
-        x = fmaxf(x, fmaxf(fmaxf(sc[1][c][0], sc[1][c][1]), fmaxf(sc[1][c][2], sc[1][c][3])));
-        mx[c] = x * a.scale2;
-        grow |= mx[c] > m[c] + 8.f;  // weights up to 2^8 lose nothing: BF16 and FP32 keep their relative precision
-      }
-      if (__any(grow)) {
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          float x = mx[c];
-          x = fmaxf(x, lane_xor(x, 16));
-          x = fmaxf(x, lane_xor(x, 32));
-          x = fmaxf(x, m[c]);
-          const float f = __builtin_amdgcn_exp2f(m[c] - x);
-          m[c] = x;
-          l[c] *= f;
-#pragma unroll
-          for (int d = 0; d < kDt; ++d) o[d][c] *= f;
-        }
-      }
       bf16x8_t pf[NT];
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        float p[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          p[j] = __builtin_amdgcn_exp2f(fmaf(sc[j / 4][c][j % 4], a.scale2, -m[c]));
-          l[c] += p[j];
-        }
-        u32x4_t w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
-        pf[c] = __builtin_bit_cast(bf16x8_t, w);
-      }
-#pragma unroll
-      for (int d = 0; d < kDt; ++d) {
-        u32x4_t w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = __builtin_amdgcn_perm(vr[2 * j + 1][d / 2], vr[2 * j][d / 2], d % 2 ? 0x07060302 : 0x05040100);
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-          o[d][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w), pf[c], o[d][c], 0, 0, 0);
-      }
+      acc.weigh(sc, a.scale2, pf);
+      acc.add(vr, pf);
       if (!more) break;
       u = next;
     }
   }
 
   // the sums of wavefronts with the same columns, brought to one maximum and added in order
+  acc.finish();
+  if (g == 0)
 #pragma unroll
-  for (int c = 0; c < NT; ++c) {
-    l[c] += lane_xor(l[c], 16);
-    l[c] += lane_xor(l[c], 32);
-    if (g == 0) {
-      s.m[wave][16 * c + n] = m[c];
-      s.l[wave][16 * c + n] = l[c];
+    for (int c = 0; c < NT; ++c) {
+      s.m[wave][16 * c + n] = acc.m[c];
+      s.l[wave][16 * c + n] = acc.l[c];
     }
-  }
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
-    float top = m[c];
+    float top = acc.m[c];
 #pragma unroll
-    for (uint32_t w = 0; w < kTurns; ++w) top = fmaxf(top, s.m[w * CW + wave % CW][16 * c + n]);
-    const float f = __builtin_amdgcn_exp2f(m[c] - top);
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, s.m[w][16 * c + n]);
+    const float f = __builtin_amdgcn_exp2f(acc.m[c] - top);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float* dst = &s.join[wave][n][kDt * (4 * g + i)];  // O^T tile t, row 4 g + i: component kDt (4 g + i) + t
+      float* dst = &join[wave][n][kDt * (4 * g + i)];  // O^T tile t, row 4 g + i: component kDt (4 g + i) + t
 #pragma unroll
-      for (int d = 0; d < kDt; ++d) dst[d] = o[d][c][i] * f;
+      for (int d = 0; d < kDt; ++d) dst[d] = acc.o[d][c][i] * f;
     }
     __syncthreads();
-    for (uint32_t i = tid; i < CW * 16 * (D / 4); i += kAttendThreads) {
-      const uint32_t col = i / (D / 4) % 16, cw = i / (D / 4) / 16, e = i % (D / 4) * 4;
-      const uint32_t cc = cw * (16 * NT) + 16 * c + col;
+    for (uint32_t i = tid; i < 16 * (D / 4); i += kAttendThreads) {
+      const uint32_t col = i / (D / 4), e = i % (D / 4) * 4, cc = 16 * c + col;
       if (cc < it.cols) {
         f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-        float total = 0.f, best = s.m[cw][16 * c + col];
+        float total = 0.f, best = s.m[0][cc];
 #pragma unroll
-        for (uint32_t w = 1; w < kTurns; ++w) best = fmaxf(best, s.m[w * CW + cw][16 * c + col]);
+        for (int w = 1; w < 4; ++w) best = fmaxf(best, s.m[w][cc]);
 #pragma unroll
-        for (uint32_t w = 0; w < kTurns; ++w) {
-          sum += *reinterpret_cast<const f32x4_t*>(&s.join[w * CW + cw][col][e]);
-          total += s.l[w * CW + cw][16 * c + col] * __builtin_amdgcn_exp2f(s.m[w * CW + cw][16 * c + col] - best);
+        for (int w = 0; w < 4; ++w) {
+          sum += *reinterpret_cast<const f32x4_t*>(&join[w][col][e]);
+          total += s.l[w][cc] * __builtin_amdgcn_exp2f(s.m[w][cc] - best);
         }
         if (direct) {
           const float r = total == 0.f ? 0.f : 1.f / total;
@@ -579,6 +605,176 @@ __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segmen
       }
     }
     __syncthreads();
+  }
+}
+
+// A wave-uniform read of an array that this grid does not write (scalar load).
+__device__ __forceinline__ int32_t sload(const int32_t* p, uint64_t i) {
+  typedef const __attribute__((address_space(4))) int32_t ci32;
+  return ((ci32*)(reinterpret_cast<uintptr_t>(p)))[i];
+}
+
+// Wait until at most n of this wavefront's vector memory operations are left
+// and all its LDS operations are done, then for the other wavefronts.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  static_assert(N >= 0 && N < 64, "vmcnt holds 6 bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 0xF) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Where piece c of key row `row` (0 .. 31 of a unit) lies in its slot row, and
+// (INVERSE) which piece lies at c.  An operand read takes one piece of the rows
+// 8 (n / 4) + n % 4, n = 0 .. 15, which a slot row of D = 64, 96, 128, 192, 256
+// puts on 2, 4, 1, 2, 1 different groups of banks by itself.
+template <int D, bool INVERSE>
+__device__ __forceinline__ uint32_t key_piece(uint32_t row, uint32_t c) {
+  constexpr uint32_t kPieces = D / 8;
+  if (D == 128 || D == 256) return c ^ ((row & 3) | (row >> 3) << 2);
+  const uint32_t by = D == 96 ? row >> 3 : (row >> 1 & 1) | (row >> 3) << 1;
+  if (D == 64) return c ^ by;
+  const uint32_t x = INVERSE ? c + kPieces - by : c + by;
+  return x >= kPieces ? x - kPieces : x;
+}
+
+// The workgroup's part of an item of more than 32 columns: the wavefronts take
+// 16 NT columns each of the same units, which pass through a ring of slots in
+// LDS, loaded straight from the pages (a quarter of a unit's rows per
+// wavefront, `ring - 1` units ahead), so a unit is read once per workgroup.
+// One barrier per unit: behind it the unit has landed for all, and the slot of
+// the unit before is free.  A slot holds 32 rows of keys, then of values; the
+// 16-byte pieces of a key row are permuted by the row, so that the 16 rows
+// that one operand read touches lie in 64 different banks.
+template <int D, int NT>
+__device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment& it, uint8_t* slots, uint32_t (&good)[4][4],
+                                              bool direct, uint64_t slot) {
+  using S = AttendShape<D>;
+  constexpr int kDt = S::kDt, kKs = S::kKs, kLoads = (D + 63) / 64;
+  constexpr uint32_t kPieces = D / 8, kSlotBytes = 128 * D;
+  constexpr int kAlign = kDt % 8 == 0 ? 16 : kDt % 4 == 0 ? 8 : 4;
+  const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave);
+  const uint32_t n = lane % 16, g = lane / 16;
+  const uint64_t head_off = (static_cast<uint64_t>(it.head) << a.pages.shift) * D;
+  const uint32_t mask = (1u << a.pages.shift) - 1, units = it.u1 - it.u0;
+  auto issue = [&](uint32_t i, uint32_t at) {  // unit i of the segment into slot `at`
+    const uint32_t pos = 32 * (it.u0 + i) + 8 * wave, idx = pos >> a.pages.shift;
+    const int32_t id = idx < a.pages.cols ? sload(it.ids, idx) : -1;
+    const bool ok = static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages;
+    const uint64_t off = (ok ? static_cast<uint64_t>(id) : 0) * a.pages.page_stride + head_off + static_cast<uint64_t>(pos & mask) * D;
+    uint8_t* to = slots + at * kSlotBytes + wave * (16 * D);
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) {
+      const uint32_t piece = 64 * x + lane, row = piece / kPieces, c = piece % kPieces;
+      if (piece < 8 * kPieces) {  // D = 96: the second load is half a wavefront
+        __builtin_amdgcn_global_load_lds(a.k + off + row * D + 8 * key_piece<D, true>(8 * wave + row, c), to + 1024 * x, 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(a.v + off + row * D + 8 * c, to + 64 * D + 1024 * x, 16, 0, 0);
+      }
+    }
+    if (lane == 0) good[at][wave] = ok;
+  };
+
+  __syncthreads();  // the slots' last readers are done
+  u32x4_t qf[kKs][NT];
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    const uint32_t col = wave * (16 * NT) + 16 * c + n;
+    const bool live = col < it.cols;
+    const uint32_t at = it.col0 + (live ? col : 0), row = it.row0 + at / a.ratio, h = it.head * a.ratio + at % a.ratio;
+    const uint16_t* p = a.q + row * a.ldq + static_cast<uint64_t>(h) * D + 8 * g;
+#pragma unroll
+    for (int k = 0; k < kKs; ++k) {
+      qf[k][c] = u32x4_t{0, 0, 0, 0};
+      if (live) qf[k][c] = *reinterpret_cast<const u32x4_t*>(p + 32 * k);
+    }
+  }
+  // the queries have to be there before the first count of loads in flight
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int k = 0; k < kKs; ++k) asm volatile("" : "+v"(qf[k][c]));
+  const uint32_t ahead = a.ring - 1;
+  for (uint32_t i = 0; i < ahead && i < units; ++i) issue(i, i);
+  Sums<D, NT> acc;
+  uint32_t at = 0, to = ahead;  // slots of unit i and of the unit loaded next
+  for (uint32_t i = 0; i < units; ++i) {
+    // unit i is there when only the units after it are in flight
+    if (ahead == 1 || i + ahead > units)
+      wait_and_meet<0>();
+    else if (ahead == 2)
+      wait_and_meet<2 * kLoads>();
+    else
+      wait_and_meet<4 * kLoads>();
+    if (i + ahead < units) issue(i + ahead, to);
+    const uint8_t* ks = slots + at * kSlotBytes;
+    const uint8_t* vs = ks + 64 * D;
+    f32x4_t sc[2][NT];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < NT; ++c) sc[t][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kKs; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t row = 8 * (n / 4) + n % 4 + 4 * t;
+        const bf16x8_t kf = *reinterpret_cast<const bf16x8_t*>(ks + 16 * (row * kPieces + key_piece<D, false>(row, 4 * k + g)));
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+          sc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, __builtin_bit_cast(bf16x8_t, qf[k][c]), sc[t][c], 0, 0, 0);
+      }
+    uint32_t vr[8][kDt / 2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) __builtin_memcpy(vr[j], __builtin_assume_aligned(vs + 2 * ((8 * g + j) * D + kDt * n), kAlign), 2 * kDt);
+    const uint32_t first = 32 * (it.u0 + i);
+    const bool ok = good[at][g] != 0;
+    if (first < it.p0 || first + 32 > it.p1 || !__all(ok)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t pos = first + 8 * g + j;
+        const bool seen = ok && pos >= it.p0 && pos < it.p1;
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+          if (!seen) sc[j / 4][c][j % 4] = -INFINITY;
+#pragma unroll
+        for (int d = 0; d < kDt / 2; ++d)
+          if (!seen) vr[j][d] = 0;
+      }
+    }
+    bf16x8_t pf[NT];
+    acc.weigh(sc, a.scale2, pf);
+    acc.add(vr, pf);
+    at = at == ahead ? 0 : at + 1;
+    to = to == ahead ? 0 : to + 1;
+  }
+  acc.finish();
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    const uint32_t cc = wave * (16 * NT) + 16 * c + n;
+    if (cc >= it.cols) continue;
+    const float r = acc.l[c] == 0.f ? 0.f : 1.f / acc.l[c];
+    const uint32_t cl = it.col0 + cc, row = it.row0 + cl / a.ratio, h = it.head * a.ratio + cl % a.ratio;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t e = kDt * (4 * g + i);
+#pragma unroll
+      for (int d = 0; d < kDt; d += 4) {
+        const f32x4_t x = {acc.o[d][c][i], acc.o[d + 1][c][i], acc.o[d + 2][c][i], acc.o[d + 3][c][i]};
+        if (direct) {
+          uint2 w;
+          w.x = pack_bf16(x[0] * r, x[1] * r);
+          w.y = pack_bf16(x[2] * r, x[3] * r);
+          *reinterpret_cast<uint2*>(a.out + row * a.ldo + static_cast<uint64_t>(h) * D + e + d) = w;
+        } else {
+          *reinterpret_cast<f32x4_t*>(a.part_o + (slot + cc) * D + e + d) = x;
+        }
+      }
+    }
+    if (!direct && g == 0) {
+      a.part_ml[2 * (slot + cc)] = acc.m[c];
+      a.part_ml[2 * (slot + cc) + 1] = acc.l[c];
+    }
   }
 }
 
@@ -605,9 +801,11 @@ __device__ __forceinline__ uint32_t find_last(const uint32_t* pre, uint32_t n, u
 template <int D>
 __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(const AttendArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  Lds<D>& s = *reinterpret_cast<Lds<D>*>(lds);
+  LdsFixed& s = *reinterpret_cast<LdsFixed*>(lds);
   const uint32_t rows = a.pages.rows, G = a.n_groups;
-  const Plan p(reinterpret_cast<uint32_t*>(lds + sizeof(Lds<D>)), rows, G);
+  const Plan p(reinterpret_cast<uint32_t*>(lds + sizeof(LdsFixed)), rows, G);
+  uint8_t* big = lds + sizeof(LdsFixed) + (Plan::words(rows, G) * 4 + 15) / 16 * 16;
+  Join<D>& join = *reinterpret_cast<Join<D>*>(big);
   make_plan(a, p, s.carry);
   if (blockIdx.x == 0)
     for (uint32_t i = threadIdx.x; i < Plan::words(rows, G); i += kAttendThreads) a.plan[i] = p.head[i];
@@ -660,13 +858,13 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
     const bool direct = !prefix && it.p0 == 0 && take == n_units;
     const uint64_t slot = part_slot(a, it.head, prefix, item_row, it.col0, wg);
     if (it.cols <= 16)
-      attend_segment<D, 1, 1>(a, it, s, direct, slot);
-    else if (it.cols <= 32)
-      attend_segment<D, 2, 1>(a, it, s, direct, slot);
+      attend_segment<D, 1>(a, it, s, join, direct, slot);
+    else if (D <= 128 && it.cols <= 32)
+      attend_segment<D, D <= 128 ? 2 : 1>(a, it, s, join, direct, slot);
     else if (it.cols <= 64)
-      attend_segment<D, 2, 2>(a, it, s, direct, slot);
+      attend_shared<D, 1>(a, it, big, s.good, direct, slot);
     else
-      attend_segment<D, 2, 4>(a, it, s, direct, slot);
+      attend_shared<D, 2>(a, it, big, s.good, direct, slot);
     at += take;
   }
 }
@@ -775,6 +973,7 @@ uint32_t cu_count() {
 // Most heads of one tensor and elements of a page: products of sizes stay far
 // below 2^63 with strides below 2^40.
 constexpr uint32_t kMaxHeads = 65536;
+constexpr size_t kMaxLds = 160 * 1024;
 constexpr uint64_t kMaxStride = uint64_t{1} << 40;
 
 nwc_status check_rope(const nwc_rope* rope, uint32_t d) {
@@ -872,8 +1071,10 @@ nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uin
 uint32_t attend_grid(uint32_t cus, uint32_t d) { return cus * (d <= 128 ? 2 : 1); }
 
 template <int D>
-nwc_status launch_attend(const AttendArgs& a, uint32_t grid, hipStream_t s) {
-  const size_t lds = sizeof(Lds<D>) + static_cast<size_t>(Plan::words(a.pages.rows, a.n_groups)) * 4;
+nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
+  const size_t fixed = sizeof(LdsFixed) + (static_cast<size_t>(Plan::words(a.pages.rows, a.n_groups)) * 4 + 15) / 16 * 16;
+  a.ring = D == 256 ? (fixed + 3 * 128 * D <= kMaxLds ? 3 : 2) : 4;
+  const size_t lds = fixed + std::max<size_t>(sizeof(Join<D>), a.ring * 128 * D);
   if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<D>), hipFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(lds)) != hipSuccess)
     return NWC_ERR_HIP;
