@@ -197,29 +197,34 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
 // Work: an item is one key-value head's part of either a group's shared prefix
 // (columns: the group's rows times the query heads of that key-value head, in
 // blocks of at most kCap) or one row's own positions (columns: its query heads).
-// An item's positions count in units of 32; all units of all items in order,
-// heads outermost, are cut into equal ranges, one per workgroup, so the split
-// needs only the lengths, which every workgroup reads for itself.  An item cut
-// between workgroups, or a row with both kinds, leaves partial sums in the
-// workspace, which k_attend_join adds in the order of the positions.
+// An item's positions count in units of 32.  All units of all prefixes in
+// order, heads outermost, are cut into equal ranges, one per workgroup; so are
+// the units of all own positions, one range per wavefront (per workgroup when
+// a key-value head has more than 32 query heads).  The split needs only the
+// lengths, which every workgroup reads for itself, so a captured launch serves
+// any lengths.  An item cut between ranges, or a row with both kinds, leaves
+// partial sums in the workspace, which k_attend_join adds.
 //
-// A unit is taken by one wavefront, all in registers.  S^T = K Q^T on the
-// matrix cores, the keys straight from the page (lane: one position, 8
-// components); with the positions of the two 16-row tiles interleaved (tile t,
-// row m is position 8 (m / 4) + 4 t + m % 4) the result leaves each lane the 8
+// A unit is computed by one wavefront in registers.  S^T = K Q^T on the matrix
+// cores, the keys straight from the page (lane: one position, 8 components);
+// with the positions of the two 16-row tiles interleaved (tile t, row m is
+// position 8 (m / 4) + 4 t + m % 4) the result leaves each lane the 8
 // neighbouring positions 8 g .. 8 g + 7 of one column, g = lane / 16, which is
-// just the operand that O^T = V^T P^T takes.  The values come straight from the
-// page too: a lane reads D / 16 neighbouring components of its 8 positions and
-// turns that block by one byte permute per operand register.  No value crosses
-// lanes in the loop but the column's maximum, and that only when it grows.
+// just the operand that O^T = V^T P^T takes.  Of the values a lane takes D / 16
+// neighbouring components of its 8 positions and turns that block by one byte
+// permute per operand register.  No value crosses lanes in the loop but the
+// column's maximum, and that only when it grows by more than 2^8.
 
-constexpr uint32_t kCap = 128;  // columns of a block: 4 wavefronts of 2 16-column tiles
+constexpr uint32_t kCap = 128;        // columns of a prefix block: 4 wavefronts of 2 16-column tiles
+constexpr uint32_t kWaveRatio = 32;   // most query heads per key-value head that one wavefront takes
+constexpr int kAttendThreads = 256;
+constexpr float kNoMax = -1e30f;      // the maximum of nothing: finite, so that exp2(-inf - it) is 0
 
 template <int D>
 struct AttendShape {
-  static constexpr int kDt = D / 16;    // 16-row tiles of O^T = components of a lane
-  static constexpr int kKs = D / 32;    // steps of the K Q^T product
-  static constexpr int kJLd = D + 4;    // padded LDS rows (banks)
+  static constexpr int kDt = D / 16;   // 16-row tiles of O^T = components of a lane
+  static constexpr int kKs = D / 32;   // steps of the K Q^T product
+  static constexpr int kJLd = D + 4;   // padded LDS rows (banks)
 };
 
 struct AttendArgs {
@@ -229,30 +234,28 @@ struct AttendArgs {
   uint64_t ldq, ldo;
   PageArgs pages;
   uint32_t hq, hkv, ratio, n_groups;
-  float scale2;  // scale * log2(e)
-  float* part_o;  // workspace: partial sums [column slot][D]
-  float* part_ml; // their maxima (log2 domain) and weight sums
-  uint32_t* plan; // the plan for k_attend_join
-  uint32_t min_quota, ring;  // least units of a workgroup; slots of the ring
+  float scale2;             // scale * log2(e)
+  float* part_o;            // workspace: partial sums [column slot][D]
+  float* part_ml;           // their maxima (log2 domain) and weight sums
+  uint32_t* plan;           // the plan for k_attend_join
+  uint64_t own_slot;        // first column slot of the own positions' parts
+  uint32_t cap_p, cap_o;    // column slots of a worker's part: prefixes, own positions
+  uint32_t ring;            // slots of the ring in LDS
 };
 
-constexpr int kAttendThreads = 256;
-constexpr float kNoMax = -1e30f;  // the maximum of nothing: finite, so that exp2(-inf - it) is 0
-
-// Plan in LDS and (for the join) in the workspace: u32 words
-//   [0] units per head, [1], [3] units per workgroup (low, high word), [2] units of prefixes per head
+// Plan in LDS and (for the join) in the workspace, u32 words:
+//   head[8]             units per head of prefixes and of own positions; units per worker (two words each)
 //   row_pre[rows + 1]   units of own positions before the row
 //   row_base[rows]      first own position (the shared length where the row shares)
 //   row_end[rows]       its length, cut to what the table covers; -1 for padding
-//   row_group[rows]     its group, or count
-//   g_start[groups + 1], g_pre[groups + 1], g_units[groups], g_row[groups]
+//   row_group[rows]     its group, or the number of groups
+//   g_start[groups + 1], g_pre[groups + 1], g_units[groups] (of a column block), g_row[groups] (whose table row)
 struct Plan {
   uint32_t *head, *row_pre, *row_base, *row_end, *row_group, *g_start, *g_pre, *g_units, *g_row;
-  __host__ __device__ static uint32_t words(uint32_t rows, uint32_t groups) { return 4 + 4 * rows + 1 + 4 * groups + 2; }
-  __device__ uint64_t quota() const { return head[1] | static_cast<uint64_t>(head[3]) << 32; }
+  __host__ __device__ static uint32_t words(uint32_t rows, uint32_t groups) { return 8 + 4 * rows + 1 + 4 * groups + 2; }
   __device__ Plan(uint32_t* p, uint32_t rows, uint32_t groups) {
     head = p;
-    row_pre = head + 4;
+    row_pre = head + 8;
     row_base = row_pre + rows + 1;
     row_end = row_base + rows;
     row_group = row_end + rows;
@@ -261,6 +264,7 @@ struct Plan {
     g_units = g_pre + groups + 1;
     g_row = g_units + groups;
   }
+  __device__ uint64_t quota(int i) const { return head[2 + 2 * i] | static_cast<uint64_t>(head[3 + 2 * i]) << 32; }
 };
 
 // In-place inclusive scan (sum or maximum) of n words in LDS by the workgroup;
@@ -314,51 +318,104 @@ __device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t* carry) {
     const bool in = G && g < G && p.g_start[g] <= r;
     const uint32_t s = in ? p.g_units[g] : 0;
     const bool shares = s > 0 && len > 0 && end >= s;
+    const uint32_t base = shares ? s : 0;
     p.row_end[r] = len < 0 ? 0xFFFFFFFFu : end;
-    p.row_base[r] = shares ? s : 0;
+    p.row_base[r] = base;
     p.row_group[r] = shares ? g : G;
+    p.row_pre[r + 1] = len > 0 && end > base ? (end + 31) / 32 - base / 32 : 0;
     if (shares) atomicMin(&p.g_row[g], r);
   }
   __syncthreads();
-  const uint32_t blocks = (a.ratio + kCap - 1) / kCap;  // column blocks of one row
-  for (uint32_t r = tid; r < rows; r += kAttendThreads) {
-    const int32_t end = static_cast<int32_t>(p.row_end[r]);
-    const uint32_t base = p.row_base[r];
-    const uint32_t units = end > static_cast<int32_t>(base) ? (end + 31u) / 32 - base / 32 : 0;
-    p.row_pre[r + 1] = units * blocks;
-  }
   for (uint32_t i = tid; i < G; i += kAttendThreads) {
     const uint32_t cols = (p.g_start[i + 1] - p.g_start[i]) * a.ratio;
     const uint32_t units = p.g_row[i] < rows ? (p.g_units[i] + 31) / 32 : 0;
     p.g_pre[i + 1] = units * ((cols + kCap - 1) / kCap);
-    // the units of one column block; the length stays the row_base of the rows
-    p.g_units[i] = units;
+    p.g_units[i] = units;  // the length in positions is the row_base of the rows that share
   }
   if (tid == 0) p.row_pre[0] = p.g_pre[0] = 0;
   __syncthreads();
   block_scan<false>(p.row_pre + 1, rows, carry);
   if (G) block_scan<false>(p.g_pre + 1, G, carry);
   if (tid == 0) {
-    const uint32_t units = p.g_pre[G] + p.row_pre[rows];
-    const uint64_t total = static_cast<uint64_t>(units) * a.hkv;
-    const uint64_t quota = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint64_t>(a.min_quota));
-    p.head[0] = units;
-    p.head[1] = static_cast<uint32_t>(quota);
-    p.head[2] = p.g_pre[G];
-    p.head[3] = static_cast<uint32_t>(quota >> 32);
+    const uint32_t workers = gridDim.x * (a.ratio <= kWaveRatio ? 4 : 1);
+    p.head[0] = p.g_pre[G];
+    p.head[1] = p.row_pre[rows];
+    // at least four units, one per wavefront, for a workgroup's part of a prefix
+    const uint64_t qp = max((static_cast<uint64_t>(p.head[0]) * a.hkv + gridDim.x - 1) / gridDim.x, uint64_t{4});
+    const uint64_t qo = max((static_cast<uint64_t>(p.head[1]) * a.hkv + workers - 1) / workers, uint64_t{1});
+    p.head[2] = static_cast<uint32_t>(qp);
+    p.head[3] = static_cast<uint32_t>(qp >> 32);
+    p.head[4] = static_cast<uint32_t>(qo);
+    p.head[5] = static_cast<uint32_t>(qo >> 32);
+    p.head[6] = p.head[7] = 0;
   }
   __syncthreads();
 }
 
-// One workgroup's part of one item.
+// A worker's part of one item; all fields wave-uniform.
 struct Segment {
-  const int32_t* ids;  // the page table row
-  uint32_t head;       // key-value head
-  uint32_t row0;       // first row of the item's columns
-  uint32_t col0, cols; // columns: (row - row0) * ratio + query head of the key-value head
-  uint32_t u0, u1;     // units (position / 32)
-  uint32_t p0, p1;     // positions that the item sees
+  const int32_t* ids;   // the page table row
+  uint32_t head;        // key-value head
+  uint32_t row0;        // first row of the item's columns
+  uint32_t col0, cols;  // columns: (row - row0) * ratio + query head of the key-value head
+  uint32_t u0, u1;      // units (position / 32)
+  uint32_t p0, p1;      // positions that the item sees
+  bool direct;          // the whole of its row's positions: the output itself, no partial sums
+  uint64_t slot;        // first column slot of the partial sums
 };
+
+// Column slot of a worker's partial sums of an item: the columns of all items
+// before it, and a full part for each worker before this one.  Items and
+// workers that meet follow each other (either the item or the worker steps
+// on), so no two overlap.
+__device__ __forceinline__ uint64_t part_slot(const AttendArgs& a, bool prefix, uint32_t head, uint32_t row, uint32_t col0,
+                                              uint64_t worker) {
+  return (prefix ? 0 : a.own_slot) + (static_cast<uint64_t>(head) * a.pages.rows + row) * a.ratio + col0 +
+         worker * (prefix ? a.cap_p : a.cap_o);
+}
+
+// A wave-uniform read of an array that this grid does not write (scalar load).
+__device__ __forceinline__ int32_t sload(const int32_t* p, uint64_t i) {
+  typedef const __attribute__((address_space(4))) int32_t ci32;
+  return ((ci32*)(reinterpret_cast<uintptr_t>(p)))[i];
+}
+
+// The page of a position that starts 8 (or 16) positions of one page: its
+// element offset for a head, less the components.  A page that does not exist
+// reads page 0 and is not seen.
+struct PagePart {
+  uint64_t off;
+  bool known;
+};
+__device__ __forceinline__ PagePart page_part(const AttendArgs& a, const Segment& it, uint32_t pos, uint32_t d) {
+  const uint32_t at = pos >> a.pages.shift;
+  const int32_t id = at < a.pages.cols ? sload(it.ids, at) : -1;
+  PagePart p;
+  p.known = static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages;
+  p.off = (p.known ? static_cast<uint64_t>(id) : 0) * a.pages.page_stride +
+          ((static_cast<uint64_t>(it.head) << a.pages.shift) + (pos & ((1u << a.pages.shift) - 1))) * d;
+  return p;
+}
+
+// The queries of NT tiles of 16 columns from col on: lane (n, g) has column n,
+// components 32 k + 8 g .. of step k; zeros past the item's last column.
+template <int D, int NT>
+__device__ __forceinline__ void load_queries(const AttendArgs& a, const Segment& it, uint32_t col,
+                                             u32x4_t (&qf)[AttendShape<D>::kKs][NT]) {
+  const uint32_t n = __lane_id() % 16, g = __lane_id() / 16;
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    const uint32_t x = col + 16 * c + n;
+    const bool live = x < it.cols;
+    const uint32_t at = it.col0 + (live ? x : 0), row = it.row0 + at / a.ratio, h = it.head * a.ratio + at % a.ratio;
+    const uint16_t* p = a.q + row * a.ldq + static_cast<uint64_t>(h) * D + 8 * g;
+#pragma unroll
+    for (int k = 0; k < AttendShape<D>::kKs; ++k) {
+      qf[k][c] = u32x4_t{0, 0, 0, 0};
+      if (live) qf[k][c] = *reinterpret_cast<const u32x4_t*>(p + 32 * k);
+    }
+  }
+}
 
 // A wavefront's running sums for NT tiles of 16 columns: lane (n, g) holds column
 // n, components kDt (4 g + i) + t of O (tile t, i = 0 .. 3), the maximum of the
@@ -369,19 +426,37 @@ struct Sums {
   static constexpr int kDt = AttendShape<D>::kDt;
   f32x4_t o[kDt][NT];
   float m[NT], l[NT];
+
   __device__ Sums() {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      m[t] = kNoMax;
-      l[t] = 0.f;
+    for (int c = 0; c < NT; ++c) {
+      m[c] = kNoMax;
+      l[c] = 0.f;
 #pragma unroll
-      for (int d = 0; d < kDt; ++d) o[d][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int d = 0; d < kDt; ++d) o[d][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
   }
-  // Weights of one unit's scores (lane: positions 8 g .. 8 g + 7 of its column),
-  // rounded to BF16 as the matrix cores take them; their sum is of the unrounded
-  // ones.
-  __device__ __forceinline__ void weigh(const f32x4_t (&sc)[2][NT], float scale2, bf16x8_t (&pf)[NT]) {
+
+  // One unit: sc are its scores (lane: positions 8 g .. 8 g + 7 of its column,
+  // tile t the positions 4 t ..), vr[j] the lane's components of position 8 g +
+  // j, first its first position, good whether the lane's positions have a page.
+  __device__ __forceinline__ void take(f32x4_t (&sc)[2][NT], uint32_t (&vr)[8][kDt / 2], const Segment& it, uint32_t first,
+                                       bool good, float scale2) {
+    if (first < it.p0 || first + 32 > it.p1 || !__all(good)) {  // an edge of the item, or a page that is none
+      const uint32_t g = __lane_id() / 16;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t pos = first + 8 * g + j;
+        const bool seen = good && pos >= it.p0 && pos < it.p1;
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+          if (!seen) sc[j / 4][c][j % 4] = -INFINITY;
+        // a slot that is not seen may hold anything, and 0 times NaN is NaN
+#pragma unroll
+        for (int d = 0; d < kDt / 2; ++d)
+          if (!seen) vr[j][d] = 0;
+      }
+    }
     float mx[NT];
     bool grow = false;
 #pragma unroll
@@ -405,6 +480,7 @@ struct Sums {
         for (int d = 0; d < kDt; ++d) o[d][c] *= f;
       }
     }
+    bf16x8_t pf[NT];  // weights as the matrix cores take them, rounded to BF16; their sum is of the unrounded ones
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
       float p[8];
@@ -418,9 +494,6 @@ struct Sums {
       for (int j = 0; j < 4; ++j) w[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
       pf[c] = __builtin_bit_cast(bf16x8_t, w);
     }
-  }
-  // o += V^T P^T for one unit: vr[j] are the lane's components of position 8 g + j.
-  __device__ __forceinline__ void add(const uint32_t (&vr)[8][kDt / 2], const bf16x8_t (&pf)[NT]) {
 #pragma unroll
     for (int d = 0; d < kDt; ++d) {
       u32x4_t w;
@@ -432,6 +505,8 @@ struct Sums {
         o[d][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w), pf[c], o[d][c], 0, 0, 0);
     }
   }
+
+  // The columns' weight sums complete in all four lanes.
   __device__ __forceinline__ void finish() {
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
@@ -439,7 +514,107 @@ struct Sums {
       l[c] += lane_xor(l[c], 32);
     }
   }
+
+  // The wavefront's columns from col on, complete: outputs or partial sums.
+  __device__ __forceinline__ void store(const AttendArgs& a, const Segment& it, uint32_t col) const {
+    const uint32_t n = __lane_id() % 16, g = __lane_id() / 16;
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      const uint32_t cc = col + 16 * c + n;
+      if (cc >= it.cols) continue;
+      const float r = l[c] == 0.f ? 0.f : 1.f / l[c];
+      const uint32_t cl = it.col0 + cc, row = it.row0 + cl / a.ratio, h = it.head * a.ratio + cl % a.ratio;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t e = kDt * (4 * g + i);
+        static_assert(kDt % 2 == 0, "pairs");
+        if (it.direct) {
+          uint32_t w[kDt / 2];
+#pragma unroll
+          for (int d = 0; d < kDt; d += 2) w[d / 2] = pack_bf16(o[d][c][i] * r, o[d + 1][c][i] * r);
+          __builtin_memcpy(a.out + row * a.ldo + static_cast<uint64_t>(h) * D + e, w, 2 * kDt);
+        } else {
+          float x[kDt];
+#pragma unroll
+          for (int d = 0; d < kDt; ++d) x[d] = o[d][c][i];
+          __builtin_memcpy(a.part_o + (it.slot + cc) * D + e, x, 4 * kDt);
+        }
+      }
+      if (!it.direct && g == 0) {
+        a.part_ml[2 * (it.slot + cc)] = m[c];
+        a.part_ml[2 * (it.slot + cc) + 1] = l[c];
+      }
+    }
+  }
 };
+
+// One wavefront's loads of a unit and the two products.
+template <int D, int NT>
+struct Unit {
+  static constexpr int kDt = AttendShape<D>::kDt, kKs = AttendShape<D>::kKs;
+  u32x4_t kf[2][kKs];
+  uint32_t vr[8][kDt / 2];
+  __device__ __forceinline__ void load_k(const AttendArgs& a, const PagePart& lo, const PagePart& hi) {
+    const uint32_t n = __lane_id() % 16, g = __lane_id() / 16;
+    const uint16_t* p = a.k + (n < 8 ? lo.off : hi.off) + (n / 4 % 2 * 8 + n % 4) * D + 8 * g;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int k = 0; k < kKs; ++k) kf[t][k] = *reinterpret_cast<const u32x4_t*>(p + 4 * t * D + 32 * k);
+  }
+  __device__ __forceinline__ void load_v(const AttendArgs& a, const PagePart& lo, const PagePart& hi) {
+    const uint32_t n = __lane_id() % 16, g = __lane_id() / 16;
+    const uint16_t* p = a.v + (g < 2 ? lo.off : hi.off) + g % 2 * (8 * D) + kDt * n;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) __builtin_memcpy(vr[j], p + j * D, 2 * kDt);
+  }
+  __device__ __forceinline__ void scores(const u32x4_t (&qf)[kKs][NT], f32x4_t (&sc)[2][NT]) const {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < NT; ++c) sc[t][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kKs; ++k)
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          sc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kf[t][k]),
+                                                             __builtin_bit_cast(bf16x8_t, qf[k][c]), sc[t][c], 0, 0, 0);
+  }
+};
+
+// Units u, u + step, .. of a segment by one wavefront.  The page numbers of a
+// unit come by scalar loads one unit before its keys and values are asked for,
+// so that waiting for them waits for no vector load.
+template <int D, int NT>
+__device__ __forceinline__ void walk(const AttendArgs& a, const Segment& it, uint32_t u, uint32_t step, Sums<D, NT>& acc) {
+  if (u >= it.u1) return;
+  auto part = [&](uint32_t unit, uint32_t half) { return page_part(a, it, 32 * unit + 16 * half, D); };
+  const bool upper = __lane_id() / 16 >= 2;
+  u32x4_t qf[AttendShape<D>::kKs][NT];
+  Unit<D, NT> x;
+  PagePart lo = part(u, 0), hi = part(u, 1);
+  x.load_k(a, lo, hi);
+  x.load_v(a, lo, hi);
+  load_queries<D, NT>(a, it, 0, qf);
+  for (;;) {
+    const bool good = upper ? hi.known : lo.known;
+    const uint32_t next = u + step;
+    const bool more = next < it.u1;
+    if (more) {
+      lo = part(next, 0);
+      hi = part(next, 1);
+    }
+    f32x4_t sc[2][NT];
+    x.scores(qf, sc);
+    if (more) x.load_k(a, lo, hi);
+    acc.take(sc, x.vr, it, 32 * u, good, a.scale2);
+    if (!more) break;
+    x.load_v(a, lo, hi);
+    u = next;
+  }
+}
 
 // LDS of a workgroup: the fixed part, then the plan, then the ring of slots or
 // the sums that the wavefronts exchange (never both).
@@ -451,111 +626,17 @@ struct LdsFixed {
 template <int D>
 using Join = float[4][16][AttendShape<D>::kJLd];
 
-// The workgroup's part of an item of at most 16 NT columns: the wavefronts take
-// its units in turn.
+// A workgroup's part of an item of at most 16 NT columns: the wavefronts take its
+// units in turn, their sums are brought to one maximum and added in order.
 template <int D, int NT>
-__device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segment& it, LdsFixed& s, Join<D>& join, bool direct,
-                                               uint64_t slot) {
-  using S = AttendShape<D>;
-  constexpr int kDt = S::kDt, kKs = S::kKs;
-  const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave), tid = threadIdx.x;
-  const uint32_t n = lane % 16, g = lane / 16;
-  const uint32_t mask = (1u << a.pages.shift) - 1;
-  const uint64_t head_off = (static_cast<uint64_t>(it.head) << a.pages.shift) * D;
-  // this lane's key positions (tile 0) and block of 8 value positions in a unit
-  const uint32_t kpos = 8 * (n / 4) + n % 4, vpos = 8 * g;
-  auto page_of = [&](uint32_t pos) -> int32_t {
-    const uint32_t at = pos >> a.pages.shift;
-    return at < a.pages.cols ? it.ids[at] : -1;
-  };
-  auto known = [&](int32_t id) { return static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages; };
-  auto offset = [&](int32_t id, uint32_t pos) {
-    return (known(id) ? static_cast<uint64_t>(id) : 0) * a.pages.page_stride + head_off +
-           static_cast<uint64_t>(pos & mask) * D;
-  };
-  u32x4_t kf[2][kKs];
-  uint32_t vr[8][kDt / 2];
-  auto load_k = [&](int32_t id, uint32_t u) {
-    const uint16_t* p = a.k + offset(id, 32 * u + kpos) + 8 * g;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int k = 0; k < kKs; ++k) kf[t][k] = *reinterpret_cast<const u32x4_t*>(p + 4 * t * D + 32 * k);
-  };
-  auto load_v = [&](int32_t id, uint32_t u) {
-    const uint16_t* p = a.v + offset(id, 32 * u + vpos) + kDt * n;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) __builtin_memcpy(vr[j], p + j * D, 2 * kDt);
-  };
-
+__device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment& it, LdsFixed& s, Join<D>& join) {
+  constexpr int kDt = AttendShape<D>::kDt;
+  const uint32_t wave = uniform(threadIdx.x / kWave), tid = threadIdx.x;
+  const uint32_t n = __lane_id() % 16, g = __lane_id() / 16;
   Sums<D, NT> acc;
-
-  uint32_t u = it.u0 + wave;
-  if (u < it.u1) {
-    int32_t kid = page_of(32 * u + kpos), vid = page_of(32 * u + vpos);
-    // queries: this lane's column of each tile, 8 components a step; zeros past the last column
-    u32x4_t qf[kKs][NT];
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      const uint32_t col = 16 * c + n;
-      const bool live = col < it.cols;
-      const uint32_t at = it.col0 + (live ? col : 0), row = it.row0 + at / a.ratio, h = it.head * a.ratio + at % a.ratio;
-      const uint16_t* p = a.q + row * a.ldq + static_cast<uint64_t>(h) * D + 8 * g;
-#pragma unroll
-      for (int k = 0; k < kKs; ++k) {
-        qf[k][c] = u32x4_t{0, 0, 0, 0};
-        if (live) qf[k][c] = *reinterpret_cast<const u32x4_t*>(p + 32 * k);
-      }
-    }
-    load_k(kid, u);
-    for (;;) {
-      load_v(vid, u);
-      const bool good = known(vid);
-      const uint32_t next = u + 4;
-      const bool more = next < it.u1;
-      if (more) {
-        kid = page_of(32 * next + kpos);
-        vid = page_of(32 * next + vpos);
-      }
-      f32x4_t sc[2][NT];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int c = 0; c < NT; ++c) sc[t][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < kKs; ++k)
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            sc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kf[t][k]),
-                                                               __builtin_bit_cast(bf16x8_t, qf[k][c]), sc[t][c], 0, 0, 0);
-      if (more) load_k(kid, next);
-      const uint32_t first = 32 * u;
-      if (first < it.p0 || first + 32 > it.p1 || !__all(good)) {  // an edge of the item, or a page that is none
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t pos = first + vpos + j;
-          const bool seen = good && pos >= it.p0 && pos < it.p1;
-#pragma unroll
-          for (int c = 0; c < NT; ++c)
-            if (!seen) sc[j / 4][c][j % 4] = -INFINITY;
-          // a slot that is not seen may hold anything, and 0 times NaN is NaN
-#pragma unroll
-          for (int d = 0; d < kDt / 2; ++d)
-            if (!seen) vr[j][d] = 0;
-        }
-      }
-      bf16x8_t pf[NT];
-      acc.weigh(sc, a.scale2, pf);
-      acc.add(vr, pf);
-      if (!more) break;
-      u = next;
-    }
-  }
-
-  // the sums of wavefronts with the same columns, brought to one maximum and added in order
+  walk<D, NT>(a, it, it.u0 + wave, 4, acc);
   acc.finish();
+  __syncthreads();  // the exchange's last readers are done
   if (g == 0)
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
@@ -569,52 +650,36 @@ __device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segmen
 #pragma unroll
     for (int w = 0; w < 4; ++w) top = fmaxf(top, s.m[w][16 * c + n]);
     const float f = __builtin_amdgcn_exp2f(acc.m[c] - top);
+    if (c) __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float* dst = &join[wave][n][kDt * (4 * g + i)];  // O^T tile t, row 4 g + i: component kDt (4 g + i) + t
+      float* dst = &join[wave][n][kDt * (4 * g + i)];
 #pragma unroll
       for (int d = 0; d < kDt; ++d) dst[d] = acc.o[d][c][i] * f;
     }
     __syncthreads();
     for (uint32_t i = tid; i < 16 * (D / 4); i += kAttendThreads) {
       const uint32_t col = i / (D / 4), e = i % (D / 4) * 4, cc = 16 * c + col;
-      if (cc < it.cols) {
-        f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-        float total = 0.f, best = s.m[0][cc];
+      if (cc >= it.cols) continue;
+      f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+      float total = 0.f, best = s.m[0][cc];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) best = fmaxf(best, s.m[w][cc]);
+      for (int w = 1; w < 4; ++w) best = fmaxf(best, s.m[w][cc]);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          sum += *reinterpret_cast<const f32x4_t*>(&join[w][col][e]);
-          total += s.l[w][cc] * __builtin_amdgcn_exp2f(s.m[w][cc] - best);
-        }
-        if (direct) {
-          const float r = total == 0.f ? 0.f : 1.f / total;
-          const uint32_t cl = it.col0 + cc, row = it.row0 + cl / a.ratio, h = it.head * a.ratio + cl % a.ratio;
-          uint2 w;
-          w.x = pack_bf16(sum[0] * r, sum[1] * r);
-          w.y = pack_bf16(sum[2] * r, sum[3] * r);
-          *reinterpret_cast<uint2*>(a.out + row * a.ldo + static_cast<uint64_t>(h) * D + e) = w;
-        } else {
-          *reinterpret_cast<f32x4_t*>(a.part_o + (slot + cc) * D + e) = sum;
-          if (e == 0) {
-            a.part_ml[2 * (slot + cc)] = best;
-            a.part_ml[2 * (slot + cc) + 1] = total;
-          }
-        }
+      for (int w = 0; w < 4; ++w) {
+        sum += *reinterpret_cast<const f32x4_t*>(&join[w][col][e]);
+        total += s.l[w][cc] * __builtin_amdgcn_exp2f(s.m[w][cc] - best);
+      }
+      *reinterpret_cast<f32x4_t*>(a.part_o + (it.slot + cc) * D + e) = sum;
+      if (e == 0) {
+        a.part_ml[2 * (it.slot + cc)] = best;
+        a.part_ml[2 * (it.slot + cc) + 1] = total;
       }
     }
-    __syncthreads();
   }
 }
 
-// A wave-uniform read of an array that this grid does not write (scalar load).
-__device__ __forceinline__ int32_t sload(const int32_t* p, uint64_t i) {
-  typedef const __attribute__((address_space(4))) int32_t ci32;
-  return ((ci32*)(reinterpret_cast<uintptr_t>(p)))[i];
-}
-
-// Wait until at most n of this wavefront's vector memory operations are left
+// Wait until at most N of this wavefront's vector memory operations are left
 // and all its LDS operations are done, then for the other wavefronts.
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
@@ -648,52 +713,35 @@ __device__ __forceinline__ uint32_t key_piece(uint32_t row, uint32_t c) {
 // 16-byte pieces of a key row are permuted by the row, so that the 16 rows
 // that one operand read touches lie in 64 different banks.
 template <int D, int NT>
-__device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment& it, uint8_t* slots, uint32_t (&good)[4][4],
-                                              bool direct, uint64_t slot) {
+__device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment& it, uint8_t* slots, uint32_t (&good)[4][4]) {
   using S = AttendShape<D>;
   constexpr int kDt = S::kDt, kKs = S::kKs, kLoads = (D + 63) / 64;
-  constexpr uint32_t kPieces = D / 8, kSlotBytes = 128 * D;
   constexpr int kAlign = kDt % 8 == 0 ? 16 : kDt % 4 == 0 ? 8 : 4;
+  constexpr uint32_t kPieces = D / 8, kSlotBytes = 128 * D;
   const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave);
-  const uint32_t n = lane % 16, g = lane / 16;
-  const uint64_t head_off = (static_cast<uint64_t>(it.head) << a.pages.shift) * D;
-  const uint32_t mask = (1u << a.pages.shift) - 1, units = it.u1 - it.u0;
+  const uint32_t n = lane % 16, g = lane / 16, units = it.u1 - it.u0;
   auto issue = [&](uint32_t i, uint32_t at) {  // unit i of the segment into slot `at`
-    const uint32_t pos = 32 * (it.u0 + i) + 8 * wave, idx = pos >> a.pages.shift;
-    const int32_t id = idx < a.pages.cols ? sload(it.ids, idx) : -1;
-    const bool ok = static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages;
-    const uint64_t off = (ok ? static_cast<uint64_t>(id) : 0) * a.pages.page_stride + head_off + static_cast<uint64_t>(pos & mask) * D;
+    const PagePart p = page_part(a, it, 32 * (it.u0 + i) + 8 * wave, D);
     uint8_t* to = slots + at * kSlotBytes + wave * (16 * D);
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) {
       const uint32_t piece = 64 * x + lane, row = piece / kPieces, c = piece % kPieces;
       if (piece < 8 * kPieces) {  // D = 96: the second load is half a wavefront
-        __builtin_amdgcn_global_load_lds(a.k + off + row * D + 8 * key_piece<D, true>(8 * wave + row, c), to + 1024 * x, 16, 0, 0);
-        __builtin_amdgcn_global_load_lds(a.v + off + row * D + 8 * c, to + 64 * D + 1024 * x, 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(a.k + p.off + row * D + 8 * key_piece<D, true>(8 * wave + row, c), to + 1024 * x, 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(a.v + p.off + row * D + 8 * c, to + 64 * D + 1024 * x, 16, 0, 0);
       }
     }
-    if (lane == 0) good[at][wave] = ok;
+    if (lane == 0) good[at][wave] = p.known;
   };
 
-  __syncthreads();  // the slots' last readers are done
   u32x4_t qf[kKs][NT];
-#pragma unroll
-  for (int c = 0; c < NT; ++c) {
-    const uint32_t col = wave * (16 * NT) + 16 * c + n;
-    const bool live = col < it.cols;
-    const uint32_t at = it.col0 + (live ? col : 0), row = it.row0 + at / a.ratio, h = it.head * a.ratio + at % a.ratio;
-    const uint16_t* p = a.q + row * a.ldq + static_cast<uint64_t>(h) * D + 8 * g;
-#pragma unroll
-    for (int k = 0; k < kKs; ++k) {
-      qf[k][c] = u32x4_t{0, 0, 0, 0};
-      if (live) qf[k][c] = *reinterpret_cast<const u32x4_t*>(p + 32 * k);
-    }
-  }
-  // the queries have to be there before the first count of loads in flight
+  load_queries<D, NT>(a, it, wave * (16 * NT), qf);
+  // the queries have to be there before the loads in flight are counted
 #pragma unroll
   for (int c = 0; c < NT; ++c)
 #pragma unroll
     for (int k = 0; k < kKs; ++k) asm volatile("" : "+v"(qf[k][c]));
+  __syncthreads();  // the slots' last readers are done
   const uint32_t ahead = a.ring - 1;
   for (uint32_t i = 0; i < ahead && i < units; ++i) issue(i, i);
   Sums<D, NT> acc;
@@ -726,66 +774,14 @@ __device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment
       }
     uint32_t vr[8][kDt / 2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) __builtin_memcpy(vr[j], __builtin_assume_aligned(vs + 2 * ((8 * g + j) * D + kDt * n), kAlign), 2 * kDt);
-    const uint32_t first = 32 * (it.u0 + i);
-    const bool ok = good[at][g] != 0;
-    if (first < it.p0 || first + 32 > it.p1 || !__all(ok)) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t pos = first + 8 * g + j;
-        const bool seen = ok && pos >= it.p0 && pos < it.p1;
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-          if (!seen) sc[j / 4][c][j % 4] = -INFINITY;
-#pragma unroll
-        for (int d = 0; d < kDt / 2; ++d)
-          if (!seen) vr[j][d] = 0;
-      }
-    }
-    bf16x8_t pf[NT];
-    acc.weigh(sc, a.scale2, pf);
-    acc.add(vr, pf);
+    for (int j = 0; j < 8; ++j)
+      __builtin_memcpy(vr[j], __builtin_assume_aligned(vs + 2 * ((8 * g + j) * D + kDt * n), kAlign), 2 * kDt);
+    acc.take(sc, vr, it, 32 * (it.u0 + i), good[at][g] != 0, a.scale2);
     at = at == ahead ? 0 : at + 1;
     to = to == ahead ? 0 : to + 1;
   }
   acc.finish();
-#pragma unroll
-  for (int c = 0; c < NT; ++c) {
-    const uint32_t cc = wave * (16 * NT) + 16 * c + n;
-    if (cc >= it.cols) continue;
-    const float r = acc.l[c] == 0.f ? 0.f : 1.f / acc.l[c];
-    const uint32_t cl = it.col0 + cc, row = it.row0 + cl / a.ratio, h = it.head * a.ratio + cl % a.ratio;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t e = kDt * (4 * g + i);
-#pragma unroll
-      for (int d = 0; d < kDt; d += 4) {
-        const f32x4_t x = {acc.o[d][c][i], acc.o[d + 1][c][i], acc.o[d + 2][c][i], acc.o[d + 3][c][i]};
-        if (direct) {
-          uint2 w;
-          w.x = pack_bf16(x[0] * r, x[1] * r);
-          w.y = pack_bf16(x[2] * r, x[3] * r);
-          *reinterpret_cast<uint2*>(a.out + row * a.ldo + static_cast<uint64_t>(h) * D + e + d) = w;
-        } else {
-          *reinterpret_cast<f32x4_t*>(a.part_o + (slot + cc) * D + e + d) = x;
-        }
-      }
-    }
-    if (!direct && g == 0) {
-      a.part_ml[2 * (slot + cc)] = acc.m[c];
-      a.part_ml[2 * (slot + cc) + 1] = acc.l[c];
-    }
-  }
-}
-
-// Column slot of a workgroup's partial sums: columns of all items before the
-// item, and a full block for each workgroup before this one.  Items and
-// workgroups that meet follow each other (either the item or the workgroup
-// steps on), so no two overlap.
-__device__ __forceinline__ uint64_t part_slot(const AttendArgs& a, uint32_t head, bool prefix, uint32_t row, uint32_t col0,
-                                              uint64_t wg) {
-  const uint64_t cols = static_cast<uint64_t>(a.pages.rows) * a.ratio;
-  return (2 * head + (prefix ? 0 : 1)) * cols + static_cast<uint64_t>(row) * a.ratio + col0 + wg * kCap;
+  acc.store(a, it, wave * (16 * NT));
 }
 
 // Largest i in [0, n) with pre[i] <= x (pre ascending, pre[0] = 0).
@@ -796,6 +792,49 @@ __device__ __forceinline__ uint32_t find_last(const uint32_t* pre, uint32_t n, u
     if (pre[mid] <= x) lo = mid; else hi = mid;
   }
   return lo;
+}
+
+// The item of own positions that unit `rem` of a head belongs to, and the part
+// of it from there on, at most `left` units.
+__device__ __forceinline__ Segment own_segment(const AttendArgs& a, const Plan& p, uint32_t head, uint32_t rem, uint64_t left,
+                                               uint64_t worker) {
+  const uint32_t r = uniform(find_last(p.row_pre, a.pages.rows, rem));
+  const uint32_t done = rem - uniform(p.row_pre[r]);
+  Segment it;
+  it.head = head;
+  it.row0 = r;
+  it.col0 = 0;
+  it.cols = a.ratio;
+  it.ids = a.pages.ids + r * a.pages.ld;
+  it.p0 = uniform(p.row_base[r]);
+  it.p1 = uniform(p.row_end[r]);
+  const uint32_t first = it.p0 / 32, units = (it.p1 + 31) / 32 - first;
+  it.u0 = first + done;
+  it.u1 = it.u0 + static_cast<uint32_t>(min(static_cast<uint64_t>(units - done), left));
+  it.direct = it.p0 == 0 && it.u1 - it.u0 == units;
+  it.slot = part_slot(a, false, head, r, 0, worker);
+  return it;
+}
+
+// The same for prefixes.
+__device__ __forceinline__ Segment prefix_segment(const AttendArgs& a, const Plan& p, uint32_t head, uint32_t rem, uint64_t left,
+                                                  uint64_t worker) {
+  const uint32_t i = uniform(find_last(p.g_pre, a.n_groups, rem));
+  const uint32_t units = uniform(p.g_units[i]), in = rem - uniform(p.g_pre[i]), block = in / units, done = in - block * units;
+  const uint32_t r = uniform(p.g_row[i]);
+  Segment it;
+  it.head = head;
+  it.row0 = uniform(p.g_start[i]);
+  it.col0 = block * kCap;
+  it.cols = min((uniform(p.g_start[i + 1]) - it.row0) * a.ratio - it.col0, kCap);
+  it.ids = a.pages.ids + r * a.pages.ld;
+  it.p0 = 0;
+  it.p1 = uniform(p.row_base[r]);
+  it.u0 = done;
+  it.u1 = done + static_cast<uint32_t>(min(static_cast<uint64_t>(units - done), left));
+  it.direct = false;
+  it.slot = part_slot(a, true, head, it.row0, it.col0, worker);
+  return it;
 }
 
 template <int D>
@@ -809,63 +848,54 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
   make_plan(a, p, s.carry);
   if (blockIdx.x == 0)
     for (uint32_t i = threadIdx.x; i < Plan::words(rows, G); i += kAttendThreads) a.plan[i] = p.head[i];
-  const uint32_t units = p.head[0], prefix_units = p.head[2];
-  const uint64_t quota = p.quota();
-  // workgroups go round the 8 XCDs in turn: neighbours in the order of the
-  // units, which share a head's pages, on one XCD
-  const uint32_t per_xcd = gridDim.x / 8;
-  const uint64_t wg = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * per_xcd + blockIdx.x / 8;
-  uint64_t at = wg * quota;
-  const uint64_t total = static_cast<uint64_t>(units) * a.hkv, end = min(at + quota, total);
-  while (at < end) {
-    Segment it;
-    it.head = static_cast<uint32_t>(at / units);
-    const uint32_t rem = static_cast<uint32_t>(at % units);
-    const bool prefix = rem < prefix_units;
-    uint32_t done, n_units, first;  // units of the item before this range, all its units, its first unit's position / 32
-    uint32_t item_row;
-    if (prefix) {
-      const uint32_t i = find_last(p.g_pre, G, rem);
-      n_units = p.g_units[i];
-      const uint32_t in = rem - p.g_pre[i], block = in / n_units;
-      done = in - block * n_units;
-      first = 0;
-      item_row = p.g_start[i];
-      it.col0 = block * kCap;
-      it.cols = (p.g_start[i + 1] - item_row) * a.ratio - it.col0;
-      it.ids = a.pages.ids + p.g_row[i] * a.pages.ld;
-      it.p0 = 0;
-      it.p1 = p.row_base[p.g_row[i]];
-    } else {
-      const uint32_t own = rem - prefix_units, r = find_last(p.row_pre, rows, own);
-      const uint32_t base = p.row_base[r], stop = p.row_end[r];
-      first = base / 32;
-      n_units = (stop + 31) / 32 - first;
-      const uint32_t in = own - p.row_pre[r], block = in / n_units;
-      done = in - block * n_units;
-      item_row = r;
-      it.col0 = block * kCap;
-      it.cols = a.ratio - it.col0;
-      it.ids = a.pages.ids + r * a.pages.ld;
-      it.p0 = base;
-      it.p1 = stop;
+  const uint32_t prefix_units = uniform(p.head[0]), own_units = uniform(p.head[1]);
+  if (prefix_units) {
+    const uint64_t quota = uniform(p.head[2]) | static_cast<uint64_t>(uniform(p.head[3])) << 32;
+    const uint64_t total = static_cast<uint64_t>(prefix_units) * a.hkv;
+    // workgroups go round the 8 XCDs in turn: neighbours in the order of the
+    // units, which share a head's pages, on one XCD if all have work
+    const bool spread = gridDim.x % 8 || total < quota * (gridDim.x / 2);
+    const uint64_t wg = spread ? blockIdx.x : blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
+    const uint64_t end = min(wg * quota + quota, total);
+    for (uint64_t at = wg * quota; at < end;) {
+      const uint32_t head = static_cast<uint32_t>(at / prefix_units);
+      const Segment it = prefix_segment(a, p, head, static_cast<uint32_t>(at % prefix_units), end - at, wg);
+      if (it.cols <= 16)
+        attend_turns<D, 1>(a, it, s, join);
+      else if (D <= 128 && it.cols <= 32)
+        attend_turns<D, D <= 128 ? 2 : 1>(a, it, s, join);
+      else if (it.cols <= 64)
+        attend_shared<D, 1>(a, it, big, s.good);
+      else
+        attend_shared<D, 2>(a, it, big, s.good);
+      at += it.u1 - it.u0;
     }
-    it.row0 = item_row;
-    it.cols = min(it.cols, kCap);
-    const uint32_t take = static_cast<uint32_t>(min(static_cast<uint64_t>(n_units - done), end - at));
-    it.u0 = first + done;
-    it.u1 = it.u0 + take;
-    const bool direct = !prefix && it.p0 == 0 && take == n_units;
-    const uint64_t slot = part_slot(a, it.head, prefix, item_row, it.col0, wg);
-    if (it.cols <= 16)
-      attend_segment<D, 1>(a, it, s, join, direct, slot);
-    else if (D <= 128 && it.cols <= 32)
-      attend_segment<D, D <= 128 ? 2 : 1>(a, it, s, join, direct, slot);
-    else if (it.cols <= 64)
-      attend_shared<D, 1>(a, it, big, s.good, direct, slot);
-    else
-      attend_shared<D, 2>(a, it, big, s.good, direct, slot);
-    at += take;
+  }
+  if (own_units) {
+    const uint64_t quota = uniform(p.head[4]) | static_cast<uint64_t>(uniform(p.head[5])) << 32;
+    const uint64_t total = static_cast<uint64_t>(own_units) * a.hkv;
+    // from the last workgroup down, where there are prefixes for the first ones only
+    const uint32_t wg = gridDim.x - 1 - blockIdx.x;
+    const uint64_t worker = a.ratio <= kWaveRatio ? static_cast<uint64_t>(uniform(threadIdx.x / kWave)) * gridDim.x + wg : wg;
+    const uint64_t end = min(worker * quota + quota, total);
+    for (uint64_t at = worker * quota; at < end;) {
+      const uint32_t head = static_cast<uint32_t>(at / own_units);
+      const Segment it = own_segment(a, p, head, static_cast<uint32_t>(at % own_units), end - at, worker);
+      if (a.ratio <= 16) {
+        Sums<D, 1> acc;
+        walk<D, 1>(a, it, it.u0, 1, acc);
+        acc.finish();
+        acc.store(a, it, 0);
+      } else if (a.ratio <= kWaveRatio) {
+        Sums<D, 2> acc;
+        walk<D, 2>(a, it, it.u0, 1, acc);
+        acc.finish();
+        acc.store(a, it, 0);
+      } else {
+        attend_shared<D, 1>(a, it, big, s.good);
+      }
+      at += it.u1 - it.u0;
+    }
   }
 }
 
@@ -879,30 +909,28 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs
   __shared__ float ms[kLines], ls[kLines];
   const uint32_t rows = a.pages.rows, r = blockIdx.x / a.hq, h = blockIdx.x % a.hq, head = h / a.ratio, j = h % a.ratio;
   const Plan p(a.plan, rows, a.n_groups);
-  const uint32_t units = p.head[0], prefix_units = p.head[2];
-  const uint64_t quota = p.quota();
-  const uint32_t base = p.row_base[r], g = p.row_group[r], own_pre = p.row_pre[r];
-  const int32_t stop = static_cast<int32_t>(p.row_end[r]);
-  if (stop < 0) return;  // padding
-  const uint32_t own_units = stop > static_cast<int32_t>(base) ? (stop + 31u) / 32 - base / 32 : 0;
-  // the workgroup that has a unit (32-bit division where the numbers allow)
-  auto owner = [&](uint64_t x) -> uint32_t {
+  const uint32_t prefix_units = p.head[0], own_units = p.head[1];
+  const uint64_t quota_p = p.quota(0), quota_o = p.quota(1);
+  const uint32_t base = p.row_base[r], g = p.row_group[r], pre = p.row_pre[r], units = p.row_pre[r + 1] - pre;
+  if (static_cast<int32_t>(p.row_end[r]) < 0) return;  // padding
+  // the worker that has a unit (32-bit division where the numbers allow)
+  auto owner = [](uint64_t x, uint64_t quota) -> uint32_t {
     return static_cast<uint32_t>((x | quota) >> 32 ? x / quota : static_cast<uint32_t>(x) / static_cast<uint32_t>(quota));
   };
-  uint32_t w0 = 0, n0 = 0, w1 = 0, n1 = 0;  // first workgroup and number of parts: of the prefix, of the own positions
+  uint32_t n0 = 0, n1 = 0;  // parts of the prefix, of the own positions
   uint64_t slot0 = 0, slot1 = 0;
   if (base) {
     const uint32_t first_row = p.g_start[g], col = (r - first_row) * a.ratio + j, block = col / kCap, n = p.g_units[g];
-    const uint64_t first = static_cast<uint64_t>(units) * head + p.g_pre[g] + static_cast<uint64_t>(block) * n;
-    w0 = owner(first);
-    n0 = owner(first + n - 1) - w0 + 1;
-    slot0 = part_slot(a, head, true, first_row, block * kCap, w0) + col % kCap;
+    const uint64_t first = static_cast<uint64_t>(prefix_units) * head + p.g_pre[g] + static_cast<uint64_t>(block) * n;
+    const uint32_t w = owner(first, quota_p);
+    n0 = owner(first + n - 1, quota_p) - w + 1;
+    slot0 = part_slot(a, true, head, first_row, block * kCap, w) + col % kCap;
   }
-  if (own_units) {
-    const uint64_t first = static_cast<uint64_t>(units) * head + prefix_units + own_pre;
-    w1 = owner(first);
-    n1 = owner(first + own_units - 1) - w1 + 1;
-    slot1 = part_slot(a, head, false, r, 0, w1) + j;
+  if (units) {
+    const uint64_t first = static_cast<uint64_t>(own_units) * head + pre;
+    const uint32_t w = owner(first, quota_o);
+    n1 = owner(first + units - 1, quota_o) - w + 1;
+    slot1 = part_slot(a, false, head, r, 0, w) + j;
     if (!base && n1 == 1) return;  // k_attend wrote the output itself
   }
   const uint32_t line = threadIdx.x / kLine, e = threadIdx.x % kLine * 4, parts = n0 + n1;
@@ -911,7 +939,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs
   if (line < kLines) {
 #pragma unroll 4
     for (uint32_t i = line; i < parts; i += kLines) {
-      const uint64_t at = i < n0 ? slot0 + static_cast<uint64_t>(i) * kCap : slot1 + static_cast<uint64_t>(i - n0) * kCap;
+      const uint64_t at = i < n0 ? slot0 + static_cast<uint64_t>(i) * a.cap_p : slot1 + static_cast<uint64_t>(i - n0) * a.cap_o;
       const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
       const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part_o + at * D + e);
       const float top = fmaxf(best, ml.x), f = __builtin_amdgcn_exp2f(best - top), f2 = __builtin_amdgcn_exp2f(ml.x - top);
@@ -1046,12 +1074,17 @@ void set_rope(HeadsArgs* a, const nwc_rope* rope) {
 // Workspace of nwc_attend: partial sums, maxima and sums, the plan.
 constexpr uint32_t kAttendMaxRows = 4096, kAttendMaxGroups = 1024, kAttendMaxRatio = 64, kAttendMaxLen = 1u << 22;
 struct AttendLayout {
-  uint64_t ml, plan, bytes;
+  uint64_t own_slot, ml, plan, bytes;
+  uint32_t cap_p, cap_o;
 };
-AttendLayout attend_layout(uint32_t rows, uint32_t q_heads, uint32_t groups, uint32_t d, uint32_t grid) {
-  const uint64_t slots = 2 * static_cast<uint64_t>(rows) * q_heads + static_cast<uint64_t>(grid) * kCap;
-  auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
+AttendLayout attend_layout(uint32_t rows, uint32_t q_heads, uint32_t ratio, uint32_t groups, uint32_t d, uint32_t grid) {
   AttendLayout L;
+  const uint64_t cols = static_cast<uint64_t>(rows) * q_heads;
+  L.cap_p = groups ? std::min(kCap, rows * ratio) : 0;
+  L.cap_o = ratio;
+  L.own_slot = groups ? cols + static_cast<uint64_t>(grid) * L.cap_p : 0;
+  const uint64_t slots = L.own_slot + cols + static_cast<uint64_t>(grid) * (ratio <= kWaveRatio ? 4 : 1) * L.cap_o;
+  auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
   L.ml = up(slots * d * 4);
   L.plan = L.ml + up(slots * 8);
   L.bytes = L.plan + up(static_cast<uint64_t>(Plan::words(rows, groups)) * 4);
@@ -1147,7 +1180,7 @@ nwc_status nwc_attend_workspace_size(const nwc_cache* cache, uint32_t rows, uint
   if (!bytes) return NWC_ERR_INVALID_ARG;
   const nwc_status st = attend_shape(cache, rows, q_heads, n_groups);
   if (st) return st;
-  *bytes = attend_layout(rows, q_heads, n_groups, cache->head_dim, attend_grid(256, cache->head_dim)).bytes;
+  *bytes = attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, cache->head_dim, attend_grid(256, cache->head_dim)).bytes;
   return NWC_OK;
 }
 
@@ -1169,11 +1202,11 @@ nwc_status nwc_attend(const nwc_cache* cache, const nwc_page_table* table, const
   if (!aligned(q_dev, 16) || !aligned(out_dev, 16) || ldq % 8 || ldo % 8 || !aligned(lengths_dev, 4) || !aligned(ws, 256) ||
       (n_groups && (!aligned(groups->start, 4) || !aligned(groups->len, 4))))
     return NWC_ERR_ALIGNMENT;
-  if (ws_bytes < attend_layout(rows, q_heads, n_groups, d, attend_grid(256, d)).bytes) return NWC_ERR_BUFFER_TOO_SMALL;
+  if (ws_bytes < attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d, attend_grid(256, d)).bytes) return NWC_ERR_BUFFER_TOO_SMALL;
   const uint32_t cus = std::min(cu_count(), 256u);
   if (cus == 0) return NWC_ERR_HIP;
   const uint32_t grid = attend_grid(cus, d);
-  const AttendLayout L = attend_layout(rows, q_heads, n_groups, d, grid);
+  const AttendLayout L = attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d, grid);
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.k = cache->k;
   a.v = cache->v;
@@ -1194,7 +1227,9 @@ nwc_status nwc_attend(const nwc_cache* cache, const nwc_page_table* table, const
   a.part_o = reinterpret_cast<float*>(w);
   a.part_ml = reinterpret_cast<float*>(w + L.ml);
   a.plan = reinterpret_cast<uint32_t*>(w + L.plan);
-  a.min_quota = 1;
+  a.own_slot = L.own_slot;
+  a.cap_p = L.cap_p;
+  a.cap_o = L.cap_o;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (d) {
     case 64: return launch_attend<64>(a, grid, s);

@@ -353,6 +353,7 @@ def test_attend_any_group_numbers():
                           ([12, 12, 12], [5, 5]), ([-2 ** 31, 2 ** 31 - 1, 0], [128, 128])):
         _say("any group numbers %s %s" % (start, shared))
         b.groups = (_i32(start), _i32(shared))
+        b.ws = torch.empty(nwc.nwc_attend_workspace_size(b.cache, 12, 8, 2), dtype=torch.uint8, device="cuda")
         b.out.fill_(7.0)
         nwc.nwc_attend(b.call())
         torch.cuda.synchronize()
