@@ -26,6 +26,7 @@ typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(2))) float f32x2_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
 
 constexpr int kWave = 64;
@@ -380,18 +381,19 @@ __device__ __forceinline__ int32_t sload(const int32_t* p, uint64_t i) {
   return ((ci32*)(reinterpret_cast<uintptr_t>(p)))[i];
 }
 
-// The page of a position that starts 8 (or 16) positions of one page: its
-// element offset for a head, less the components.  A page that does not exist
-// reads page 0 and is not seen.
+// The page that holds a position (8 or 16 positions from it on share it), read
+// ahead of its use, and then that position's element offset for a head.  A page
+// that does not exist reads page 0 and is not seen.
+__device__ __forceinline__ int32_t page_id(const AttendArgs& a, const Segment& it, uint32_t pos) {
+  return sload(it.ids, min(pos >> a.pages.shift, a.pages.cols - 1));
+}
 struct PagePart {
   uint64_t off;
   bool known;
 };
-__device__ __forceinline__ PagePart page_part(const AttendArgs& a, const Segment& it, uint32_t pos, uint32_t d) {
-  const uint32_t at = pos >> a.pages.shift;
-  const int32_t id = at < a.pages.cols ? sload(it.ids, at) : -1;
+__device__ __forceinline__ PagePart page_part(const AttendArgs& a, const Segment& it, int32_t id, uint32_t pos, uint32_t d) {
   PagePart p;
-  p.known = static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages;
+  p.known = static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages && pos >> a.pages.shift < a.pages.cols;
   p.off = (p.known ? static_cast<uint64_t>(id) : 0) * a.pages.page_stride +
           ((static_cast<uint64_t>(it.head) << a.pages.shift) + (pos & ((1u << a.pages.shift) - 1))) * d;
   return p;
@@ -457,19 +459,26 @@ struct Sums {
           if (!seen) vr[j][d] = 0;
       }
     }
-    float mx[NT];
-    bool grow = false;
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      float x = fmaxf(fmaxf(sc[0][c][0], sc[0][c][1]), fmaxf(sc[0][c][2], sc[0][c][3]));
-      x = fmaxf(x, fmaxf(fmaxf(sc[1][c][0], sc[1][c][1]), fmaxf(sc[1][c][2], sc[1][c][3])));
-      mx[c] = x * scale2;
-      grow |= mx[c] > m[c] + 8.f;  // weights up to 2^8 lose nothing: BF16 and FP32 keep their relative precision
-    }
-    if (__any(grow)) {
+    // Weights relative to the maximum so far.  They may grow to 2^11 before the
+    // maximum moves (BF16 and FP32 keep their relative precision), so the common
+    // unit looks at no maximum at all: a lane's sum of 8 says whether one grew.
+    float p[NT][8], sum[NT];
+    auto weigh = [&] {
+      bool grown = false;
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
-        float x = mx[c];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[c][j] = __builtin_amdgcn_exp2f(fmaf(sc[j / 4][c][j % 4], scale2, -m[c]));
+        sum[c] = ((p[c][0] + p[c][1]) + (p[c][2] + p[c][3])) + ((p[c][4] + p[c][5]) + (p[c][6] + p[c][7]));
+        grown |= !(sum[c] <= 2048.f);
+      }
+      return grown;
+    };
+    if (__any(weigh())) {
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        float x = fmaxf(fmaxf(sc[0][c][0], sc[0][c][1]), fmaxf(sc[0][c][2], sc[0][c][3]));
+        x = fmaxf(x, fmaxf(fmaxf(sc[1][c][0], sc[1][c][1]), fmaxf(sc[1][c][2], sc[1][c][3]))) * scale2;
         x = fmaxf(x, lane_xor(x, 16));
         x = fmaxf(x, lane_xor(x, 32));
         x = fmaxf(x, m[c]);
@@ -479,19 +488,15 @@ struct Sums {
 #pragma unroll
         for (int d = 0; d < kDt; ++d) o[d][c] *= f;
       }
+      weigh();
     }
-    bf16x8_t pf[NT];  // weights as the matrix cores take them, rounded to BF16; their sum is of the unrounded ones
+    bf16x8_t pf[NT];  // as the matrix cores take them, rounded to BF16; their sum is of the unrounded ones
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
-      float p[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        p[j] = __builtin_amdgcn_exp2f(fmaf(sc[j / 4][c][j % 4], scale2, -m[c]));
-        l[c] += p[j];
-      }
+      l[c] += sum[c];
       u32x4_t w;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
+      for (int j = 0; j < 4; ++j) w[j] = pack_bf16(p[c][2 * j], p[c][2 * j + 1]);
       pf[c] = __builtin_bit_cast(bf16x8_t, w);
     }
 #pragma unroll
@@ -590,29 +595,35 @@ struct Unit {
 template <int D, int NT>
 __device__ __forceinline__ void walk(const AttendArgs& a, const Segment& it, uint32_t u, uint32_t step, Sums<D, NT>& acc) {
   if (u >= it.u1) return;
-  auto part = [&](uint32_t unit, uint32_t half) { return page_part(a, it, 32 * unit + 16 * half, D); };
   const bool upper = __lane_id() / 16 >= 2;
   u32x4_t qf[AttendShape<D>::kKs][NT];
   Unit<D, NT> x;
-  PagePart lo = part(u, 0), hi = part(u, 1);
+  int32_t id0 = page_id(a, it, 32 * u), id1 = page_id(a, it, 32 * u + 16);
+  PagePart lo = page_part(a, it, id0, 32 * u, D), hi = page_part(a, it, id1, 32 * u + 16, D);
   x.load_k(a, lo, hi);
   x.load_v(a, lo, hi);
   load_queries<D, NT>(a, it, 0, qf);
+  uint32_t next = u + step;
+  if (next < it.u1) {
+    id0 = page_id(a, it, 32 * next);
+    id1 = page_id(a, it, 32 * next + 16);
+  }
   for (;;) {
-    const bool good = upper ? hi.known : lo.known;
-    const uint32_t next = u + step;
-    const bool more = next < it.u1;
-    if (more) {
-      lo = part(next, 0);
-      hi = part(next, 1);
-    }
+    const bool good = upper ? hi.known : lo.known, more = next < it.u1;
     f32x4_t sc[2][NT];
     x.scores(qf, sc);
-    if (more) x.load_k(a, lo, hi);
+    if (more) {
+      lo = page_part(a, it, id0, 32 * next, D);
+      hi = page_part(a, it, id1, 32 * next + 16, D);
+      x.load_k(a, lo, hi);
+      id0 = page_id(a, it, 32 * (next + step));
+      id1 = page_id(a, it, 32 * (next + step) + 16);
+    }
     acc.take(sc, x.vr, it, 32 * u, good, a.scale2);
     if (!more) break;
     x.load_v(a, lo, hi);
     u = next;
+    next += step;
   }
 }
 
@@ -716,12 +727,12 @@ template <int D, int NT>
 __device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment& it, uint8_t* slots, uint32_t (&good)[4][4]) {
   using S = AttendShape<D>;
   constexpr int kDt = S::kDt, kKs = S::kKs, kLoads = (D + 63) / 64;
-  constexpr int kAlign = kDt % 8 == 0 ? 16 : kDt % 4 == 0 ? 8 : 4;
   constexpr uint32_t kPieces = D / 8, kSlotBytes = 128 * D;
   const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave);
   const uint32_t n = lane % 16, g = lane / 16, units = it.u1 - it.u0;
-  auto issue = [&](uint32_t i, uint32_t at) {  // unit i of the segment into slot `at`
-    const PagePart p = page_part(a, it, 32 * (it.u0 + i) + 8 * wave, D);
+  auto pos_of = [&](uint32_t i) { return 32 * (it.u0 + i) + 8 * wave; };  // this wavefront's rows of unit i
+  auto issue = [&](int32_t id, uint32_t i, uint32_t at) {                // unit i into slot `at`
+    const PagePart p = page_part(a, it, id, pos_of(i), D);
     uint8_t* to = slots + at * kSlotBytes + wave * (16 * D);
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) {
@@ -743,7 +754,8 @@ __device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment
     for (int k = 0; k < kKs; ++k) asm volatile("" : "+v"(qf[k][c]));
   __syncthreads();  // the slots' last readers are done
   const uint32_t ahead = a.ring - 1;
-  for (uint32_t i = 0; i < ahead && i < units; ++i) issue(i, i);
+  for (uint32_t i = 0; i < ahead && i < units; ++i) issue(page_id(a, it, pos_of(i)), i, i);
+  int32_t next = page_id(a, it, pos_of(ahead));  // page numbers come a unit ahead of the loads
   Sums<D, NT> acc;
   uint32_t at = 0, to = ahead;  // slots of unit i and of the unit loaded next
   for (uint32_t i = 0; i < units; ++i) {
@@ -754,29 +766,48 @@ __device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment
       wait_and_meet<2 * kLoads>();
     else
       wait_and_meet<4 * kLoads>();
-    if (i + ahead < units) issue(i + ahead, to);
+    const bool known = good[at][g] != 0;
+    if (i + ahead < units) issue(next, i + ahead, to);
+    next = page_id(a, it, pos_of(i + ahead + 1));
     const uint8_t* ks = slots + at * kSlotBytes;
     const uint8_t* vs = ks + 64 * D;
-    f32x4_t sc[2][NT];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int c = 0; c < NT; ++c) sc[t][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // all reads first: the products start as they arrive.  (Typed reads, never
+    // memcpy: a read that may alias the loads in flight makes the compiler wait
+    // for all of them.)
+    Unit<D, NT> x;
 #pragma unroll
     for (int k = 0; k < kKs; ++k)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const uint32_t row = 8 * (n / 4) + n % 4 + 4 * t;
-        const bf16x8_t kf = *reinterpret_cast<const bf16x8_t*>(ks + 16 * (row * kPieces + key_piece<D, false>(row, 4 * k + g)));
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-          sc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, __builtin_bit_cast(bf16x8_t, qf[k][c]), sc[t][c], 0, 0, 0);
+        x.kf[t][k] = *reinterpret_cast<const u32x4_t*>(ks + 16 * (row * kPieces + key_piece<D, false>(row, 4 * k + g)));
       }
-    uint32_t vr[8][kDt / 2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      __builtin_memcpy(vr[j], __builtin_assume_aligned(vs + 2 * ((8 * g + j) * D + kDt * n), kAlign), 2 * kDt);
-    acc.take(sc, vr, it, 32 * (it.u0 + i), good[at][g] != 0, a.scale2);
+    for (int j = 0; j < 8; ++j) {
+      const uint8_t* v = vs + 2 * ((8 * g + j) * D + kDt * n);
+      if constexpr (kDt % 8 == 0) {
+#pragma unroll
+        for (int e = 0; e < kDt / 8; ++e) {
+          const u32x4_t y = reinterpret_cast<const u32x4_t*>(v)[e];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x.vr[j][4 * e + q] = y[q];
+        }
+      } else if constexpr (kDt % 4 == 0) {
+#pragma unroll
+        for (int e = 0; e < kDt / 4; ++e) {
+          const u32x2_t y = reinterpret_cast<const u32x2_t*>(v)[e];
+          x.vr[j][2 * e] = y[0];
+          x.vr[j][2 * e + 1] = y[1];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kDt / 2; ++e) x.vr[j][e] = reinterpret_cast<const uint32_t*>(v)[e];
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4_t sc[2][NT];
+    x.scores(qf, sc);
+    acc.take(sc, x.vr, it, 32 * (it.u0 + i), known, a.scale2);
     at = at == ahead ? 0 : at + 1;
     to = to == ahead ? 0 : to + 1;
   }
