@@ -241,11 +241,13 @@ struct AttendArgs {
   uint32_t* plan;           // the plan for k_attend_join
   uint64_t own_slot;        // first column slot of the own positions' parts
   uint32_t cap_p, cap_o;    // column slots of a worker's part: prefixes, own positions
+  uint32_t own_wgs;         // workgroups for own positions, the last of the grid
   uint32_t ring;            // slots of the ring in LDS
 };
 
 // Plan in LDS and (for the join) in the workspace, u32 words:
-//   head[8]             units per head of prefixes and of own positions; units per worker (two words each)
+//   head[8]             units per head of prefixes and of own positions; units per worker (two words each);
+//                       workgroups that prefixes are cut for
 //   row_pre[rows + 1]   units of own positions before the row
 //   row_base[rows]      first own position (the shared length where the row shares)
 //   row_end[rows]       its length, cut to what the table covers; -1 for padding
@@ -338,17 +340,23 @@ __device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t* carry) {
   block_scan<false>(p.row_pre + 1, rows, carry);
   if (G) block_scan<false>(p.g_pre + 1, G, carry);
   if (tid == 0) {
-    const uint32_t workers = gridDim.x * (a.ratio <= kWaveRatio ? 4 : 1);
     p.head[0] = p.g_pre[G];
     p.head[1] = p.row_pre[rows];
-    // at least four units, one per wavefront, for a workgroup's part of a prefix
-    const uint64_t qp = max((static_cast<uint64_t>(p.head[0]) * a.hkv + gridDim.x - 1) / gridDim.x, uint64_t{4});
-    const uint64_t qo = max((static_cast<uint64_t>(p.head[1]) * a.hkv + workers - 1) / workers, uint64_t{1});
+    const uint64_t prefix = static_cast<uint64_t>(p.head[0]) * a.hkv, own = static_cast<uint64_t>(p.head[1]) * a.hkv;
+    // prefixes to the first half of the workgroups, own positions to the second
+    // (one of each per compute unit); all take part in the prefixes where there
+    // is little else.  At least four units, one per wavefront, for a
+    // workgroup's part of a prefix.
+    const uint32_t wp = own < prefix / 2 ? gridDim.x : gridDim.x - a.own_wgs;
+    const uint32_t wo = a.own_wgs * (a.ratio <= kWaveRatio ? 4 : 1);
+    const uint64_t qp = wp ? max((prefix + wp - 1) / wp, uint64_t{4}) : 4;
+    const uint64_t qo = max((own + wo - 1) / wo, uint64_t{1});
     p.head[2] = static_cast<uint32_t>(qp);
     p.head[3] = static_cast<uint32_t>(qp >> 32);
     p.head[4] = static_cast<uint32_t>(qo);
     p.head[5] = static_cast<uint32_t>(qo >> 32);
-    p.head[6] = p.head[7] = 0;
+    p.head[6] = wp;
+    p.head[7] = 0;
   }
   __syncthreads();
 }
@@ -589,41 +597,54 @@ struct Unit {
   }
 };
 
-// Units u, u + step, .. of a segment by one wavefront.  The page numbers of a
-// unit come by scalar loads one unit before its keys and values are asked for,
-// so that waiting for them waits for no vector load.
+// Units u, u + step, .. of a segment by one wavefront.  For 16 columns two units
+// are held in registers, so that one is in flight while the other is computed;
+// for 32, where the registers go to the sums, a unit's keys are asked for when
+// the keys before them are used up, and its values likewise.  Page numbers come
+// by scalar loads a unit before their use, so that waiting for them waits for
+// no vector load.
 template <int D, int NT>
 __device__ __forceinline__ void walk(const AttendArgs& a, const Segment& it, uint32_t u, uint32_t step, Sums<D, NT>& acc) {
   if (u >= it.u1) return;
+  constexpr int kBuf = NT == 1 ? 2 : 1;
   const bool upper = __lane_id() / 16 >= 2;
   u32x4_t qf[AttendShape<D>::kKs][NT];
-  Unit<D, NT> x;
+  Unit<D, NT> x[kBuf];
+  bool good[kBuf];
   int32_t id0 = page_id(a, it, 32 * u), id1 = page_id(a, it, 32 * u + 16);
-  PagePart lo = page_part(a, it, id0, 32 * u, D), hi = page_part(a, it, id1, 32 * u + 16, D);
-  x.load_k(a, lo, hi);
-  x.load_v(a, lo, hi);
-  load_queries<D, NT>(a, it, 0, qf);
-  uint32_t next = u + step;
-  if (next < it.u1) {
-    id0 = page_id(a, it, 32 * next);
-    id1 = page_id(a, it, 32 * next + 16);
-  }
-  for (;;) {
-    const bool good = upper ? hi.known : lo.known, more = next < it.u1;
-    f32x4_t sc[2][NT];
-    x.scores(qf, sc);
-    if (more) {
-      lo = page_part(a, it, id0, 32 * next, D);
-      hi = page_part(a, it, id1, 32 * next + 16, D);
-      x.load_k(a, lo, hi);
-      id0 = page_id(a, it, 32 * (next + step));
-      id1 = page_id(a, it, 32 * (next + step) + 16);
+  auto part = [&](uint32_t unit, PagePart& lo, PagePart& hi) {  // of the page numbers read last; then the next unit's
+    lo = page_part(a, it, id0, 32 * unit, D);
+    hi = page_part(a, it, id1, 32 * unit + 16, D);
+    id0 = page_id(a, it, 32 * (unit + step));
+    id1 = page_id(a, it, 32 * (unit + step) + 16);
+  };
+  PagePart lo, hi;
+#pragma unroll
+  for (int b = 0; b < kBuf; ++b)
+    if (b == 0 || u + step < it.u1) {
+      part(u + b * step, lo, hi);
+      x[b].load_k(a, lo, hi);
+      x[b].load_v(a, lo, hi);
+      good[b] = upper ? hi.known : lo.known;
     }
-    acc.take(sc, x.vr, it, 32 * u, good, a.scale2);
-    if (!more) break;
-    x.load_v(a, lo, hi);
-    u = next;
-    next += step;
+  load_queries<D, NT>(a, it, 0, qf);
+  for (;;) {
+#pragma unroll
+    for (int b = 0; b < kBuf; ++b) {
+      const uint32_t next = u + kBuf * step;
+      f32x4_t sc[2][NT];
+      x[b].scores(qf, sc);
+      const bool now = good[b], more = next < it.u1;
+      if (more) {
+        part(next, lo, hi);
+        x[b].load_k(a, lo, hi);
+        good[b] = upper ? hi.known : lo.known;
+      }
+      acc.take(sc, x[b].vr, it, 32 * u, now, a.scale2);
+      if (more) x[b].load_v(a, lo, hi);
+      u += step;
+      if (u >= it.u1) return;
+    }
   }
 }
 
@@ -885,8 +906,9 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
     const uint64_t total = static_cast<uint64_t>(prefix_units) * a.hkv;
     // workgroups go round the 8 XCDs in turn: neighbours in the order of the
     // units, which share a head's pages, on one XCD if all have work
-    const bool spread = gridDim.x % 8 || total < quota * (gridDim.x / 2);
-    const uint64_t wg = spread ? blockIdx.x : blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
+    const uint32_t wp = uniform(p.head[6]);
+    const bool near = wp % 8 == 0 && blockIdx.x < wp && total > quota * (wp / 2);
+    const uint64_t wg = near ? blockIdx.x % 8 * (wp / 8) + blockIdx.x / 8 : blockIdx.x;
     const uint64_t end = min(wg * quota + quota, total);
     for (uint64_t at = wg * quota; at < end;) {
       const uint32_t head = static_cast<uint32_t>(at / prefix_units);
@@ -905,9 +927,10 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
   if (own_units) {
     const uint64_t quota = uniform(p.head[4]) | static_cast<uint64_t>(uniform(p.head[5])) << 32;
     const uint64_t total = static_cast<uint64_t>(own_units) * a.hkv;
-    // from the last workgroup down, where there are prefixes for the first ones only
+    // from the last workgroup down
     const uint32_t wg = gridDim.x - 1 - blockIdx.x;
-    const uint64_t worker = a.ratio <= kWaveRatio ? static_cast<uint64_t>(uniform(threadIdx.x / kWave)) * gridDim.x + wg : wg;
+    if (wg >= a.own_wgs) return;
+    const uint64_t worker = a.ratio <= kWaveRatio ? static_cast<uint64_t>(uniform(threadIdx.x / kWave)) * a.own_wgs + wg : wg;
     const uint64_t end = min(worker * quota + quota, total);
     for (uint64_t at = worker * quota; at < end;) {
       const uint32_t head = static_cast<uint32_t>(at / own_units);
@@ -1108,13 +1131,13 @@ struct AttendLayout {
   uint64_t own_slot, ml, plan, bytes;
   uint32_t cap_p, cap_o;
 };
-AttendLayout attend_layout(uint32_t rows, uint32_t q_heads, uint32_t ratio, uint32_t groups, uint32_t d, uint32_t grid) {
+AttendLayout attend_layout(uint32_t rows, uint32_t q_heads, uint32_t ratio, uint32_t groups, uint32_t d, uint32_t cus) {
   AttendLayout L;
   const uint64_t cols = static_cast<uint64_t>(rows) * q_heads;
   L.cap_p = groups ? std::min(kCap, rows * ratio) : 0;
   L.cap_o = ratio;
-  L.own_slot = groups ? cols + static_cast<uint64_t>(grid) * L.cap_p : 0;
-  const uint64_t slots = L.own_slot + cols + static_cast<uint64_t>(grid) * (ratio <= kWaveRatio ? 4 : 1) * L.cap_o;
+  L.own_slot = groups ? cols + 2 * static_cast<uint64_t>(cus) * L.cap_p : 0;
+  const uint64_t slots = L.own_slot + cols + static_cast<uint64_t>(cus) * (ratio <= kWaveRatio ? 4 : 1) * L.cap_o;
   auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
   L.ml = up(slots * d * 4);
   L.plan = L.ml + up(slots * 8);
@@ -1132,7 +1155,7 @@ nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uin
   return NWC_OK;
 }
 
-uint32_t attend_grid(uint32_t cus, uint32_t d) { return cus * (d <= 128 ? 2 : 1); }
+
 
 template <int D>
 nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
@@ -1211,7 +1234,7 @@ nwc_status nwc_attend_workspace_size(const nwc_cache* cache, uint32_t rows, uint
   if (!bytes) return NWC_ERR_INVALID_ARG;
   const nwc_status st = attend_shape(cache, rows, q_heads, n_groups);
   if (st) return st;
-  *bytes = attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, cache->head_dim, attend_grid(256, cache->head_dim)).bytes;
+  *bytes = attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, cache->head_dim, 256).bytes;
   return NWC_OK;
 }
 
@@ -1233,11 +1256,11 @@ nwc_status nwc_attend(const nwc_cache* cache, const nwc_page_table* table, const
   if (!aligned(q_dev, 16) || !aligned(out_dev, 16) || ldq % 8 || ldo % 8 || !aligned(lengths_dev, 4) || !aligned(ws, 256) ||
       (n_groups && (!aligned(groups->start, 4) || !aligned(groups->len, 4))))
     return NWC_ERR_ALIGNMENT;
-  if (ws_bytes < attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d, attend_grid(256, d)).bytes) return NWC_ERR_BUFFER_TOO_SMALL;
+  if (ws_bytes < attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d, 256).bytes) return NWC_ERR_BUFFER_TOO_SMALL;
   const uint32_t cus = std::min(cu_count(), 256u);
   if (cus == 0) return NWC_ERR_HIP;
-  const uint32_t grid = attend_grid(cus, d);
-  const AttendLayout L = attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d, grid);
+  const uint32_t grid = n_groups ? 2 * cus : cus;
+  const AttendLayout L = attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d, cus);
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.k = cache->k;
   a.v = cache->v;
@@ -1259,6 +1282,7 @@ nwc_status nwc_attend(const nwc_cache* cache, const nwc_page_table* table, const
   a.part_ml = reinterpret_cast<float*>(w + L.ml);
   a.plan = reinterpret_cast<uint32_t*>(w + L.plan);
   a.own_slot = L.own_slot;
+  a.own_wgs = cus;
   a.cap_p = L.cap_p;
   a.cap_o = L.cap_o;
   const hipStream_t s = static_cast<hipStream_t>(stream);
