@@ -174,9 +174,16 @@ def _ptr_params(p):
     return ctypes.byref(p) if p is not None else None
 
 
+# the current stream's handle without building a Stream object (3 us of an 8 us
+# call); the public lookup where this torch does not have it
+_raw_stream = getattr(getattr(globals().get("torch"), "_C", None), "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
         import torch
+        if _raw_stream is not None:
+            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if hasattr(stream, "cuda_stream"):
         return ctypes.c_void_p(stream.cuda_stream)
