@@ -3,11 +3,9 @@
 // to a paged key-value cache, attention over that cache with shared prefixes
 // read once.
 //
-//  * k_heads: one wavefront per token and group of heads; a head is head_dim / 8
-//    lanes of 8 components.  The norm's sum runs over those lanes, the rotation
-//    takes its partner from another lane (halves) or the same one (pairs), and
-//    the result goes to a row or to a slot of a page.  Bound by HBM for long
-//    inputs, by one chain of dependent loads for a single token.
+//  * k_heads: a head is head_dim / 8 lanes of 8 components, both of a rotated
+//    pair in one lane.  The result goes to a row or to a slot of a page.  Bound
+//    by HBM for long inputs, by one chain of dependent loads for a single token.
 //  * k_attend: attention of all rows in one grid; see there.
 //  * k_attend_join: adds the partial results of rows whose positions several
 //    workgroups had.
@@ -17,6 +15,7 @@
 #include <cmath>
 #include <cstdint>
 #include <tuple>
+#include <type_traits>
 
 #include "nwc.h"
 
@@ -64,130 +63,154 @@ struct HeadsArgs {
   PageArgs pages;
   uint32_t hq, hk, hv;
   uint32_t tokens, d, half;  // half: dims / 2 (0: no rotation)
-  uint32_t style;
+  uint32_t style, split;     // split: wavefronts that share a token's passes
   float eps, inv_d;
 };
 
-// A wavefront takes U passes over one token's heads (queries, then keys, then
-// values), 64 / G heads a pass: lane c of a head's G lanes holds components
-// 8 c .. 8 c + 7 (idle if 8 c >= head_dim).  The angles of a token serve all
-// its passes: lane c turns the same components of every head.
+// Sum over the G lanes of a head, in each of them (DPP: swaps within four lanes,
+// then mirrors of 8 and 16 whose halves are equal by then).
+template <int G>
+__device__ __forceinline__ float head_sum(float v) {
+  auto dpp = [](float x, auto ctrl) {
+    const int y = __builtin_bit_cast(int, x);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, y, decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  v += dpp(v, std::integral_constant<int, 0xB1>{});   // quad_perm 1 0 3 2
+  v += dpp(v, std::integral_constant<int, 0x4E>{});   // quad_perm 2 3 0 1
+  v += dpp(v, std::integral_constant<int, 0x141>{});  // row_half_mirror
+  if (G >= 16) v += dpp(v, std::integral_constant<int, 0x140>{});  // row_mirror
+  if (G >= 32) v += lane_xor(v, 16);
+  return v;
+}
+
+// A pass takes 64 / G heads of one token (queries, then keys, then values), G
+// lanes each, of which head_dim / 8 hold two pieces of 4 components, a and b.
+// With halves a lane turns the pairs (a_j, b_j) of components 4 c + j and half +
+// 4 c + j, with pairs (a_0, a_1), (a_2, a_3), .. of 8 neighbouring ones; the
+// components past `dims` go to the lanes after. So a pair never leaves its lane,
+// a lane needs 4 angles, and those serve all heads of the token. A wavefront
+// takes U passes at a time, their loads together; `split` wavefronts share a
+// token, so that few tokens still fill the GPU.
+// 16384 tokens of 32 + 8 heads of 128 (336 MB): see the measurements at
+// launch_heads.
 template <int G, int U>
 __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
   constexpr uint32_t kHeads = kWave / G;  // heads of a pass
   const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave);
   const uint32_t all = a.hq + a.hk + a.hv;
-  const uint32_t per_token = (all + kHeads * U - 1) / (kHeads * U);
-  const uint64_t n = static_cast<uint64_t>(a.tokens) * per_token;
+  const uint64_t n = static_cast<uint64_t>(a.tokens) * a.split;
   const uint32_t c = lane % G, sub = lane / G;
   const bool on = 8 * c < a.d;
-  // the rotation's components of this lane: angles 8 c' .. (halves: c' = c or c
-  // less the lanes of the first half) or 4 c .. (pairs, each twice)
-  const uint32_t hl = a.half / 8;  // lanes of a half
-  const bool turned = on && 8 * c < 2 * a.half;
   const bool pairs = a.style == NWC_ROPE_PAIRS;
+  const bool turned = 8 * c < 2 * a.half;
+  const uint32_t at_a = turned && !pairs ? 4 * c : 8 * c, at_b = turned && !pairs ? a.half + 4 * c : 8 * c + 4;
+  float freq[4] = {0.f, 0.f, 0.f, 0.f};
+  if (turned)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) freq[j] = a.freqs[4 * c + j];
   for (uint64_t w = static_cast<uint64_t>(blockIdx.x) * 4 + wave; w < n; w += static_cast<uint64_t>(gridDim.x) * 4) {
-    const uint32_t t = static_cast<uint32_t>(w / per_token), part = static_cast<uint32_t>(w % per_token);
+    const uint32_t t = static_cast<uint32_t>(w / a.split);
     const int32_t pos = a.positions[t];
-    if (pos < 0) continue;  // a padding token
-    u32x4_t raw[U], wt[U];
-    uint32_t head[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      head[u] = (part * U + u) * kHeads + sub;
-      const bool live = on && head[u] < all;
-      const bool is_q = head[u] < a.hq, is_k = !is_q && head[u] < a.hq + a.hk;
-      const uint16_t* src = is_q ? a.q + t * a.ld_q + static_cast<uint64_t>(head[u]) * a.d
-                            : is_k ? a.k + t * a.ld_k + static_cast<uint64_t>(head[u] - a.hq) * a.d
-                                   : a.v + t * a.ld_v + static_cast<uint64_t>(head[u] - a.hq - a.hk) * a.d;
-      const uint16_t* wsrc = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
-      raw[u] = u32x4_t{0, 0, 0, 0};
-      wt[u] = raw[u];
-      if (live) raw[u] = *reinterpret_cast<const u32x4_t*>(src + 8 * c);
-      if (live && wsrc) wt[u] = *reinterpret_cast<const u32x4_t*>(wsrc + 8 * c);
-    }
-    // angles in turns, reduced in FP64: position (31 bits) times frequency (24
-    // bits) is exact to 2^-53 of its size, so after the whole turns are gone at
-    // most 2^31 / (2 pi) 2^-52, 8e-8 turns, is lost
-    float cs[8], sn[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      cs[j] = 1.f;
-      sn[j] = 0.f;
-    }
-    if (turned) {
-      const uint32_t first = pairs ? 4 * c : 8 * (c < hl ? c : c - hl);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const double turns = static_cast<double>(pos) * (static_cast<double>(a.freqs[first + (pairs ? j / 2 : j)]) *
-                                                         0.15915494309189533577);
-        const float r = static_cast<float>(turns - __builtin_rint(turns));
-        cs[j] = __builtin_amdgcn_cosf(r);  // the hardware's sine and cosine take turns
-        const float s = __builtin_amdgcn_sinf(r);
-        sn[j] = (pairs ? j % 2 == 0 : c < hl) ? -s : s;
-      }
-    }
+    const uint32_t row = a.rows ? static_cast<uint32_t>(a.rows[t]) : t;
+    float cs[4], sn[4];
     uint64_t slot = 0;  // element offset of the token's slot, less the head's part
     bool stored = true;
-    if (a.pages.ids) {
-      const uint32_t row = a.rows ? static_cast<uint32_t>(a.rows[t]) : t;
-      const uint32_t at = static_cast<uint32_t>(pos) >> a.pages.shift;
-      stored = row < a.pages.rows && at < a.pages.cols;
-      const int32_t id = stored ? a.pages.ids[row * a.pages.ld + at] : -1;
-      stored = static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages;
-      if (stored)
-        slot = id * a.pages.page_stride +
-               static_cast<uint64_t>(static_cast<uint32_t>(pos) & ((1u << a.pages.shift) - 1)) * a.d;
-    }
+    bool first = true;
+    for (uint32_t part = static_cast<uint32_t>(w % a.split); part * U * kHeads < all; part += a.split) {
+      u32x2_t xa[U], xb[U], wa[U], wb[U];
+      uint32_t head[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool is_q = head[u] < a.hq, is_k = !is_q && head[u] < a.hq + a.hk;
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[2 * j] = bf16_lo(raw[u][j]);
-        y[2 * j + 1] = bf16_hi(raw[u][j]);
+      for (int u = 0; u < U; ++u) {
+        head[u] = (part * U + u) * kHeads + sub;
+        const bool live = on && head[u] < all;
+        const bool is_q = head[u] < a.hq, is_k = !is_q && head[u] < a.hq + a.hk;
+        const uint16_t* src = is_q ? a.q + t * a.ld_q + static_cast<uint64_t>(head[u]) * a.d
+                              : is_k ? a.k + t * a.ld_k + static_cast<uint64_t>(head[u] - a.hq) * a.d
+                                     : a.v + t * a.ld_v + static_cast<uint64_t>(head[u] - a.hq - a.hk) * a.d;
+        const uint16_t* wsrc = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
+        xa[u] = xb[u] = wa[u] = wb[u] = u32x2_t{0, 0};
+        if (live) {
+          xa[u] = *reinterpret_cast<const u32x2_t*>(src + at_a);
+          xb[u] = *reinterpret_cast<const u32x2_t*>(src + at_b);
+        }
+        if (live && wsrc) {
+          wa[u] = *reinterpret_cast<const u32x2_t*>(wsrc + at_a);
+          wb[u] = *reinterpret_cast<const u32x2_t*>(wsrc + at_b);
+        }
       }
-      if (is_q ? a.q_weight != nullptr : is_k && a.k_weight != nullptr) {
+      if (first) {
+        first = false;
+        if (pos < 0) break;  // a padding token
+        // angles in turns, reduced in FP64: position (31 bits) times frequency
+        // (24 bits) is exact to 2^-53 of its size, so after the whole turns are
+        // gone at most 2^31 / (2 pi) 2^-52, 8e-8 turns, is lost
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const double turns = static_cast<double>(pos) * (static_cast<double>(freq[j]) * 0.15915494309189533577);
+          const float r = static_cast<float>(turns - __builtin_rint(turns));
+          cs[j] = __builtin_amdgcn_cosf(r);  // the hardware's sine and cosine take turns
+          sn[j] = __builtin_amdgcn_sinf(r);
+        }
+        if (a.pages.ids) {
+          const uint32_t at = static_cast<uint32_t>(pos) >> a.pages.shift;
+          stored = row < a.pages.rows && at < a.pages.cols;
+          const int32_t id = stored ? a.pages.ids[row * a.pages.ld + at] : -1;
+          stored = static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages;
+          if (stored)
+            slot = id * a.pages.page_stride +
+                   static_cast<uint64_t>(static_cast<uint32_t>(pos) & ((1u << a.pages.shift) - 1)) * a.d;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool is_q = head[u] < a.hq, is_k = !is_q && head[u] < a.hq + a.hk;
+        float y[8] = {bf16_lo(xa[u][0]), bf16_hi(xa[u][0]), bf16_lo(xa[u][1]), bf16_hi(xa[u][1]),
+                      bf16_lo(xb[u][0]), bf16_hi(xb[u][0]), bf16_lo(xb[u][1]), bf16_hi(xb[u][1])};
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
+        sum = head_sum<G>(sum);
+        if (is_q ? a.q_weight != nullptr : is_k && a.k_weight != nullptr) {
+          const float r = 1.f / sqrtf(fmaf(sum, a.inv_d, a.eps));
+          const float g[8] = {bf16_lo(wa[u][0]), bf16_hi(wa[u][0]), bf16_lo(wa[u][1]), bf16_hi(wa[u][1]),
+                              bf16_lo(wb[u][0]), bf16_hi(wb[u][0]), bf16_lo(wb[u][1]), bf16_hi(wb[u][1])};
 #pragma unroll
-        for (int m = 1; m < G; m *= 2) sum += lane_xor(sum, m);
-        const float r = 1.f / sqrtf(fmaf(sum, a.inv_d, a.eps));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[2 * j] *= r * bf16_lo(wt[u][j]);
-          y[2 * j + 1] *= r * bf16_hi(wt[u][j]);
+          for (int j = 0; j < 8; ++j) y[j] *= r * g[j];
         }
-      }
-      float z[8];
-      if (a.half) {  // the partner of every component (uniform branch: all lanes take part)
-        const int from = static_cast<int>(!turned || pairs ? lane : c < hl ? lane + hl : lane - hl);
+        if (turned) {
+          float z[8];
+          if (pairs) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float other = pairs ? y[j ^ 1]
-                                    : __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(
-                                                                    4 * from, __builtin_bit_cast(int, y[j])));
-          z[j] = turned ? fmaf(y[j], cs[j], other * sn[j]) : y[j];
+            for (int j = 0; j < 4; ++j) {
+              z[2 * j] = fmaf(y[2 * j], cs[j], -y[2 * j + 1] * sn[j]);
+              z[2 * j + 1] = fmaf(y[2 * j + 1], cs[j], y[2 * j] * sn[j]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              z[j] = fmaf(y[j], cs[j], -y[j + 4] * sn[j]);
+              z[j + 4] = fmaf(y[j + 4], cs[j], y[j] * sn[j]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = z[j];
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = y[j];
-      }
-      u32x4_t res;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) res[j] = pack_bf16(z[2 * j], z[2 * j + 1]);
-      if (!is_q && !is_k) res = raw[u];  // values as they are
-      if (!on || head[u] >= all) continue;
-      if (is_q) {
-        *reinterpret_cast<u32x4_t*>(a.q_out + t * a.ld_q_out + static_cast<uint64_t>(head[u]) * a.d + 8 * c) = res;
-      } else {
-        const uint32_t h = is_k ? head[u] - a.hq : head[u] - a.hq - a.hk;
-        uint16_t* dst = is_k ? a.k_out : a.v_out;
-        dst += a.pages.ids ? slot + (static_cast<uint64_t>(h) << a.pages.shift) * a.d
-                           : t * a.ld_k_out + static_cast<uint64_t>(h) * a.d;
-        if (stored) *reinterpret_cast<u32x4_t*>(dst + 8 * c) = res;
+        u32x2_t ra = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])}, rb = {pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
+        if (!is_q && !is_k) {  // values as they are
+          ra = xa[u];
+          rb = xb[u];
+        }
+        if (!on || head[u] >= all || !(is_q || stored)) continue;
+        uint16_t* dst;
+        if (is_q) {
+          dst = a.q_out + t * a.ld_q_out + static_cast<uint64_t>(head[u]) * a.d;
+        } else {
+          const uint32_t h = is_k ? head[u] - a.hq : head[u] - a.hq - a.hk;
+          dst = (is_k ? a.k_out : a.v_out) + (a.pages.ids ? slot + (static_cast<uint64_t>(h) << a.pages.shift) * a.d
+                                                          : t * a.ld_k_out + static_cast<uint64_t>(h) * a.d);
+        }
+        *reinterpret_cast<u32x2_t*>(dst + at_a) = ra;
+        *reinterpret_cast<u32x2_t*>(dst + at_b) = rb;
       }
     }
   }
@@ -1061,7 +1084,7 @@ constexpr uint64_t kMaxStride = uint64_t{1} << 40;
 nwc_status check_rope(const nwc_rope* rope, uint32_t d) {
   if (!rope || rope->dims == 0) return NWC_OK;
   if (!rope->freqs || rope->dims > d || rope->style > NWC_ROPE_PAIRS) return NWC_ERR_INVALID_ARG;
-  if (rope->dims % 16) return NWC_ERR_UNSUPPORTED;
+  if (rope->dims % 8) return NWC_ERR_UNSUPPORTED;
   return aligned(rope->freqs, 4) ? NWC_OK : NWC_ERR_ALIGNMENT;
 }
 
@@ -1105,9 +1128,13 @@ nwc_status launch_heads(HeadsArgs& a, hipStream_t s) {
   if (cus == 0) return NWC_ERR_HIP;
   const uint32_t g = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
   const uint32_t passes = (all + kWave / g - 1) / (kWave / g);
-  // one pass per wavefront while that leaves compute units idle, else four
-  const bool few = static_cast<uint64_t>(a.tokens) * passes < static_cast<uint64_t>(cus) * 16;
-  const uint64_t waves = static_cast<uint64_t>(a.tokens) * (few ? passes : (passes + 3) / 4);
+  // one pass per wavefront while that leaves compute units idle, else four at a
+  // time, a token's passes over as many wavefronts as it takes to have 16 per
+  // compute unit
+  const uint32_t want = cus * 16;
+  const bool few = static_cast<uint64_t>(a.tokens) * passes < want;
+  a.split = few ? passes : std::min((passes + 3) / 4, std::max(1u, want / a.tokens));
+  const uint64_t waves = static_cast<uint64_t>(a.tokens) * a.split;
   const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>((waves + 3) / 4, uint64_t{1} << 24));
   auto go = [&](auto one, auto four) { return launch(few ? one : four, dim3(grid), dim3(256), 0, s, a); };
   if (g == 8) return go(k_heads<8, 1>, k_heads<8, 4>);

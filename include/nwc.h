@@ -378,7 +378,7 @@ typedef struct {
  * position * freqs[i] radians (freqs: device, dims / 2 floats, 4-byte
  * aligned; the product and its reduction to one turn in FP64, so far
  * positions keep their angle).  style NWC_ROPE_HALF: pair i is (i, i + dims
- * / 2); NWC_ROPE_PAIRS: (2 i, 2 i + 1).  dims a multiple of 16, at most
+ * / 2); NWC_ROPE_PAIRS: (2 i, 2 i + 1).  dims a multiple of 8, at most
  * head_dim; 0 (freqs may be NULL): no rotation. */
 typedef enum { NWC_ROPE_HALF = 0, NWC_ROPE_PAIRS = 1 } nwc_rope_style;
 typedef struct {

@@ -57,7 +57,7 @@ def test_norm_rope_refusals():
         assert _norm_rope(_heads(**bad)) == want, bad
         assert _norm_rope(None, _heads(**bad)) == want, bad
     for bad, want in ((dict(freqs=None), nwc.NWC_ERR_INVALID_ARG), (dict(dims=144), nwc.NWC_ERR_INVALID_ARG),
-                      (dict(style=2), nwc.NWC_ERR_INVALID_ARG), (dict(dims=24), nwc.NWC_ERR_UNSUPPORTED),
+                      (dict(style=2), nwc.NWC_ERR_INVALID_ARG), (dict(dims=20), nwc.NWC_ERR_UNSUPPORTED),
                       (dict(dims=1), nwc.NWC_ERR_UNSUPPORTED), (dict(freqs=A + 2), nwc.NWC_ERR_ALIGNMENT)):
         assert _norm_rope(q, rope=_rope(**bad)) == want, bad
 
@@ -95,7 +95,7 @@ def test_append_refusals():
     assert _append(rows=A + 2) == nwc.NWC_ERR_ALIGNMENT
     assert _append(k=_heads(heads=4)) == nwc.NWC_ERR_INVALID_ARG                       # the cache has 8 heads
     assert _append(q=_heads(dst=None)) == nwc.NWC_ERR_INVALID_ARG
-    assert _append(rope=_rope(dims=24)) == nwc.NWC_ERR_UNSUPPORTED
+    assert _append(rope=_rope(dims=20)) == nwc.NWC_ERR_UNSUPPORTED
     assert _append(cache=_cache(head_dim=0)) == nwc.NWC_ERR_INVALID_ARG
     assert _append(cache=_cache(head_dim=100)) == nwc.NWC_ERR_UNSUPPORTED
     for bad, want in CACHE_BAD:

@@ -67,7 +67,8 @@ HEAD_CASES = [  # tokens, q heads, k heads, head_dim, dims, style, norm
     (7, 5, 2, 64, 32, "half", True), (33, 28, 4, 128, 64, "pairs", True), (3, 20, 4, 96, 96, "half", False),
     (130, 2, 1, 40, 32, "half", True), (11, 10, 5, 192, 96, "pairs", True), (2, 8, 2, 256, 256, "half", True),
     (9, 0, 7, 80, 80, "half", True), (1000, 32, 8, 128, 128, "half", True), (601, 16, 1, 112, 48, "half", True),
-    (1024, 7, 3, 248, 16, "pairs", False), (4, 3, 3, 72, 0, "pairs", False)]
+    (1024, 7, 3, 248, 16, "pairs", False), (4, 3, 3, 72, 0, "pairs", False), (6, 4, 2, 128, 24, "half", True),
+    (300, 5, 5, 64, 8, "half", False), (70, 9, 1, 200, 200, "half", True), (5000, 9, 3, 64, 40, "pairs", True)]
 
 
 @pytest.mark.parametrize("case", HEAD_CASES, ids=lambda c: "-".join(map(str, c)))
