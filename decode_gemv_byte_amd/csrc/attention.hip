@@ -268,45 +268,60 @@ struct AttendArgs {
   uint32_t ring;            // slots of the ring in LDS
 };
 
-// Plan in LDS and (for the join) in the workspace, u32 words:
+// The split of a call, made in LDS by every workgroup, u32 words:
 //   head[8]             units per head of prefixes and of own positions; units per worker (two words each);
 //                       workgroups that prefixes are cut for
 //   row_pre[rows + 1]   units of own positions before the row
-//   row_base[rows]      first own position (the shared length where the row shares)
 //   row_end[rows]       its length, cut to what the table covers; -1 for padding
-//   row_group[rows]     its group, or the number of groups
-//   g_start[groups + 1], g_pre[groups + 1], g_units[groups] (of a column block), g_row[groups] (whose table row)
+//   row_group[rows]     the group whose prefix it shares, or the number of groups
+//   g_start[groups + 1], g_pre[groups + 1] (units before the group), g_len[groups + 1] (positions; 0 for no group),
+//   g_row[groups] (whose table row is read)
+// and for k_attend_join in the workspace, four words each: the head, then per
+// row {row_pre, units, group, length}, then per group {start, pre, len, 0}.
 struct Plan {
-  uint32_t *head, *row_pre, *row_base, *row_end, *row_group, *g_start, *g_pre, *g_units, *g_row;
-  __host__ __device__ static uint32_t words(uint32_t rows, uint32_t groups) { return 8 + 4 * rows + 1 + 4 * groups + 2; }
+  uint32_t *head, *row_pre, *row_end, *row_group, *g_start, *g_pre, *g_len, *g_row;
+  __host__ __device__ static constexpr uint32_t words(uint32_t rows, uint32_t groups) { return 8 + 3 * rows + 1 + 4 * groups + 3; }
+  __host__ __device__ static constexpr uint64_t record_words(uint32_t rows, uint32_t groups) { return 8 + 4 * (uint64_t{rows} + groups); }
   __device__ Plan(uint32_t* p, uint32_t rows, uint32_t groups) {
     head = p;
     row_pre = head + 8;
-    row_base = row_pre + rows + 1;
-    row_end = row_base + rows;
+    row_end = row_pre + rows + 1;
     row_group = row_end + rows;
     g_start = row_group + rows;
     g_pre = g_start + groups + 1;
-    g_units = g_pre + groups + 1;
-    g_row = g_units + groups;
+    g_len = g_pre + groups + 1;
+    g_row = g_len + groups + 1;
   }
-  __device__ uint64_t quota(int i) const { return head[2 + 2 * i] | static_cast<uint64_t>(head[3 + 2 * i]) << 32; }
+  __device__ uint32_t base(uint32_t r) const { return g_len[row_group[r]]; }  // the row's first own position
 };
 
-// In-place inclusive scan (sum or maximum) of n words in LDS by the workgroup;
-// carry: 8 words of LDS.
+// Inclusive scan (sum or maximum of unsigned values) over the wavefront: shifts
+// within rows of 16 lanes, then the rows' last lanes.
+template <bool MAX>
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  auto step = [&](auto ctrl, auto rows) {
+    const uint32_t y = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+        0, static_cast<int>(v), decltype(ctrl)::value, decltype(rows)::value, 0xF, false));
+    v = MAX ? max(v, y) : v + y;
+  };
+  using std::integral_constant;
+  step(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});  // row_shr 1, 2, 4, 8
+  step(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});
+  step(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});
+  step(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});
+  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});  // row_bcast 15 to rows 1 and 3
+  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});  // row_bcast 31 to rows 2 and 3
+  return v;
+}
+
+// In-place inclusive scan of n words in LDS by the workgroup; carry: 8 words of LDS.
 template <bool MAX>
 __device__ void block_scan(uint32_t* v, uint32_t n, uint32_t* carry) {
   const uint32_t lane = __lane_id(), wave = threadIdx.x / kWave;
   uint32_t before = 0;
   for (uint32_t base = 0; base < n; base += kAttendThreads) {
     const uint32_t i = base + threadIdx.x;
-    uint32_t x = i < n ? v[i] : 0;
-#pragma unroll
-    for (int s = 1; s < kWave; s *= 2) {
-      const uint32_t y = __shfl_up(x, s, kWave);
-      if (lane >= static_cast<uint32_t>(s)) x = MAX ? max(x, y) : x + y;
-    }
+    uint32_t x = wave_scan<MAX>(i < n ? v[i] : 0);
     if (lane == kWave - 1) carry[wave] = x;
     __syncthreads();
     for (uint32_t w = 0; w < 4; ++w) {
@@ -325,16 +340,21 @@ __device__ void block_scan(uint32_t* v, uint32_t n, uint32_t* carry) {
 __device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t* carry) {
   const uint32_t rows = a.pages.rows, G = a.n_groups, tid = threadIdx.x;
   const int32_t most = static_cast<int32_t>(a.pages.cols << a.pages.shift);
+  int32_t len = tid < rows ? a.lengths[tid] : -1;  // asked for before the groups are looked at
   for (uint32_t i = tid; i < G; i += kAttendThreads) {
     p.g_start[i] = static_cast<uint32_t>(min(max(a.group_start[i], 0), static_cast<int32_t>(rows)));
-    p.g_units[i] = static_cast<uint32_t>(min(max(a.group_len[i], 0), most));  // positions, for now
+    p.g_len[i] = static_cast<uint32_t>(min(max(a.group_len[i], 0), most));
     p.g_row[i] = rows;
   }
-  if (tid == 0) p.g_start[G] = G ? static_cast<uint32_t>(min(max(a.group_start[G], 0), static_cast<int32_t>(rows))) : 0;
+  if (tid == 0) {
+    p.g_len[G] = 0;
+    p.g_start[G] = G ? static_cast<uint32_t>(min(max(a.group_start[G], 0), static_cast<int32_t>(rows))) : 0;
+    p.row_pre[0] = p.g_pre[0] = 0;
+  }
   __syncthreads();
   if (G) block_scan<true>(p.g_start, G + 1, carry);
   for (uint32_t r = tid; r < rows; r += kAttendThreads) {
-    const int32_t len = a.lengths[r];
+    if (r != tid) len = a.lengths[r];
     const uint32_t end = static_cast<uint32_t>(min(len, most));
     uint32_t g = 0, hi = G + 1;  // the last start <= r
     while (G && g + 1 < hi) {
@@ -342,11 +362,10 @@ __device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t* carry) {
       if (p.g_start[mid] <= r) g = mid; else hi = mid;
     }
     const bool in = G && g < G && p.g_start[g] <= r;
-    const uint32_t s = in ? p.g_units[g] : 0;
+    const uint32_t s = in ? p.g_len[g] : 0;
     const bool shares = s > 0 && len > 0 && end >= s;
     const uint32_t base = shares ? s : 0;
     p.row_end[r] = len < 0 ? 0xFFFFFFFFu : end;
-    p.row_base[r] = base;
     p.row_group[r] = shares ? g : G;
     p.row_pre[r + 1] = len > 0 && end > base ? (end + 31) / 32 - base / 32 : 0;
     if (shares) atomicMin(&p.g_row[g], r);
@@ -354,13 +373,10 @@ __device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t* carry) {
   __syncthreads();
   for (uint32_t i = tid; i < G; i += kAttendThreads) {
     const uint32_t cols = (p.g_start[i + 1] - p.g_start[i]) * a.ratio;
-    const uint32_t units = p.g_row[i] < rows ? (p.g_units[i] + 31) / 32 : 0;
+    const uint32_t units = p.g_row[i] < rows ? (p.g_len[i] + 31) / 32 : 0;
     p.g_pre[i + 1] = units * ((cols + kCap - 1) / kCap);
-    p.g_units[i] = units;  // the length in positions is the row_base of the rows that share
   }
-  if (tid == 0) p.row_pre[0] = p.g_pre[0] = 0;
-  __syncthreads();
-  block_scan<false>(p.row_pre + 1, rows, carry);
+  block_scan<false>(p.row_pre + 1, rows, carry);  // its barriers serve g_pre too
   if (G) block_scan<false>(p.g_pre + 1, G, carry);
   if (tid == 0) {
     p.head[0] = p.g_pre[G];
@@ -382,6 +398,13 @@ __device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t* carry) {
     p.head[7] = 0;
   }
   __syncthreads();
+  if (blockIdx.x == 0) {
+    u32x4_t* rec = reinterpret_cast<u32x4_t*>(a.plan);
+    if (tid < 2) rec[tid] = u32x4_t{p.head[4 * tid], p.head[4 * tid + 1], p.head[4 * tid + 2], p.head[4 * tid + 3]};
+    for (uint32_t r = tid; r < rows; r += kAttendThreads)
+      rec[2 + r] = u32x4_t{p.row_pre[r], p.row_pre[r + 1] - p.row_pre[r], p.row_group[r], p.row_end[r]};
+    for (uint32_t i = tid; i < G; i += kAttendThreads) rec[2 + rows + i] = u32x4_t{p.g_start[i], p.g_pre[i], p.g_len[i], 0};
+  }
 }
 
 // A worker's part of one item; all fields wave-uniform.
@@ -674,22 +697,22 @@ __device__ __forceinline__ void walk(const AttendArgs& a, const Segment& it, uin
 // LDS of a workgroup: the fixed part, then the plan, then the ring of slots or
 // the sums that the wavefronts exchange (never both).
 struct LdsFixed {
-  float m[4][32], l[4][32];  // [wavefront][column]
+  float m[8][32], l[8][32];  // [wavefront][column]
   uint32_t good[4][4];       // [slot][wavefront]: the page exists
   uint32_t carry[8];
 };
-template <int D>
-using Join = float[4][16][AttendShape<D>::kJLd];
+template <int D, int W>
+using Join = float[W][16][AttendShape<D>::kJLd];
 
-// A workgroup's part of an item of at most 16 NT columns: the wavefronts take its
-// units in turn, their sums are brought to one maximum and added in order.
-template <int D, int NT>
-__device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment& it, LdsFixed& s, Join<D>& join) {
+// An item of at most 16 NT columns by a workgroup of W wavefronts, which take its
+// units in turn; their sums are brought to one maximum and added in order.
+template <int D, int NT, int W>
+__device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment& it, LdsFixed& s, Join<D, W>& join) {
   constexpr int kDt = AttendShape<D>::kDt;
   const uint32_t wave = uniform(threadIdx.x / kWave), tid = threadIdx.x;
   const uint32_t n = __lane_id() % 16, g = __lane_id() / 16;
   Sums<D, NT> acc;
-  walk<D, NT>(a, it, it.u0 + wave, 4, acc);
+  walk<D, NT>(a, it, it.u0 + wave, W, acc);
   acc.finish();
   __syncthreads();  // the exchange's last readers are done
   if (g == 0)
@@ -703,7 +726,7 @@ __device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment&
   for (int c = 0; c < NT; ++c) {
     float top = acc.m[c];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, s.m[w][16 * c + n]);
+    for (int w = 0; w < W; ++w) top = fmaxf(top, s.m[w][16 * c + n]);
     const float f = __builtin_amdgcn_exp2f(acc.m[c] - top);
     if (c) __syncthreads();
 #pragma unroll
@@ -713,17 +736,24 @@ __device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment&
       for (int d = 0; d < kDt; ++d) dst[d] = acc.o[d][c][i] * f;
     }
     __syncthreads();
-    for (uint32_t i = tid; i < 16 * (D / 4); i += kAttendThreads) {
+    for (uint32_t i = tid; i < 16 * (D / 4); i += W * kWave) {
       const uint32_t col = i / (D / 4), e = i % (D / 4) * 4, cc = 16 * c + col;
       if (cc >= it.cols) continue;
       f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
       float total = 0.f, best = s.m[0][cc];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) best = fmaxf(best, s.m[w][cc]);
+      for (int w = 1; w < W; ++w) best = fmaxf(best, s.m[w][cc]);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < W; ++w) {
         sum += *reinterpret_cast<const f32x4_t*>(&join[w][col][e]);
         total += s.l[w][cc] * __builtin_amdgcn_exp2f(s.m[w][cc] - best);
+      }
+      if (it.direct) {
+        const float r = total == 0.f ? 0.f : 1.f / total;
+        const uint32_t cl = it.col0 + cc, row = it.row0 + cl / a.ratio, h = it.head * a.ratio + cl % a.ratio;
+        const u32x2_t w = {pack_bf16(sum[0] * r, sum[1] * r), pack_bf16(sum[2] * r, sum[3] * r)};
+        *reinterpret_cast<u32x2_t*>(a.out + row * a.ldo + static_cast<uint64_t>(h) * D + e) = w;
+        continue;
       }
       *reinterpret_cast<f32x4_t*>(a.part_o + (it.slot + cc) * D + e) = sum;
       if (e == 0) {
@@ -881,7 +911,7 @@ __device__ __forceinline__ Segment own_segment(const AttendArgs& a, const Plan& 
   it.col0 = 0;
   it.cols = a.ratio;
   it.ids = a.pages.ids + r * a.pages.ld;
-  it.p0 = uniform(p.row_base[r]);
+  it.p0 = uniform(p.base(r));
   it.p1 = uniform(p.row_end[r]);
   const uint32_t first = it.p0 / 32, units = (it.p1 + 31) / 32 - first;
   it.u0 = first + done;
@@ -895,7 +925,8 @@ __device__ __forceinline__ Segment own_segment(const AttendArgs& a, const Plan& 
 __device__ __forceinline__ Segment prefix_segment(const AttendArgs& a, const Plan& p, uint32_t head, uint32_t rem, uint64_t left,
                                                   uint64_t worker) {
   const uint32_t i = uniform(find_last(p.g_pre, a.n_groups, rem));
-  const uint32_t units = uniform(p.g_units[i]), in = rem - uniform(p.g_pre[i]), block = in / units, done = in - block * units;
+  const uint32_t len = uniform(p.g_len[i]), units = (len + 31) / 32, in = rem - uniform(p.g_pre[i]);
+  const uint32_t block = in / units, done = in - block * units;
   const uint32_t r = uniform(p.g_row[i]);
   Segment it;
   it.head = head;
@@ -904,7 +935,7 @@ __device__ __forceinline__ Segment prefix_segment(const AttendArgs& a, const Pla
   it.cols = min((uniform(p.g_start[i + 1]) - it.row0) * a.ratio - it.col0, kCap);
   it.ids = a.pages.ids + r * a.pages.ld;
   it.p0 = 0;
-  it.p1 = uniform(p.row_base[r]);
+  it.p1 = len;
   it.u0 = done;
   it.u1 = done + static_cast<uint32_t>(min(static_cast<uint64_t>(units - done), left));
   it.direct = false;
@@ -919,10 +950,8 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
   const uint32_t rows = a.pages.rows, G = a.n_groups;
   const Plan p(reinterpret_cast<uint32_t*>(lds + sizeof(LdsFixed)), rows, G);
   uint8_t* big = lds + sizeof(LdsFixed) + (Plan::words(rows, G) * 4 + 15) / 16 * 16;
-  Join<D>& join = *reinterpret_cast<Join<D>*>(big);
+  Join<D, 4>& join = *reinterpret_cast<Join<D, 4>*>(big);
   make_plan(a, p, s.carry);
-  if (blockIdx.x == 0)
-    for (uint32_t i = threadIdx.x; i < Plan::words(rows, G); i += kAttendThreads) a.plan[i] = p.head[i];
   const uint32_t prefix_units = uniform(p.head[0]), own_units = uniform(p.head[1]);
   if (prefix_units) {
     const uint64_t quota = uniform(p.head[2]) | static_cast<uint64_t>(uniform(p.head[3])) << 32;
@@ -937,9 +966,9 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
       const uint32_t head = static_cast<uint32_t>(at / prefix_units);
       const Segment it = prefix_segment(a, p, head, static_cast<uint32_t>(at % prefix_units), end - at, wg);
       if (it.cols <= 16)
-        attend_turns<D, 1>(a, it, s, join);
+        attend_turns<D, 1, 4>(a, it, s, join);
       else if (D <= 128 && it.cols <= 32)
-        attend_turns<D, D <= 128 ? 2 : 1>(a, it, s, join);
+        attend_turns<D, D <= 128 ? 2 : 1, 4>(a, it, s, join);
       else if (it.cols <= 64)
         attend_shared<D, 1>(a, it, big, s.good);
       else
@@ -976,6 +1005,36 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
   }
 }
 
+// Short tables: one workgroup per row, key-value head and 32 query heads of it
+// takes all of the row's positions, 8 wavefronts in turn.  One launch, no plan
+// and no partial sums.
+constexpr int kRowWaves = 8;
+template <int D>
+__global__ __launch_bounds__(kRowWaves * kWave) void k_attend_rows(const AttendArgs a) {
+  __shared__ LdsFixed s;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  Join<D, kRowWaves>& join = *reinterpret_cast<Join<D, kRowWaves>*>(lds);
+  const uint32_t r = blockIdx.x / a.hkv;
+  const int32_t len = sload(a.lengths, r);
+  if (len < 0) return;  // padding
+  Segment it;
+  it.head = blockIdx.x % a.hkv;
+  it.row0 = r;
+  it.col0 = blockIdx.y * kWaveRatio;
+  it.cols = min(a.ratio - it.col0, kWaveRatio);
+  it.ids = a.pages.ids + r * a.pages.ld;
+  it.p0 = 0;
+  it.p1 = min(static_cast<uint32_t>(len), a.pages.cols << a.pages.shift);
+  it.u0 = 0;
+  it.u1 = (it.p1 + 31) / 32;
+  it.direct = true;
+  it.slot = 0;
+  if (it.cols <= 16)
+    attend_turns<D, 1, kRowWaves>(a, it, s, join);
+  else
+    attend_turns<D, 2, kRowWaves>(a, it, s, join);
+}
+
 // One workgroup per row and query head: the partial sums of its column, prefix
 // first.  D / 4 threads hold a column's components; the parts go round kLines
 // such lines, each keeps a running maximum, and the lines are added in order.
@@ -985,20 +1044,22 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs
   __shared__ f32x4_t sums[kLines][kLine];
   __shared__ float ms[kLines], ls[kLines];
   const uint32_t rows = a.pages.rows, r = blockIdx.x / a.hq, h = blockIdx.x % a.hq, head = h / a.ratio, j = h % a.ratio;
-  const Plan p(a.plan, rows, a.n_groups);
-  const uint32_t prefix_units = p.head[0], own_units = p.head[1];
-  const uint64_t quota_p = p.quota(0), quota_o = p.quota(1);
-  const uint32_t base = p.row_base[r], g = p.row_group[r], pre = p.row_pre[r], units = p.row_pre[r + 1] - pre;
-  if (static_cast<int32_t>(p.row_end[r]) < 0) return;  // padding
+  const u32x4_t* rec = reinterpret_cast<const u32x4_t*>(a.plan);
+  const u32x4_t h0 = rec[0], h1 = rec[1], row = rec[2 + r];
+  const uint32_t prefix_units = h0[0], own_units = h0[1], pre = row[0], units = row[1], g = row[2];
+  const uint64_t quota_p = h0[2] | static_cast<uint64_t>(h0[3]) << 32, quota_o = h1[0] | static_cast<uint64_t>(h1[1]) << 32;
+  if (static_cast<int32_t>(row[3]) < 0) return;  // padding
+  const bool shares = g < a.n_groups;
   // the worker that has a unit (32-bit division where the numbers allow)
   auto owner = [](uint64_t x, uint64_t quota) -> uint32_t {
     return static_cast<uint32_t>((x | quota) >> 32 ? x / quota : static_cast<uint32_t>(x) / static_cast<uint32_t>(quota));
   };
   uint32_t n0 = 0, n1 = 0;  // parts of the prefix, of the own positions
   uint64_t slot0 = 0, slot1 = 0;
-  if (base) {
-    const uint32_t first_row = p.g_start[g], col = (r - first_row) * a.ratio + j, block = col / kCap, n = p.g_units[g];
-    const uint64_t first = static_cast<uint64_t>(prefix_units) * head + p.g_pre[g] + static_cast<uint64_t>(block) * n;
+  if (shares) {
+    const u32x4_t group = rec[2 + rows + g];
+    const uint32_t first_row = group[0], col = (r - first_row) * a.ratio + j, block = col / kCap, n = (group[2] + 31) / 32;
+    const uint64_t first = static_cast<uint64_t>(prefix_units) * head + group[1] + static_cast<uint64_t>(block) * n;
     const uint32_t w = owner(first, quota_p);
     n0 = owner(first + n - 1, quota_p) - w + 1;
     slot0 = part_slot(a, true, head, first_row, block * kCap, w) + col % kCap;
@@ -1008,7 +1069,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs
     const uint32_t w = owner(first, quota_o);
     n1 = owner(first + units - 1, quota_o) - w + 1;
     slot1 = part_slot(a, false, head, r, 0, w) + j;
-    if (!base && n1 == 1) return;  // k_attend wrote the output itself
+    if (!shares && n1 == 1) return;  // k_attend wrote the output itself
   }
   const uint32_t line = threadIdx.x / kLine, e = threadIdx.x % kLine * 4, parts = n0 + n1;
   f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
@@ -1153,7 +1214,7 @@ void set_rope(HeadsArgs* a, const nwc_rope* rope) {
 }
 
 // Workspace of nwc_attend: partial sums, maxima and sums, the plan.
-constexpr uint32_t kAttendMaxRows = 4096, kAttendMaxGroups = 1024, kAttendMaxRatio = 64, kAttendMaxLen = 1u << 22;
+constexpr uint32_t kAttendMaxRows = 4096, kAttendMaxGroups = 512, kAttendMaxRatio = 64, kAttendMaxLen = 1u << 22;
 struct AttendLayout {
   uint64_t own_slot, ml, plan, bytes;
   uint32_t cap_p, cap_o;
@@ -1168,7 +1229,7 @@ AttendLayout attend_layout(uint32_t rows, uint32_t q_heads, uint32_t ratio, uint
   auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
   L.ml = up(slots * d * 4);
   L.plan = L.ml + up(slots * 8);
-  L.bytes = L.plan + up(static_cast<uint64_t>(Plan::words(rows, groups)) * 4);
+  L.bytes = L.plan + up(Plan::record_words(rows, groups) * 4);
   return L;
 }
 
@@ -1184,11 +1245,30 @@ nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uin
 
 
 
+// Positions that a table may cover for k_attend_rows to take it: any call up to
+// 512, calls with a workgroup for half the compute units up to 1024.  Measured
+// (32 / 8 heads of 128, all rows full, us a call in a graph, k_attend_rows and
+// k_attend + k_attend_join): 1 row of 256: 6.1 and 7.9, 512: 8.5 and 8.4, 1024:
+// 12.8 and 8.4; 16 rows of 512: 9.9 and 14.2, 1024: 14.9 and 18.8; 64 rows of
+// 1024: 50.8 and 55.9.  Longer ones win less and lose more where one row is
+// much longer than the others.
+constexpr uint32_t kRowsMost = 512, kRowsMostMany = 1024;
+
 template <int D>
 nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
+  const uint32_t covers = a.pages.cols << a.pages.shift;
+  if (!a.n_groups && covers <= (2 * a.pages.rows * a.hkv >= a.own_wgs ? kRowsMostMany : kRowsMost)) {
+    constexpr size_t lds = sizeof(Join<D, kRowWaves>);
+    static_assert(sizeof(LdsFixed) + lds <= kMaxLds, "LDS");
+    if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend_rows<D>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds)) != hipSuccess)
+      return NWC_ERR_HIP;
+    return launch(k_attend_rows<D>, dim3(a.pages.rows * a.hkv, (a.ratio + kWaveRatio - 1) / kWaveRatio),
+                  dim3(kRowWaves * kWave), lds, s, a);
+  }
   const size_t fixed = sizeof(LdsFixed) + (static_cast<size_t>(Plan::words(a.pages.rows, a.n_groups)) * 4 + 15) / 16 * 16;
   a.ring = D == 256 ? (fixed + 3 * 128 * D <= kMaxLds ? 3 : 2) : 4;
-  const size_t lds = fixed + std::max<size_t>(sizeof(Join<D>), a.ring * 128 * D);
+  const size_t lds = fixed + std::max<size_t>(sizeof(Join<D, 4>), a.ring * 128 * D);
   if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<D>), hipFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(lds)) != hipSuccess)
     return NWC_ERR_HIP;

@@ -461,7 +461,7 @@ typedef struct {
  * with the same pages and lengths one apart, in one group.  groups NULL or
  * count 0: nothing shared.
  * scale finite and > 0.  head_dim 64, 96, 128, 192 or 256; q_heads a multiple of kv_heads, at most
- * 64 times it; at most 4096 rows and 1024 groups; cols * page_len <= 2^22.
+ * 64 times it; at most 4096 rows and 512 groups; cols * page_len <= 2^22.
  * Softmax statistics and sums in FP32; the weights w are rounded to BF16 for
  * the matrix cores (relative error 2^-9 each, the size of the output's own
  * rounding).  Repeated calls give the same bits.  ws (device, 256-byte

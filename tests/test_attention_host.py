@@ -134,7 +134,7 @@ def test_attend_refusals():
     assert _attend(groups=g(None, A, 1, 0)) == nwc.NWC_ERR_INVALID_ARG
     assert _attend(groups=g(A, None, 1, 0)) == nwc.NWC_ERR_INVALID_ARG
     assert _attend(groups=g(A, A, 1, 5)) == nwc.NWC_ERR_INVALID_ARG
-    assert _attend(groups=g(A, A, 1025, 0)) == nwc.NWC_ERR_UNSUPPORTED
+    assert _attend(groups=g(A, A, 513, 0)) == nwc.NWC_ERR_UNSUPPORTED
     assert _attend(groups=g(A + 2, A, 1, 0)) == nwc.NWC_ERR_ALIGNMENT
     assert _attend(groups=g(A, A + 1, 1, 0)) == nwc.NWC_ERR_ALIGNMENT
     for bad, want in CACHE_BAD:
