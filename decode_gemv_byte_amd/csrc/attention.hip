@@ -249,6 +249,8 @@ struct AttendShape {
   static constexpr int kDt = D / 16;   // 16-row tiles of O^T = components of a lane
   static constexpr int kKs = D / 32;   // steps of the K Q^T product
   static constexpr int kJLd = D + 4;   // padded LDS rows (banks)
+  static constexpr int kRowWaves = D <= 128 ? 8 : 4;  // of k_attend_rows: as many as their registers allow
+  static constexpr int kRing = D <= 128 ? 4 : 3;  // units in the LDS ring (64 KB at 128: two workgroups fit a compute unit)
 };
 
 struct AttendArgs {
@@ -265,7 +267,6 @@ struct AttendArgs {
   uint64_t own_slot;        // first column slot of the own positions' parts
   uint32_t cap_p, cap_o;    // column slots of a worker's part: prefixes, own positions
   uint32_t own_wgs;         // workgroups for own positions, the last of the grid
-  uint32_t ring;            // slots of the ring in LDS
 };
 
 // The split of a call, made in LDS by every workgroup, u32 words:
@@ -607,6 +608,20 @@ struct Sums {
   }
 };
 
+// Where piece c of key row `row` (0 .. 31 of a unit) lies in its slot row, and
+// (INVERSE) which piece lies at c.  An operand read takes one piece of the rows
+// 8 (n / 4) + n % 4, n = 0 .. 15, which a slot row of D = 64, 96, 128, 192, 256
+// puts on 2, 4, 1, 2, 1 different groups of banks by itself.
+template <int D, bool INVERSE>
+__device__ __forceinline__ uint32_t key_piece(uint32_t row, uint32_t c) {
+  constexpr uint32_t kPieces = D / 8;
+  if (D == 128 || D == 256) return c ^ ((row & 3) | (row >> 3) << 2);
+  const uint32_t by = D == 96 ? row >> 3 : (row >> 1 & 1) | (row >> 3) << 1;
+  if (D == 64) return c ^ by;
+  const uint32_t x = INVERSE ? c + kPieces - by : c + by;
+  return x >= kPieces ? x - kPieces : x;
+}
+
 // One wavefront's loads of a unit and the two products.
 template <int D, int NT>
 struct Unit {
@@ -620,6 +635,19 @@ struct Unit {
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int k = 0; k < kKs; ++k) kf[t][k] = *reinterpret_cast<const u32x4_t*>(p + 4 * t * D + 32 * k);
+  }
+  // The keys from a slot of LDS (32 rows, pieces as key_piece puts them).  A
+  // typed read, never memcpy: a read that may alias the loads in flight makes
+  // the compiler wait for all of them.
+  __device__ __forceinline__ void read_k(const uint8_t* ks) {
+    const uint32_t n = __lane_id() % 16, g = __lane_id() / 16;
+#pragma unroll
+    for (int k = 0; k < kKs; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t row = 8 * (n / 4) + n % 4 + 4 * t;
+        kf[t][k] = *reinterpret_cast<const u32x4_t*>(ks + 16 * (row * (D / 8) + key_piece<D, false>(row, 4 * k + g)));
+      }
   }
   __device__ __forceinline__ void load_v(const AttendArgs& a, const PagePart& lo, const PagePart& hi) {
     const uint32_t n = __lane_id() % 16, g = __lane_id() / 16;
@@ -698,7 +726,6 @@ __device__ __forceinline__ void walk(const AttendArgs& a, const Segment& it, uin
 // the sums that the wavefronts exchange (never both).
 struct LdsFixed {
   float m[8][32], l[8][32];  // [wavefront][column]
-  uint32_t good[4][4];       // [slot][wavefront]: the page exists
   uint32_t carry[8];
 };
 template <int D, int W>
@@ -775,48 +802,42 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("" ::: "memory");
 }
 
-// Where piece c of key row `row` (0 .. 31 of a unit) lies in its slot row, and
-// (INVERSE) which piece lies at c.  An operand read takes one piece of the rows
-// 8 (n / 4) + n % 4, n = 0 .. 15, which a slot row of D = 64, 96, 128, 192, 256
-// puts on 2, 4, 1, 2, 1 different groups of banks by itself.
-template <int D, bool INVERSE>
-__device__ __forceinline__ uint32_t key_piece(uint32_t row, uint32_t c) {
-  constexpr uint32_t kPieces = D / 8;
-  if (D == 128 || D == 256) return c ^ ((row & 3) | (row >> 3) << 2);
-  const uint32_t by = D == 96 ? row >> 3 : (row >> 1 & 1) | (row >> 3) << 1;
-  if (D == 64) return c ^ by;
-  const uint32_t x = INVERSE ? c + kPieces - by : c + by;
-  return x >= kPieces ? x - kPieces : x;
-}
-
 // The workgroup's part of an item of more than 32 columns: the wavefronts take
 // 16 NT columns each of the same units, which pass through a ring of slots in
 // LDS, loaded straight from the pages (a quarter of a unit's rows per
-// wavefront, `ring - 1` units ahead), so a unit is read once per workgroup.
+// wavefront, kRing - 1 units ahead), so a unit is read once per workgroup.
 // One barrier per unit: behind it the unit has landed for all, and the slot of
 // the unit before is free.  A slot holds 32 rows of keys, then of values; the
 // 16-byte pieces of a key row are permuted by the row, so that the 16 rows
 // that one operand read touches lie in 64 different banks.
 template <int D, int NT>
-__device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment& it, uint8_t* slots, uint32_t (&good)[4][4]) {
+__device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment& it, uint8_t* slots) {
   using S = AttendShape<D>;
   constexpr int kDt = S::kDt, kKs = S::kKs, kLoads = (D + 63) / 64;
-  constexpr uint32_t kPieces = D / 8, kSlotBytes = 128 * D;
+  constexpr uint32_t kPieces = D / 8, kSlotBytes = 128 * D, kRing = S::kRing, kAhead = kRing - 1;
   const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave);
   const uint32_t n = lane % 16, g = lane / 16, units = it.u1 - it.u0;
-  auto pos_of = [&](uint32_t i) { return 32 * (it.u0 + i) + 8 * wave; };  // this wavefront's rows of unit i
-  auto issue = [&](int32_t id, uint32_t i, uint32_t at) {                // unit i into slot `at`
-    const PagePart p = page_part(a, it, id, pos_of(i), D);
+  uint32_t seen = 0;  // two bits a unit, the last 16 units: the pages of its halves exist
+  int32_t id0 = 0, id1 = 0;
+  auto ask = [&](uint32_t i) {  // page numbers of unit i, a unit ahead of their use
+    id0 = page_id(a, it, 32 * (it.u0 + i));
+    id1 = page_id(a, it, 32 * (it.u0 + i) + 16);
+  };
+  auto issue = [&](uint32_t i, uint32_t at) {  // this wavefront's 8 rows of unit i into slot `at`
+    const uint32_t pos = 32 * (it.u0 + i);
+    const PagePart lo = page_part(a, it, id0, pos, D), hi = page_part(a, it, id1, pos + 16, D);
+    const uint64_t off = (wave < 2 ? lo.off : hi.off) + wave % 2 * (8 * D);
     uint8_t* to = slots + at * kSlotBytes + wave * (16 * D);
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) {
       const uint32_t piece = 64 * x + lane, row = piece / kPieces, c = piece % kPieces;
-      if (piece < 8 * kPieces) {  // D = 96: the second load is half a wavefront
-        __builtin_amdgcn_global_load_lds(a.k + p.off + row * D + 8 * key_piece<D, true>(8 * wave + row, c), to + 1024 * x, 16, 0, 0);
-        __builtin_amdgcn_global_load_lds(a.v + p.off + row * D + 8 * c, to + 64 * D + 1024 * x, 16, 0, 0);
+      if (64 * (x + 1) <= 8 * kPieces || piece < 8 * kPieces) {  // D = 96: the second load is half a wavefront
+        __builtin_amdgcn_global_load_lds(a.k + off + row * D + 8 * key_piece<D, true>(8 * wave + row, c), to + 1024 * x, 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(a.v + off + row * D + 8 * c, to + 64 * D + 1024 * x, 16, 0, 0);
       }
     }
-    if (lane == 0) good[at][wave] = p.known;
+    const uint32_t sh = 2 * (i % 16);
+    seen = (seen & ~(3u << sh)) | ((lo.known ? 1u : 0u) | (hi.known ? 2u : 0u)) << sh;
   };
 
   u32x4_t qf[kKs][NT];
@@ -827,38 +848,25 @@ __device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment
 #pragma unroll
     for (int k = 0; k < kKs; ++k) asm volatile("" : "+v"(qf[k][c]));
   __syncthreads();  // the slots' last readers are done
-  const uint32_t ahead = a.ring - 1;
-  for (uint32_t i = 0; i < ahead && i < units; ++i) issue(page_id(a, it, pos_of(i)), i, i);
-  int32_t next = page_id(a, it, pos_of(ahead));  // page numbers come a unit ahead of the loads
+  ask(0);
+  for (uint32_t i = 0; i < kAhead && i < units; ++i) {
+    issue(i, i);
+    ask(i + 1);
+  }
   Sums<D, NT> acc;
-  uint32_t at = 0, to = ahead;  // slots of unit i and of the unit loaded next
+  uint32_t at = 0, to = kAhead;  // slots of unit i and of the unit loaded next
   for (uint32_t i = 0; i < units; ++i) {
-    // unit i is there when only the units after it are in flight
-    if (ahead == 1 || i + ahead > units)
-      wait_and_meet<0>();
-    else if (ahead == 2)
-      wait_and_meet<2 * kLoads>();
+    // unit i is there when at most the kAhead - 1 units after it are in flight
+    if (i + kAhead <= units)
+      wait_and_meet<2 * kLoads*(kAhead - 1)>();
     else
-      wait_and_meet<4 * kLoads>();
-    const bool known = good[at][g] != 0;
-    if (i + ahead < units) issue(next, i + ahead, to);
-    next = page_id(a, it, pos_of(i + ahead + 1));
-    const uint8_t* ks = slots + at * kSlotBytes;
-    const uint8_t* vs = ks + 64 * D;
-    // all reads first: the products start as they arrive.  (Typed reads, never
-    // memcpy: a read that may alias the loads in flight makes the compiler wait
-    // for all of them.)
+      wait_and_meet<0>();
+    // all reads first: the products start as they arrive
     Unit<D, NT> x;
-#pragma unroll
-    for (int k = 0; k < kKs; ++k)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint32_t row = 8 * (n / 4) + n % 4 + 4 * t;
-        x.kf[t][k] = *reinterpret_cast<const u32x4_t*>(ks + 16 * (row * kPieces + key_piece<D, false>(row, 4 * k + g)));
-      }
+    x.read_k(slots + at * kSlotBytes);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint8_t* v = vs + 2 * ((8 * g + j) * D + kDt * n);
+      const uint8_t* v = slots + at * kSlotBytes + 64 * D + 2 * ((8 * g + j) * D + kDt * n);
       if constexpr (kDt % 8 == 0) {
 #pragma unroll
         for (int e = 0; e < kDt / 8; ++e) {
@@ -881,9 +889,13 @@ __device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment
     __builtin_amdgcn_sched_barrier(0);
     f32x4_t sc[2][NT];
     x.scores(qf, sc);
-    acc.take(sc, x.vr, it, 32 * (it.u0 + i), known, a.scale2);
-    at = at == ahead ? 0 : at + 1;
-    to = to == ahead ? 0 : to + 1;
+    if (i + kAhead < units) {  // while the products run
+      issue(i + kAhead, to);
+      ask(i + kAhead + 1);
+    }
+    acc.take(sc, x.vr, it, 32 * (it.u0 + i), (seen >> (2 * (i % 16) + g / 2) & 1) != 0, a.scale2);
+    at = at + 1 == kRing ? 0 : at + 1;
+    to = to + 1 == kRing ? 0 : to + 1;
   }
   acc.finish();
   acc.store(a, it, wave * (16 * NT));
@@ -970,9 +982,9 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
       else if (D <= 128 && it.cols <= 32)
         attend_turns<D, D <= 128 ? 2 : 1, 4>(a, it, s, join);
       else if (it.cols <= 64)
-        attend_shared<D, 1>(a, it, big, s.good);
+        attend_shared<D, 1>(a, it, big);
       else
-        attend_shared<D, 2>(a, it, big, s.good);
+        attend_shared<D, 2>(a, it, big);
       at += it.u1 - it.u0;
     }
   }
@@ -998,7 +1010,7 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
         acc.finish();
         acc.store(a, it, 0);
       } else {
-        attend_shared<D, 1>(a, it, big, s.good);
+        attend_shared<D, 1>(a, it, big);
       }
       at += it.u1 - it.u0;
     }
@@ -1006,11 +1018,11 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
 }
 
 // Short tables: one workgroup per row, key-value head and 32 query heads of it
-// takes all of the row's positions, 8 wavefronts in turn.  One launch, no plan
+// takes all of the row's positions, its wavefronts in turn.  One launch, no plan
 // and no partial sums.
-constexpr int kRowWaves = 8;
 template <int D>
-__global__ __launch_bounds__(kRowWaves * kWave) void k_attend_rows(const AttendArgs a) {
+__global__ __launch_bounds__(AttendShape<D>::kRowWaves * kWave) void k_attend_rows(const AttendArgs a) {
+  constexpr int kRowWaves = AttendShape<D>::kRowWaves;
   __shared__ LdsFixed s;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   Join<D, kRowWaves>& join = *reinterpret_cast<Join<D, kRowWaves>*>(lds);
@@ -1258,6 +1270,7 @@ template <int D>
 nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
   const uint32_t covers = a.pages.cols << a.pages.shift;
   if (!a.n_groups && covers <= (2 * a.pages.rows * a.hkv >= a.own_wgs ? kRowsMostMany : kRowsMost)) {
+    constexpr int kRowWaves = AttendShape<D>::kRowWaves;
     constexpr size_t lds = sizeof(Join<D, kRowWaves>);
     static_assert(sizeof(LdsFixed) + lds <= kMaxLds, "LDS");
     if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend_rows<D>),
@@ -1267,8 +1280,9 @@ nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
                   dim3(kRowWaves * kWave), lds, s, a);
   }
   const size_t fixed = sizeof(LdsFixed) + (static_cast<size_t>(Plan::words(a.pages.rows, a.n_groups)) * 4 + 15) / 16 * 16;
-  a.ring = D == 256 ? (fixed + 3 * 128 * D <= kMaxLds ? 3 : 2) : 4;
-  const size_t lds = fixed + std::max<size_t>(sizeof(Join<D, 4>), a.ring * 128 * D);
+  constexpr size_t big = std::max(sizeof(Join<D, 4>), size_t{AttendShape<D>::kRing * 128 * D});
+  static_assert(sizeof(LdsFixed) + 4 * Plan::words(kAttendMaxRows, kAttendMaxGroups) + 16 + big <= kMaxLds, "LDS");
+  const size_t lds = fixed + big;
   if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<D>), hipFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(lds)) != hipSuccess)
     return NWC_ERR_HIP;
