@@ -671,54 +671,44 @@ struct Unit {
   }
 };
 
-// Units u, u + step, .. of a segment by one wavefront.  For 16 columns two units
-// are held in registers, so that one is in flight while the other is computed;
-// for 32, where the registers go to the sums, a unit's keys are asked for when
-// the keys before them are used up, and its values likewise.  Page numbers come
-// by scalar loads a unit before their use, so that waiting for them waits for
-// no vector load.
+// Units u, u + step, .. of a segment by one wavefront: a unit's keys are asked for
+// when the keys before them are used up, and its values likewise (a second set
+// of registers, with two units in flight, was no faster: 99.0 and 98.7 us for
+// 131071 positions, 84.9 and 86.2 us for 48 ragged rows).  Page numbers come by
+// scalar loads a unit before their use, so that waiting for them waits for no
+// vector load.
 template <int D, int NT>
 __device__ __forceinline__ void walk(const AttendArgs& a, const Segment& it, uint32_t u, uint32_t step, Sums<D, NT>& acc) {
   if (u >= it.u1) return;
-  constexpr int kBuf = NT == 1 ? 2 : 1;
   const bool upper = __lane_id() / 16 >= 2;
   u32x4_t qf[AttendShape<D>::kKs][NT];
-  Unit<D, NT> x[kBuf];
-  bool good[kBuf];
+  Unit<D, NT> x;
   int32_t id0 = page_id(a, it, 32 * u), id1 = page_id(a, it, 32 * u + 16);
-  auto part = [&](uint32_t unit, PagePart& lo, PagePart& hi) {  // of the page numbers read last; then the next unit's
+  PagePart lo, hi;
+  auto part = [&](uint32_t unit) {  // of the page numbers read last; then the next unit's
     lo = page_part(a, it, id0, 32 * unit, D);
     hi = page_part(a, it, id1, 32 * unit + 16, D);
     id0 = page_id(a, it, 32 * (unit + step));
     id1 = page_id(a, it, 32 * (unit + step) + 16);
   };
-  PagePart lo, hi;
-#pragma unroll
-  for (int b = 0; b < kBuf; ++b)
-    if (b == 0 || u + step < it.u1) {
-      part(u + b * step, lo, hi);
-      x[b].load_k(a, lo, hi);
-      x[b].load_v(a, lo, hi);
-      good[b] = upper ? hi.known : lo.known;
-    }
+  part(u);
+  x.load_k(a, lo, hi);
+  x.load_v(a, lo, hi);
   load_queries<D, NT>(a, it, 0, qf);
   for (;;) {
-#pragma unroll
-    for (int b = 0; b < kBuf; ++b) {
-      const uint32_t next = u + kBuf * step;
-      f32x4_t sc[2][NT];
-      x[b].scores(qf, sc);
-      const bool now = good[b], more = next < it.u1;
-      if (more) {
-        part(next, lo, hi);
-        x[b].load_k(a, lo, hi);
-        good[b] = upper ? hi.known : lo.known;
-      }
-      acc.take(sc, x[b].vr, it, 32 * u, now, a.scale2);
-      if (more) x[b].load_v(a, lo, hi);
-      u += step;
-      if (u >= it.u1) return;
+    const bool good = upper ? hi.known : lo.known;
+    const uint32_t next = u + step;
+    const bool more = next < it.u1;
+    f32x4_t sc[2][NT];
+    x.scores(qf, sc);
+    if (more) {
+      part(next);
+      x.load_k(a, lo, hi);
     }
+    acc.take(sc, x.vr, it, 32 * u, good, a.scale2);
+    if (!more) break;
+    x.load_v(a, lo, hi);
+    u = next;
   }
 }
 
