@@ -49,7 +49,8 @@ __device__ __forceinline__ float lane_xor(float v, int mask) {
 
 struct PageArgs {
   const int32_t* ids;
-  uint64_t ld, n_pages, page_stride;
+  uint64_t ld;
+  uint32_t n_pages, stride8;   // pages; elements / 8 from page to page
   uint32_t rows, cols, shift;  // page_len = 1 << shift
 };
 
@@ -155,9 +156,9 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
           const uint32_t at = static_cast<uint32_t>(pos) >> a.pages.shift;
           stored = row < a.pages.rows && at < a.pages.cols;
           const int32_t id = stored ? a.pages.ids[row * a.pages.ld + at] : -1;
-          stored = static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages;
+          stored = static_cast<uint32_t>(id) < a.pages.n_pages;
           if (stored)
-            slot = id * a.pages.page_stride +
+            slot = static_cast<uint64_t>(id) * a.pages.stride8 * 8 +
                    static_cast<uint64_t>(static_cast<uint32_t>(pos) & ((1u << a.pages.shift) - 1)) * a.d;
         }
       }
@@ -447,10 +448,12 @@ struct PagePart {
   bool known;
 };
 __device__ __forceinline__ PagePart page_part(const AttendArgs& a, const Segment& it, int32_t id, uint32_t pos, uint32_t d) {
+  // in pieces of 8 elements, of which a page has less than 2^32: few scalar
+  // instructions, which are what a wavefront waits for here
   PagePart p;
-  p.known = static_cast<uint64_t>(static_cast<int64_t>(id)) < a.pages.n_pages && pos >> a.pages.shift < a.pages.cols;
-  p.off = (p.known ? static_cast<uint64_t>(id) : 0) * a.pages.page_stride +
-          ((static_cast<uint64_t>(it.head) << a.pages.shift) + (pos & ((1u << a.pages.shift) - 1))) * d;
+  p.known = static_cast<uint32_t>(id) < a.pages.n_pages && pos >> a.pages.shift < a.pages.cols;
+  const uint32_t within = ((it.head << a.pages.shift) + (pos & ((1u << a.pages.shift) - 1))) * (d / 8);
+  p.off = (static_cast<uint64_t>(p.known ? id : 0) * a.pages.stride8 + within) << 3;
   return p;
 }
 
@@ -796,8 +799,8 @@ __device__ __forceinline__ void wait_and_meet() {
 // 16 NT columns each of the same units, which pass through a ring of slots in
 // LDS, loaded straight from the pages (a quarter of a unit's rows per
 // wavefront, kRing - 1 units ahead), so a unit is read once per workgroup.
-// One barrier per unit: behind it the unit has landed for all, and the slot of
-// the unit before is free.  A slot holds 32 rows of keys, then of values; the
+// One barrier per unit i: behind it unit i + 1 has landed for all, so that its
+// keys can be read while unit i is weighed, and the slot of unit i - 1 is free.  A slot holds 32 rows of keys, then of values; the
 // 16-byte pieces of a key row are permuted by the row, so that the 16 rows
 // that one operand read touches lie in 64 different banks.
 template <int D, int NT>
@@ -844,16 +847,21 @@ __device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment
     ask(i + 1);
   }
   Sums<D, NT> acc;
-  uint32_t at = 0, to = kAhead;  // slots of unit i and of the unit loaded next
+  Unit<D, NT> x;
+  // unit 0 has landed when at most the kAhead - 1 units behind it are in flight
+  if (units >= kAhead)
+    wait_and_meet<2 * kLoads*(kAhead - 1)>();
+  else
+    wait_and_meet<0>();
+  x.read_k(slots);
+  uint32_t at = 0;  // slot of unit i
   for (uint32_t i = 0; i < units; ++i) {
-    // unit i is there when at most the kAhead - 1 units after it are in flight
+    // unit i + 1 has landed when at most the kAhead - 2 units behind it are in flight
     if (i + kAhead <= units)
-      wait_and_meet<2 * kLoads*(kAhead - 1)>();
+      wait_and_meet<2 * kLoads*(kAhead - 2)>();
     else
       wait_and_meet<0>();
-    // all reads first: the products start as they arrive
-    Unit<D, NT> x;
-    x.read_k(slots + at * kSlotBytes);
+    const uint32_t after = at + 1 == kRing ? 0 : at + 1;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint8_t* v = slots + at * kSlotBytes + 64 * D + 2 * ((8 * g + j) * D + kDt * n);
@@ -876,16 +884,15 @@ __device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment
         for (int e = 0; e < kDt / 2; ++e) x.vr[j][e] = reinterpret_cast<const uint32_t*>(v)[e];
       }
     }
-    __builtin_amdgcn_sched_barrier(0);
     f32x4_t sc[2][NT];
     x.scores(qf, sc);
-    if (i + kAhead < units) {  // while the products run
-      issue(i + kAhead, to);
+    if (i + 1 < units) x.read_k(slots + after * kSlotBytes);
+    if (i + kAhead < units) {
+      issue(i + kAhead, at == 0 ? kRing - 1 : at - 1);
       ask(i + kAhead + 1);
     }
     acc.take(sc, x.vr, it, 32 * (it.u0 + i), (seen >> (2 * (i % 16) + g / 2) & 1) != 0, a.scale2);
-    at = at + 1 == kRing ? 0 : at + 1;
-    to = to + 1 == kRing ? 0 : to + 1;
+    at = after;
   }
   acc.finish();
   acc.store(a, it, wave * (16 * NT));
@@ -1167,11 +1174,11 @@ nwc_status check_cache(const nwc_cache* c, const nwc_page_table* t, PageArgs* p)
       c->page_len == 0 || c->reserved)
     return NWC_ERR_INVALID_ARG;
   if (c->page_len < 16 || c->page_len > 1024 || (c->page_len & (c->page_len - 1))) return NWC_ERR_UNSUPPORTED;
-  if (c->page_stride < static_cast<uint64_t>(c->kv_heads) * c->page_len * c->head_dim || c->page_stride > kMaxStride)
+  if (c->page_stride < static_cast<uint64_t>(c->kv_heads) * c->page_len * c->head_dim || c->page_stride / 8 > 0xFFFFFFFF)
     return NWC_ERR_INVALID_ARG;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % 8) return NWC_ERR_ALIGNMENT;
-  p->n_pages = c->n_pages;
-  p->page_stride = c->page_stride;
+  p->n_pages = static_cast<uint32_t>(c->n_pages);
+  p->stride8 = static_cast<uint32_t>(c->page_stride / 8);
   p->shift = static_cast<uint32_t>(__builtin_ctz(c->page_len));
   if (t) {
     if (!t->ids || t->rows == 0 || t->cols == 0 || t->ld < t->cols || t->ld > kMaxStride) return NWC_ERR_INVALID_ARG;
