@@ -135,6 +135,12 @@ def parse():
     ap.add_argument("--model-step", type=int, default=0, metavar="LAYERS",
                     help="only time a whole decode step (tokens/s) through a Qwen3-4B-shaped stack of LAYERS "
                          "layers on synthetic weights, compressed vs dense BF16")
+    ap.add_argument("--paged", action="store_true",
+                    help="with --model-step: norm and rotate queries and keys, append to a paged KV cache and attend "
+                         "over it with the library's kernels (--batch rows of --context positions behind a shared "
+                         "prefix of --prefix), beside the same step with that part in torch")
+    ap.add_argument("--context", type=int, default=512, help="with --paged: positions of each row's own")
+    ap.add_argument("--prefix", type=int, default=0, help="with --paged: positions that all rows share")
     ap.add_argument("--copy-calibration", type=int, default=0, metavar="MIB",
                     help="only run a device-to-device copy of MIB MiB, 5 times (scales HBM byte counters)")
     ap.add_argument("--probe-only", action="store_true", help="only run the HBM read probe")
@@ -297,6 +303,161 @@ def model_step(args):
     return line
 
 
+def model_step_paged(args):
+    """One generated token of each of --batch sequences through the stack of
+    model_step, with everything a decode step does between its projections:
+    q/k/v, then one launch that norms (RMSNorm per head) and rotates queries and
+    keys and appends keys and values to a paged cache, attention over the cache
+    with the prefix that all sequences share read once, o, residual, RMSNorm,
+    gate/up, SiLU * up, down, residual.  Batch 1 runs the fused decode-GEMV
+    (nwc_gemv*), larger ones nwc_gemm_skinny (up to 32).  All layers' pages are
+    views of one allocation.  The step is captured as one HIP graph at a fixed
+    length (each replay writes the same slots).  The comparator is the same step
+    with the norm, rotation, append and attention as torch operations (FP32, the
+    cache gathered by the page table).  Reports whole-batch tokens/s."""
+    import torch
+    import torch.nn.functional as F
+
+    import decode_gemv_byte_amd as nwc
+    import workloads
+
+    torch.cuda.set_device(0)
+    dev = torch.device("cuda", 0)
+    L, H, HQ, HKV, D, PAGE, EPS = args.model_step, 2560, 32, 8, 128, 64, 1e-6
+    B, own, prefix = max(1, getattr(args, "batch", 0)), args.context, args.prefix // PAGE * PAGE
+    if B > 32 or own < 1:
+        print("--paged takes a batch of 1..32 and at least one position of each row's own", file=sys.stderr)
+        sys.exit(2)
+    names = ["q", "k", "v", "o", "gate", "up", "down"]
+    blob = {n: nwc.nwc_encode(workloads.weights(2, n)) for n in names}
+    info = {n: nwc.nwc_inspect(blob[n]) for n in names}
+    lay = [{n: torch.from_numpy(blob[n]).to(dev) for n in names} for _ in range(L)]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    bf = torch.bfloat16
+    length = prefix + own                      # the new token's position is length - 1
+    shared, private = prefix // PAGE, -(-length // PAGE) - prefix // PAGE
+    n_pages = shared + B * private
+    pool = torch.randn((n_pages, L, 2, HKV, PAGE, D), generator=g, device=dev, dtype=torch.float32).to(bf)
+    order = torch.randperm(n_pages, generator=torch.Generator().manual_seed(5)).to(torch.int32)
+    table = torch.empty((B, shared + private), dtype=torch.int32)
+    table[:, :shared] = order[:shared]
+    table[:, shared:] = order[shared:].view(B, private)
+    table = table.to(dev)
+    positions = torch.full((B,), length - 1, dtype=torch.int32, device=dev)
+    lengths = torch.full((B,), length, dtype=torch.int32, device=dev)
+    groups = dict(group_start=torch.tensor([0, B], dtype=torch.int32, device=dev),
+                  shared_len=torch.tensor([prefix], dtype=torch.int32, device=dev)) if prefix and B > 1 else {}
+    freqs = (1e6 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().to(dev)
+    wq, wk = ((1 + 0.1 * torch.randn(D, generator=g, device=dev)).to(bf) for _ in range(2))
+    x0 = torch.randn((B, H), generator=g, device=dev).to(bf)
+    x = x0.clone()
+    buf = {n: torch.empty((B, info[n].rows), dtype=bf, device=dev) for n in names}
+    q_rot, att = (torch.empty((B, HQ, D), dtype=bf, device=dev) for _ in range(2))
+    act = torch.empty((B, 9728), dtype=bf, device=dev)
+    heads = {"q": buf["q"].view(B, HQ, D), "k": buf["k"].view(B, HKV, D), "v": buf["v"].view(B, HKV, D)}
+    caches = [nwc.PagedCache(pool[:, l, 0], pool[:, l, 1]) for l in range(L)]
+    ws = torch.empty(nwc.nwc_attend_workspace_size(caches[0], B, HQ, 1 if groups else 0), dtype=torch.uint8, device=dev)
+    appends = [nwc.KvAppend(c, table, heads["k"], heads["v"], positions, k_weight=wk, q=heads["q"], q_out=q_rot, q_weight=wq,
+                            eps=EPS, freqs=freqs) for c in caches]
+    attends = [nwc.Attend(c, table, lengths, q_rot, att, ws, **groups) for c in caches]
+    ws_proj = {n: torch.zeros(max(1, nwc.nwc_workspace_size(info[n], B)), dtype=torch.uint8, device=dev) for n in names}
+    ws_grp = {grp: torch.zeros(nwc.gemv_batched_workspace_size([info[n] for n in grp]), dtype=torch.uint8, device=dev)
+              for grp in (("q", "k", "v"), ("gate", "up"))}
+    stream = torch.cuda.Stream()
+    keep = []
+
+    def project(l, grp, h):
+        if B == 1 and len(grp) > 1:
+            call = nwc.GemvBatch([info[n] for n in grp], [lay[l][n] for n in grp], [h[0]] * len(grp), [buf[n][0] for n in grp],
+                                 ws_grp[grp])
+            keep.append(call)
+            nwc.nwc_gemv_batched(call, stream=stream)
+        else:
+            for n in grp:
+                if B == 1:
+                    nwc.nwc_gemv(info[n], lay[l][n], h[0], buf[n][0], ws_proj[n], stream=stream)
+                else:
+                    nwc.nwc_gemm_skinny(info[n], lay[l][n], h, buf[n], ws_proj[n], stream=stream)
+        keep.append(h)
+
+    angle = (length - 1) * freqs.double()
+    cos, sin = angle.cos().float(), angle.sin().float()
+    slot = (length - 1) % PAGE
+    last = table[:, (length - 1) // PAGE].long()
+    gather = table.long()
+
+    def turned(t, w):
+        t = t.float()
+        t = t * torch.rsqrt((t * t).mean(-1, keepdim=True) + EPS) * w.float()
+        a, b = t[..., :D // 2], t[..., D // 2:]
+        return torch.cat((a * cos - b * sin, b * cos + a * sin), -1).to(bf)
+
+    def torch_attention(l):
+        pool[last, l, 0, :, slot] = turned(heads["k"], wk)
+        pool[last, l, 1, :, slot] = heads["v"]
+        k, v = (pool[:, l, i][gather].transpose(1, 2).reshape(B, HKV, -1, D)[:, :, :length].float() for i in (0, 1))
+        q = turned(heads["q"], wq).float().view(B, HKV, HQ // HKV, D)
+        w = torch.softmax(torch.matmul(q, k.transpose(-1, -2)) * D ** -0.5, -1)
+        att.copy_(torch.matmul(w, v).view(B, HQ, D))
+
+    def step(ours):
+        for l in range(L):
+            project(l, ("q", "k", "v"), F.rms_norm(x, (H,), eps=1e-6))
+            if ours:
+                nwc.nwc_kv_append(appends[l], stream=stream)
+                nwc.nwc_attend(attends[l], stream=stream)
+            else:
+                torch_attention(l)
+            project(l, ("o",), att.view(B, -1))
+            x.add_(buf["o"])
+            project(l, ("gate", "up"), F.rms_norm(x, (H,), eps=1e-6))
+            torch.mul(F.silu(buf["gate"]), buf["up"], out=act)
+            project(l, ("down",), act)
+            x.add_(buf["down"])
+
+    ms, outs, match = {}, {}, {}
+    for ours in (True, False):
+        with torch.cuda.stream(stream):
+            x.copy_(x0)
+            step(ours)
+        torch.cuda.synchronize()
+        outs[ours] = x.float().cpu().clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step(ours)
+        settle(torch, stream, lambda i: graph.replay())
+        for i in range(args.warmup):
+            graph.replay()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        with torch.cuda.stream(stream):
+            e0.record(stream)
+            for i in range(args.steps):
+                graph.replay()
+            e1.record(stream)
+        torch.cuda.synchronize()
+        ms[ours] = e0.elapsed_time(e1) / args.steps
+        with torch.cuda.stream(stream):        # a replay after many others still gives the eager step's bits
+            x.copy_(x0)
+            graph.replay()
+        torch.cuda.synchronize()
+        match[ours] = bool(torch.equal(outs[ours], x.float().cpu()))
+        del graph
+    line = {
+        "metric": "decode step tokens/s over a paged KV cache (Qwen3-4B-shaped stack, synthetic weights)",
+        "value": round(B * 1e3 / ms[True], 2), "unit": "tokens/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": round(ms[True], 4), "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16",
+        "data": "synthetic",
+        "config": {"workload": "qwen3_4b_stack", "layers": L, "batch": B, "context": own, "prefix": prefix, "page_len": PAGE,
+                   "hip_graph": True},
+        "torch_attention": {"tokens_per_s": round(B * 1e3 / ms[False], 2), "ms_per_step": round(ms[False], 4)},
+        "speedup_vs_torch_attention": round(ms[False] / ms[True], 3),
+        "final_hidden_rel_diff": round(float((outs[True] - outs[False]).norm() / outs[False].norm()), 6),
+        "graph_replays_match_eager": {"ours": match[True], "torch": match[False]}}
+    print(json.dumps(line))
+    return line
+
+
 def copy_calibration(mib):
     """A plain copy of known size: what FETCH_SIZE and WRITE_SIZE read for it
     gives the factors that turn those counters into HBM bytes."""
@@ -368,7 +529,7 @@ def main():
         copy_calibration(args.copy_calibration)
         return
     if args.model_step:
-        model_step(args)
+        (model_step_paged if args.paged else model_step)(args)
         return
     if args.gpus != 1 or int(os.environ.get("WORLD_SIZE", "1")) != 1:
         print("bench.py measures one GPU: the library has no multi-GPU path (a matrix would shard by row "

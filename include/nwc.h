@@ -398,8 +398,8 @@ nwc_status nwc_qk_norm_rope(const nwc_heads *q, const nwc_heads *k, uint32_t tok
 /* A paged cache of one layer: page p of the keys is kv_heads x page_len x
  * head_dim BF16 values at k + p * page_stride, of the values the same at v
  * (page_stride >= kv_heads * page_len * head_dim elements, a multiple of 8, so
- * keys, values and layers may interleave in one allocation; 16-byte aligned
- * pointers).  page_len a power of two, 16..1024. */
+ * keys, values and layers may interleave in one allocation, below 2^35; 16-byte
+ * aligned pointers).  page_len a power of two, 16..1024. */
 typedef struct {
   uint16_t *k, *v;
   uint64_t n_pages, page_stride;
