@@ -513,11 +513,13 @@ class _Call:
         return cache.struct
 
     def _run(self, fn, where: str, stream):
-        if self.device.index == torch.cuda.current_device():
-            _check(fn(*self.args, _stream(stream)), where)
-        else:   # streams and launches belong to the tensors' device
+        index = self.device.index
+        if index != torch.cuda.current_device():   # streams and launches belong to the tensors' device
             with torch.cuda.device(self.device):
-                _check(fn(*self.args, _stream(stream)), where)
+                return _check(fn(*self.args, _stream(stream)), where)
+        st = fn(*self.args, _raw_stream(index) if stream is None and _raw_stream is not None else _stream(stream))
+        if st:
+            _check(st, where)
 
 
 class PagedCache:
