@@ -271,22 +271,21 @@ struct AttendArgs {
 };
 
 // The split of a call, made in LDS by every workgroup, u32 words:
-//   head[8]             units per head of prefixes and of own positions; units per worker (two words each);
-//                       workgroups that prefixes are cut for
 //   row_pre[rows + 1]   units of own positions before the row
 //   row_end[rows]       its length, cut to what the table covers; -1 for padding
 //   row_group[rows]     the group whose prefix it shares, or the number of groups
 //   g_start[groups + 1], g_pre[groups + 1] (units before the group), g_len[groups + 1] (positions; 0 for no group),
 //   g_row[groups] (whose table row is read)
-// and for k_attend_join in the workspace, four words each: the head, then per
-// row {row_pre, units, group, length}, then per group {start, pre, len, 0}.
+// and for k_attend_join in the workspace, four words each: {units per head of
+// prefixes, of own positions, 0, 0}, {units per worker: of prefixes, of own
+// positions, two words each}, then per row {row_pre, units, group, length},
+// then per group {start, pre, len, 0}.
 struct Plan {
-  uint32_t *head, *row_pre, *row_end, *row_group, *g_start, *g_pre, *g_len, *g_row;
-  __host__ __device__ static constexpr uint32_t words(uint32_t rows, uint32_t groups) { return 8 + 3 * rows + 1 + 4 * groups + 3; }
+  uint32_t *row_pre, *row_end, *row_group, *g_start, *g_pre, *g_len, *g_row;
+  __host__ __device__ static constexpr uint32_t words(uint32_t rows, uint32_t groups) { return 3 * rows + 1 + 4 * groups + 3; }
   __host__ __device__ static constexpr uint64_t record_words(uint32_t rows, uint32_t groups) { return 8 + 4 * (uint64_t{rows} + groups); }
   __device__ Plan(uint32_t* p, uint32_t rows, uint32_t groups) {
-    head = p;
-    row_pre = head + 8;
+    row_pre = p;
     row_end = row_pre + rows + 1;
     row_group = row_end + rows;
     g_start = row_group + rows;
@@ -295,6 +294,12 @@ struct Plan {
     g_row = g_len + groups + 1;
   }
   __device__ uint32_t base(uint32_t r) const { return g_len[row_group[r]]; }  // the row's first own position
+};
+// What it comes to, wave-uniform.
+struct Split {
+  uint32_t prefix_units, own_units;  // per head
+  uint32_t prefix_wgs;               // workgroups that prefixes are cut for, the first of the grid
+  uint64_t prefix_quota, own_quota;  // units per workgroup; per wavefront (or workgroup)
 };
 
 // Inclusive scan (sum or maximum of unsigned values) over the wavefront: shifts
@@ -339,22 +344,39 @@ __device__ void block_scan(uint32_t* v, uint32_t n, uint32_t* carry) {
 
 // Lengths and groups (whatever they hold) into a plan whose ranges are all in
 // bounds: starts made ascending within 0..rows, lengths within 0..capacity.
-__device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t* carry) {
-  const uint32_t rows = a.pages.rows, G = a.n_groups, tid = threadIdx.x;
+// Up to 64 rows and 63 groups one wavefront scans each list in registers, with
+// three barriers in all (8 rows in one group: 3.2 us with the scans by the
+// workgroup).
+__device__ Split make_plan(const AttendArgs& a, const Plan& p, uint32_t* carry) {
+  const uint32_t rows = a.pages.rows, G = a.n_groups, tid = threadIdx.x, lane = __lane_id(), wave = uniform(tid / kWave);
   const int32_t most = static_cast<int32_t>(a.pages.cols << a.pages.shift);
+  const bool small = rows <= kWave && G < kWave;
   int32_t len = tid < rows ? a.lengths[tid] : -1;  // asked for before the groups are looked at
-  for (uint32_t i = tid; i < G; i += kAttendThreads) {
-    p.g_start[i] = static_cast<uint32_t>(min(max(a.group_start[i], 0), static_cast<int32_t>(rows)));
-    p.g_len[i] = static_cast<uint32_t>(min(max(a.group_len[i], 0), most));
-    p.g_row[i] = rows;
+  auto start_of = [&](uint32_t i) { return static_cast<uint32_t>(min(max(a.group_start[i], 0), static_cast<int32_t>(rows))); };
+  auto length_of = [&](uint32_t i) { return static_cast<uint32_t>(min(max(a.group_len[i], 0), most)); };
+  if (small && G) {
+    if (wave == 0) {
+      const uint32_t x = wave_scan<true>(lane <= G ? start_of(lane) : 0);
+      if (lane <= G) p.g_start[lane] = x;
+    } else if (wave == 1 && lane <= G) {
+      p.g_len[lane] = lane < G ? length_of(lane) : 0;
+      if (lane < G) p.g_row[lane] = rows;
+    }
+  } else {
+    for (uint32_t i = tid; i < G; i += kAttendThreads) {
+      p.g_start[i] = start_of(i);
+      p.g_len[i] = length_of(i);
+      p.g_row[i] = rows;
+    }
+    if (tid == 0) {
+      p.g_len[G] = 0;
+      p.g_start[G] = G ? start_of(G) : 0;
+    }
   }
-  if (tid == 0) {
-    p.g_len[G] = 0;
-    p.g_start[G] = G ? static_cast<uint32_t>(min(max(a.group_start[G], 0), static_cast<int32_t>(rows))) : 0;
-    p.row_pre[0] = p.g_pre[0] = 0;
-  }
+  if (tid == 0) p.row_pre[0] = p.g_pre[0] = 0;
   __syncthreads();
-  if (G) block_scan<true>(p.g_start, G + 1, carry);
+  if (G && !small) block_scan<true>(p.g_start, G + 1, carry);
+  uint32_t units = 0;  // of this thread's (last) row, then of its group
   for (uint32_t r = tid; r < rows; r += kAttendThreads) {
     if (r != tid) len = a.lengths[r];
     const uint32_t end = static_cast<uint32_t>(min(len, most));
@@ -369,44 +391,54 @@ __device__ void make_plan(const AttendArgs& a, const Plan& p, uint32_t* carry) {
     const uint32_t base = shares ? s : 0;
     p.row_end[r] = len < 0 ? 0xFFFFFFFFu : end;
     p.row_group[r] = shares ? g : G;
-    p.row_pre[r + 1] = len > 0 && end > base ? (end + 31) / 32 - base / 32 : 0;
+    units = len > 0 && end > base ? (end + 31) / 32 - base / 32 : 0;
+    p.row_pre[r + 1] = units;
     if (shares) atomicMin(&p.g_row[g], r);
   }
-  __syncthreads();
-  for (uint32_t i = tid; i < G; i += kAttendThreads) {
+  if (small && wave == 0) {
+    units = wave_scan<false>(units);
+    if (lane < rows) p.row_pre[lane + 1] = units;
+  }
+  if (G || !small) __syncthreads();
+  auto units_of = [&](uint32_t i) {
     const uint32_t cols = (p.g_start[i + 1] - p.g_start[i]) * a.ratio;
-    const uint32_t units = p.g_row[i] < rows ? (p.g_len[i] + 31) / 32 : 0;
-    p.g_pre[i + 1] = units * ((cols + kCap - 1) / kCap);
+    return p.g_row[i] < rows ? (p.g_len[i] + 31) / 32 * ((cols + kCap - 1) / kCap) : 0;
+  };
+  if (small) {
+    if (G && wave == 1) {
+      units = wave_scan<false>(lane < G ? units_of(lane) : 0);
+      if (lane < G) p.g_pre[lane + 1] = units;
+    }
+    __syncthreads();
+  } else {
+    for (uint32_t i = tid; i < G; i += kAttendThreads) p.g_pre[i + 1] = units_of(i);
+    block_scan<false>(p.row_pre + 1, rows, carry);  // its barriers serve g_pre too
+    if (G) block_scan<false>(p.g_pre + 1, G, carry);
   }
-  block_scan<false>(p.row_pre + 1, rows, carry);  // its barriers serve g_pre too
-  if (G) block_scan<false>(p.g_pre + 1, G, carry);
-  if (tid == 0) {
-    p.head[0] = p.g_pre[G];
-    p.head[1] = p.row_pre[rows];
-    const uint64_t prefix = static_cast<uint64_t>(p.head[0]) * a.hkv, own = static_cast<uint64_t>(p.head[1]) * a.hkv;
-    // prefixes to the first half of the workgroups, own positions to the second
-    // (one of each per compute unit); all take part in the prefixes where there
-    // is little else.  At least four units, one per wavefront, for a
-    // workgroup's part of a prefix.
-    const uint32_t wp = own < prefix / 2 ? gridDim.x : gridDim.x - a.own_wgs;
-    const uint32_t wo = a.own_wgs * (a.ratio <= kWaveRatio ? 4 : 1);
-    const uint64_t qp = wp ? max((prefix + wp - 1) / wp, uint64_t{4}) : 4;
-    const uint64_t qo = max((own + wo - 1) / wo, uint64_t{1});
-    p.head[2] = static_cast<uint32_t>(qp);
-    p.head[3] = static_cast<uint32_t>(qp >> 32);
-    p.head[4] = static_cast<uint32_t>(qo);
-    p.head[5] = static_cast<uint32_t>(qo >> 32);
-    p.head[6] = wp;
-    p.head[7] = 0;
-  }
-  __syncthreads();
+  Split s;
+  s.prefix_units = uniform(p.g_pre[G]);
+  s.own_units = uniform(p.row_pre[rows]);
+  const uint64_t prefix = static_cast<uint64_t>(s.prefix_units) * a.hkv, own = static_cast<uint64_t>(s.own_units) * a.hkv;
+  // prefixes to the first half of the workgroups, own positions to the second
+  // (one of each per compute unit); all take part in the prefixes where there is
+  // little else.  At least four units, one per wavefront, for a workgroup's
+  // part of a prefix.
+  s.prefix_wgs = own < prefix / 2 ? gridDim.x : gridDim.x - a.own_wgs;
+  const uint32_t owners = a.own_wgs * (a.ratio <= kWaveRatio ? 4 : 1);
+  s.prefix_quota = s.prefix_wgs ? max((prefix + s.prefix_wgs - 1) / s.prefix_wgs, uint64_t{4}) : 4;
+  s.own_quota = max((own + owners - 1) / owners, uint64_t{1});
   if (blockIdx.x == 0) {
     u32x4_t* rec = reinterpret_cast<u32x4_t*>(a.plan);
-    if (tid < 2) rec[tid] = u32x4_t{p.head[4 * tid], p.head[4 * tid + 1], p.head[4 * tid + 2], p.head[4 * tid + 3]};
+    if (tid == 0) {
+      rec[0] = u32x4_t{s.prefix_units, s.own_units, 0, 0};
+      rec[1] = u32x4_t{static_cast<uint32_t>(s.prefix_quota), static_cast<uint32_t>(s.prefix_quota >> 32),
+                       static_cast<uint32_t>(s.own_quota), static_cast<uint32_t>(s.own_quota >> 32)};
+    }
     for (uint32_t r = tid; r < rows; r += kAttendThreads)
       rec[2 + r] = u32x4_t{p.row_pre[r], p.row_pre[r + 1] - p.row_pre[r], p.row_group[r], p.row_end[r]};
     for (uint32_t i = tid; i < G; i += kAttendThreads) rec[2 + rows + i] = u32x4_t{p.g_start[i], p.g_pre[i], p.g_len[i], 0};
   }
+  return s;
 }
 
 // A worker's part of one item; all fields wave-uniform.
@@ -795,7 +827,7 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("" ::: "memory");
 }
 
-// The workgroup's part of an item of more than 32 columns: the wavefronts take
+// The workgroup's part of an item of more than 16 columns: the wavefronts take
 // 16 NT columns each of the same units, which pass through a ring of slots in
 // LDS, loaded straight from the pages (a quarter of a unit's rows per
 // wavefront, kRing - 1 units ahead), so a unit is read once per workgroup.
@@ -960,14 +992,14 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
   const Plan p(reinterpret_cast<uint32_t*>(lds + sizeof(LdsFixed)), rows, G);
   uint8_t* big = lds + sizeof(LdsFixed) + (Plan::words(rows, G) * 4 + 15) / 16 * 16;
   Join<D, 4>& join = *reinterpret_cast<Join<D, 4>*>(big);
-  make_plan(a, p, s.carry);
-  const uint32_t prefix_units = uniform(p.head[0]), own_units = uniform(p.head[1]);
+  const Split split = make_plan(a, p, s.carry);
+  const uint32_t prefix_units = split.prefix_units, own_units = split.own_units;
   if (prefix_units) {
-    const uint64_t quota = uniform(p.head[2]) | static_cast<uint64_t>(uniform(p.head[3])) << 32;
+    const uint64_t quota = split.prefix_quota;
     const uint64_t total = static_cast<uint64_t>(prefix_units) * a.hkv;
     // workgroups go round the 8 XCDs in turn: neighbours in the order of the
     // units, which share a head's pages, on one XCD if all have work
-    const uint32_t wp = uniform(p.head[6]);
+    const uint32_t wp = split.prefix_wgs;
     const bool near = wp % 8 == 0 && blockIdx.x < wp && total > quota * (wp / 2);
     const uint64_t wg = near ? blockIdx.x % 8 * (wp / 8) + blockIdx.x / 8 : blockIdx.x;
     const uint64_t end = min(wg * quota + quota, total);
@@ -976,8 +1008,6 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
       const Segment it = prefix_segment(a, p, head, static_cast<uint32_t>(at % prefix_units), end - at, wg);
       if (it.cols <= 16)
         attend_turns<D, 1, 4>(a, it, s, join);
-      else if (D <= 128 && it.cols <= 32)
-        attend_turns<D, D <= 128 ? 2 : 1, 4>(a, it, s, join);
       else if (it.cols <= 64)
         attend_shared<D, 1>(a, it, big);
       else
@@ -986,7 +1016,7 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
     }
   }
   if (own_units) {
-    const uint64_t quota = uniform(p.head[4]) | static_cast<uint64_t>(uniform(p.head[5])) << 32;
+    const uint64_t quota = split.own_quota;
     const uint64_t total = static_cast<uint64_t>(own_units) * a.hkv;
     // from the last workgroup down
     const uint32_t wg = gridDim.x - 1 - blockIdx.x;
@@ -1056,7 +1086,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs
   const u32x4_t* rec = reinterpret_cast<const u32x4_t*>(a.plan);
   const u32x4_t h0 = rec[0], h1 = rec[1], row = rec[2 + r];
   const uint32_t prefix_units = h0[0], own_units = h0[1], pre = row[0], units = row[1], g = row[2];
-  const uint64_t quota_p = h0[2] | static_cast<uint64_t>(h0[3]) << 32, quota_o = h1[0] | static_cast<uint64_t>(h1[1]) << 32;
+  const uint64_t quota_p = h1[0] | static_cast<uint64_t>(h1[1]) << 32, quota_o = h1[2] | static_cast<uint64_t>(h1[3]) << 32;
   if (static_cast<int32_t>(row[3]) < 0) return;  // padding
   const bool shares = g < a.n_groups;
   // the worker that has a unit (32-bit division where the numbers allow)
