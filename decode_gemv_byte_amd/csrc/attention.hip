@@ -49,7 +49,7 @@ __device__ __forceinline__ float lane_xor(float v, int mask) {
 
 struct PageArgs {
   const int32_t* ids;
-  uint64_t ld;
+  uint32_t ld;
   uint32_t n_pages, stride8;   // pages; elements / 8 from page to page
   uint32_t rows, cols, shift;  // page_len = 1 << shift
 };
@@ -60,12 +60,11 @@ struct HeadsArgs {
   const uint16_t *q_weight, *k_weight;
   const float* freqs;
   const int32_t *positions, *rows;
-  uint64_t ld_q, ld_k, ld_v, ld_q_out, ld_k_out;
   PageArgs pages;
-  uint32_t hq, hk, hv;
-  uint32_t tokens, d, half;  // half: dims / 2 (0: no rotation)
-  uint32_t style, split;     // split: wavefronts that share a token's passes
-  float eps, inv_d;
+  uint32_t ld_q, ld_k, ld_v, ld_q_out, ld_k_out;  // elements / 8
+  uint32_t tokens, split;                         // split: wavefronts that share a token's passes
+  float eps;
+  uint16_t hq, hk, hv, d, half, style;            // half: dims / 2 (0: no rotation)
 };
 
 // Sum over the G lanes of a head, in each of them (DPP: swaps within four lanes,
@@ -99,6 +98,7 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
   constexpr uint32_t kHeads = kWave / G;  // heads of a pass
   const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave);
   const uint32_t all = a.hq + a.hk + a.hv;
+  const float inv_d = 1.f / static_cast<float>(a.d);
   const uint64_t n = static_cast<uint64_t>(a.tokens) * a.split;
   const uint32_t c = lane % G, sub = lane / G;
   const bool on = 8 * c < a.d;
@@ -113,6 +113,7 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
     const uint32_t t = static_cast<uint32_t>(w / a.split);
     const int32_t pos = a.positions[t];
     const uint32_t row = a.rows ? static_cast<uint32_t>(a.rows[t]) : t;
+    auto row_of = [&](uint32_t ld) { return static_cast<uint64_t>(t) * ld * 8; };  // the token's first element
     float cs[4], sn[4];
     uint64_t slot = 0;  // element offset of the token's slot, less the head's part
     bool stored = true;
@@ -125,9 +126,9 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
         head[u] = (part * U + u) * kHeads + sub;
         const bool live = on && head[u] < all;
         const bool is_q = head[u] < a.hq, is_k = !is_q && head[u] < a.hq + a.hk;
-        const uint16_t* src = is_q ? a.q + t * a.ld_q + static_cast<uint64_t>(head[u]) * a.d
-                              : is_k ? a.k + t * a.ld_k + static_cast<uint64_t>(head[u] - a.hq) * a.d
-                                     : a.v + t * a.ld_v + static_cast<uint64_t>(head[u] - a.hq - a.hk) * a.d;
+        const uint16_t* src = is_q ? a.q + row_of(a.ld_q) + (head[u]) * a.d
+                              : is_k ? a.k + row_of(a.ld_k) + (head[u] - a.hq) * a.d
+                                     : a.v + row_of(a.ld_v) + (head[u] - a.hq - a.hk) * a.d;
         const uint16_t* wsrc = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
         xa[u] = xb[u] = wa[u] = wb[u] = u32x2_t{0, 0};
         if (live) {
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
         if (a.pages.ids) {
           const uint32_t at = static_cast<uint32_t>(pos) >> a.pages.shift;
           stored = row < a.pages.rows && at < a.pages.cols;
-          const int32_t id = stored ? a.pages.ids[row * a.pages.ld + at] : -1;
+          const int32_t id = stored ? a.pages.ids[static_cast<uint64_t>(row) * a.pages.ld + at] : -1;
           stored = static_cast<uint32_t>(id) < a.pages.n_pages;
           if (stored)
             slot = static_cast<uint64_t>(id) * a.pages.stride8 * 8 +
@@ -172,7 +173,7 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
         for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
         sum = head_sum<G>(sum);
         if (is_q ? a.q_weight != nullptr : is_k && a.k_weight != nullptr) {
-          const float r = 1.f / sqrtf(fmaf(sum, a.inv_d, a.eps));
+          const float r = 1.f / sqrtf(fmaf(sum, inv_d, a.eps));
           const float g[8] = {bf16_lo(wa[u][0]), bf16_hi(wa[u][0]), bf16_lo(wa[u][1]), bf16_hi(wa[u][1]),
                               bf16_lo(wb[u][0]), bf16_hi(wb[u][0]), bf16_lo(wb[u][1]), bf16_hi(wb[u][1])};
 #pragma unroll
@@ -204,11 +205,11 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
         if (!on || head[u] >= all || !(is_q || stored)) continue;
         uint16_t* dst;
         if (is_q) {
-          dst = a.q_out + t * a.ld_q_out + static_cast<uint64_t>(head[u]) * a.d;
+          dst = a.q_out + row_of(a.ld_q_out) + head[u] * a.d;
         } else {
           const uint32_t h = is_k ? head[u] - a.hq : head[u] - a.hq - a.hk;
           dst = (is_k ? a.k_out : a.v_out) + (a.pages.ids ? slot + (static_cast<uint64_t>(h) << a.pages.shift) * a.d
-                                                          : t * a.ld_k_out + static_cast<uint64_t>(h) * a.d);
+                                                          : row_of(a.ld_k_out) + h * a.d);
         }
         *reinterpret_cast<u32x2_t*>(dst + at_a) = ra;
         *reinterpret_cast<u32x2_t*>(dst + at_b) = rb;
@@ -951,7 +952,7 @@ __device__ __forceinline__ Segment own_segment(const AttendArgs& a, const Plan& 
   it.row0 = r;
   it.col0 = 0;
   it.cols = a.ratio;
-  it.ids = a.pages.ids + r * a.pages.ld;
+  it.ids = a.pages.ids + static_cast<uint64_t>(r) * a.pages.ld;
   it.p0 = uniform(p.base(r));
   it.p1 = uniform(p.row_end[r]);
   const uint32_t first = it.p0 / 32, units = (it.p1 + 31) / 32 - first;
@@ -974,7 +975,7 @@ __device__ __forceinline__ Segment prefix_segment(const AttendArgs& a, const Pla
   it.row0 = uniform(p.g_start[i]);
   it.col0 = block * kCap;
   it.cols = min((uniform(p.g_start[i + 1]) - it.row0) * a.ratio - it.col0, kCap);
-  it.ids = a.pages.ids + r * a.pages.ld;
+  it.ids = a.pages.ids + static_cast<uint64_t>(r) * a.pages.ld;
   it.p0 = 0;
   it.p1 = len;
   it.u0 = done;
@@ -1061,7 +1062,7 @@ __global__ __launch_bounds__(AttendShape<D>::kRowWaves * kWave) void k_attend_ro
   it.row0 = r;
   it.col0 = blockIdx.y * kWaveRatio;
   it.cols = min(a.ratio - it.col0, kWaveRatio);
-  it.ids = a.pages.ids + r * a.pages.ld;
+  it.ids = a.pages.ids + static_cast<uint64_t>(r) * a.pages.ld;
   it.p0 = 0;
   it.p1 = min(static_cast<uint32_t>(len), a.pages.cols << a.pages.shift);
   it.u0 = 0;
@@ -1175,11 +1176,11 @@ uint32_t cu_count() {
   return static_cast<uint32_t>(n);
 }
 
-// Most heads of one tensor and elements of a page: products of sizes stay far
-// below 2^63 with strides below 2^40.
-constexpr uint32_t kMaxHeads = 65536;
+// Most heads of one tensor, and strides that fit 32 bits in pieces of 8 elements.
+constexpr uint32_t kMaxHeads = 65535;
 constexpr size_t kMaxLds = 160 * 1024;
-constexpr uint64_t kMaxStride = uint64_t{1} << 40;
+constexpr uint64_t kMaxStride = uint64_t{0xFFFFFFFF} * 8;
+uint32_t pieces(uint64_t ld) { return static_cast<uint32_t>(ld / 8); }
 
 nwc_status check_rope(const nwc_rope* rope, uint32_t d) {
   if (!rope || rope->dims == 0) return NWC_OK;
@@ -1204,17 +1205,17 @@ nwc_status check_cache(const nwc_cache* c, const nwc_page_table* t, PageArgs* p)
       c->page_len == 0 || c->reserved)
     return NWC_ERR_INVALID_ARG;
   if (c->page_len < 16 || c->page_len > 1024 || (c->page_len & (c->page_len - 1))) return NWC_ERR_UNSUPPORTED;
-  if (c->page_stride < static_cast<uint64_t>(c->kv_heads) * c->page_len * c->head_dim || c->page_stride / 8 > 0xFFFFFFFF)
+  if (c->page_stride < static_cast<uint64_t>(c->kv_heads) * c->page_len * c->head_dim || c->page_stride > kMaxStride)
     return NWC_ERR_INVALID_ARG;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % 8) return NWC_ERR_ALIGNMENT;
   p->n_pages = static_cast<uint32_t>(c->n_pages);
-  p->stride8 = static_cast<uint32_t>(c->page_stride / 8);
+  p->stride8 = pieces(c->page_stride);
   p->shift = static_cast<uint32_t>(__builtin_ctz(c->page_len));
   if (t) {
-    if (!t->ids || t->rows == 0 || t->cols == 0 || t->ld < t->cols || t->ld > kMaxStride) return NWC_ERR_INVALID_ARG;
+    if (!t->ids || t->rows == 0 || t->cols == 0 || t->ld < t->cols || t->ld > 0xFFFFFFFF) return NWC_ERR_INVALID_ARG;
     if (!aligned(t->ids, 4)) return NWC_ERR_ALIGNMENT;
     p->ids = t->ids;
-    p->ld = t->ld;
+    p->ld = static_cast<uint32_t>(t->ld);
     p->rows = t->rows;
     p->cols = t->cols;
   }
@@ -1222,8 +1223,7 @@ nwc_status check_cache(const nwc_cache* c, const nwc_page_table* t, PageArgs* p)
 }
 
 nwc_status launch_heads(HeadsArgs& a, hipStream_t s) {
-  const uint32_t all = a.hq + a.hk + a.hv, lanes = a.d / 8;
-  a.inv_d = 1.f / static_cast<float>(a.d);
+  const uint32_t all = a.hq + a.hk + a.hv, lanes = a.d / 8u;
   const uint32_t cus = cu_count();
   if (cus == 0) return NWC_ERR_HIP;
   const uint32_t g = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
@@ -1247,8 +1247,8 @@ bool heads_dim_ok(uint32_t d) { return d >= 8 && d <= 256 && d % 8 == 0; }
 void set_rope(HeadsArgs* a, const nwc_rope* rope) {
   if (rope && rope->dims) {
     a->freqs = rope->freqs;
-    a->half = rope->dims / 2;
-    a->style = rope->style;
+    a->half = static_cast<uint16_t>(rope->dims / 2);
+    a->style = static_cast<uint16_t>(rope->style);
   }
 }
 
@@ -1334,15 +1334,15 @@ nwc_status nwc_qk_norm_rope(const nwc_heads* q, const nwc_heads* k, uint32_t tok
   if (st) return st;
   HeadsArgs a = {};
   if (q) {
-    a.q = q->src; a.q_out = q->dst; a.q_weight = q->weight; a.ld_q = q->ld_src; a.ld_q_out = q->ld_dst; a.hq = q->heads;
+    a.q = q->src; a.q_out = q->dst; a.q_weight = q->weight; a.ld_q = pieces(q->ld_src); a.ld_q_out = pieces(q->ld_dst); a.hq = static_cast<uint16_t>(q->heads);
   }
   if (k) {
-    a.k = k->src; a.k_out = k->dst; a.k_weight = k->weight; a.ld_k = k->ld_src; a.ld_k_out = k->ld_dst; a.hk = k->heads;
+    a.k = k->src; a.k_out = k->dst; a.k_weight = k->weight; a.ld_k = pieces(k->ld_src); a.ld_k_out = pieces(k->ld_dst); a.hk = static_cast<uint16_t>(k->heads);
   }
   set_rope(&a, rope);
   a.positions = positions_dev;
   a.tokens = tokens;
-  a.d = head_dim;
+  a.d = static_cast<uint16_t>(head_dim);
   a.eps = eps;
   return launch_heads(a, static_cast<hipStream_t>(stream));
 }
@@ -1365,15 +1365,15 @@ nwc_status nwc_kv_append(const nwc_cache* cache, const nwc_page_table* table, co
   if (!rows_dev && tokens > table->rows) return NWC_ERR_INVALID_ARG;  // token t is row t
   if (!aligned(v_dev, 16) || ld_v % 8 || !aligned(positions_dev, 4) || !aligned(rows_dev, 4)) return NWC_ERR_ALIGNMENT;
   if (q) {
-    a.q = q->src; a.q_out = q->dst; a.q_weight = q->weight; a.ld_q = q->ld_src; a.ld_q_out = q->ld_dst; a.hq = q->heads;
+    a.q = q->src; a.q_out = q->dst; a.q_weight = q->weight; a.ld_q = pieces(q->ld_src); a.ld_q_out = pieces(q->ld_dst); a.hq = static_cast<uint16_t>(q->heads);
   }
-  a.k = k->src; a.k_out = cache->k; a.k_weight = k->weight; a.ld_k = k->ld_src; a.hk = k->heads;
-  a.v = v_dev; a.v_out = cache->v; a.ld_v = ld_v; a.hv = k->heads;
+  a.k = k->src; a.k_out = cache->k; a.k_weight = k->weight; a.ld_k = pieces(k->ld_src); a.hk = static_cast<uint16_t>(k->heads);
+  a.v = v_dev; a.v_out = cache->v; a.ld_v = pieces(ld_v); a.hv = a.hk;
   set_rope(&a, rope);
   a.positions = positions_dev;
   a.rows = rows_dev;
   a.tokens = tokens;
-  a.d = d;
+  a.d = static_cast<uint16_t>(d);
   a.eps = eps;
   return launch_heads(a, static_cast<hipStream_t>(stream));
 }

@@ -360,7 +360,8 @@ nwc_status nwc_read_probe(const void *buf_dev, size_t bytes, uint32_t *sink_dev,
  * outside the described memory. */
 
 /* Heads of one tensor: [tokens, heads, head_dim], a token's heads side by
- * side, tokens ld elements apart (ld % 8 == 0, pointers 16-byte aligned).
+ * side, tokens ld elements apart (ld % 8 == 0, below 2^35; pointers 16-byte
+ * aligned).  At most 65535 heads.
  * weight (device, head_dim BF16, 16-byte aligned): each head is divided by
  * the root of its mean square (+ eps) and multiplied by it; NULL: no norm.
  * dst may be src itself with the same ld (each head is read before it is
