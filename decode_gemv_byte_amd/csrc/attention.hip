@@ -748,6 +748,106 @@ __device__ __forceinline__ void walk(const AttendArgs& a, const Segment& it, uin
   }
 }
 
+// Wait until at most N of this wavefront's vector memory operations are left.
+template <int N>
+__device__ __forceinline__ void wait_vmem() {
+  static_assert(N >= 0 && N < 64, "vmcnt holds 6 bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 0xF) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
+
+// The same with the keys by way of LDS: two slots of the wavefront's own, filled
+// straight from the pages, whole rows at a time, two units ahead.  Read into
+// registers as the product wants them, the lanes of a load touch 64 cache lines
+// for 16 bytes each, and a compute unit gets 25 B a clock of them.
+template <int D, int NT>
+__device__ __forceinline__ void walk_lds(const AttendArgs& a, const Segment& it, uint32_t u, uint32_t step, uint8_t* slots,
+                                         Sums<D, NT>& acc) {
+  if (u >= it.u1) return;
+  constexpr int kLoads = D / 16, kSlot = 64 * D;
+  constexpr uint32_t kPieces = D / 8;
+  const uint32_t lane = __lane_id();
+  const bool upper = lane / 16 >= 2;
+  u32x4_t qf[AttendShape<D>::kKs][NT];
+  load_queries<D, NT>(a, it, 0, qf);
+  int32_t id0 = page_id(a, it, 32 * u), id1 = page_id(a, it, 32 * u + 16);
+  PagePart lo = page_part(a, it, id0, 32 * u, D), hi = page_part(a, it, id1, 32 * u + 16, D);
+  uint32_t ahead = u + step;  // the unit whose keys are asked for next
+  id0 = page_id(a, it, 32 * ahead);
+  id1 = page_id(a, it, 32 * ahead + 16);
+  auto keys = [&](const PagePart& l, const PagePart& h, uint8_t* to) {
+    asm volatile("" ::: "memory");  // in the order that the waits count
+#pragma unroll
+    for (int y = 0; y < kLoads; ++y) {
+      const uint32_t piece = 64 * y + lane, row = piece / kPieces, c = piece % kPieces;
+      const uint32_t from = (row % 16) * D + 8 * key_piece<D, true>(row, c);
+      __builtin_amdgcn_global_load_lds(a.k + (y < kLoads / 2 ? l.off : h.off) + from, to + 1024 * y, 16, 0, 0);
+    }
+    asm volatile("" ::: "memory");
+  };
+  // the queries have to be there before the loads in flight are counted
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int k = 0; k < AttendShape<D>::kKs; ++k) asm volatile("" : "+v"(qf[k][c]));
+  Unit<D, NT> x;
+  bool good = upper ? hi.known : lo.known;
+  keys(lo, hi, slots);
+  x.load_v(a, lo, hi);
+  if (ahead < it.u1) {
+    lo = page_part(a, it, id0, 32 * ahead, D);
+    hi = page_part(a, it, id1, 32 * ahead + 16, D);
+    keys(lo, hi, slots + kSlot);
+    id0 = page_id(a, it, 32 * (ahead + step));
+    id1 = page_id(a, it, 32 * (ahead + step) + 16);
+  }
+  uint32_t slot = 0;
+  for (;;) {
+    // lo, hi: the pages of the next unit, whose keys are in flight or here
+    const uint32_t next = u + step;
+    const bool more = next < it.u1;
+    // behind this unit's keys: a unit's values (8 loads at least), and the next unit's keys
+    if (more)
+      wait_vmem<8 + kLoads>();
+    else
+      wait_vmem<8>();
+    x.read_k(slots + slot);
+    f32x4_t sc[2][NT];
+    x.scores(qf, sc);
+    const PagePart vlo = lo, vhi = hi;
+    ahead = next + step;
+    if (ahead < it.u1) {
+      lo = page_part(a, it, id0, 32 * ahead, D);
+      hi = page_part(a, it, id1, 32 * ahead + 16, D);
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slot's reads are done
+      keys(lo, hi, slots + slot);
+      id0 = page_id(a, it, 32 * (ahead + step));
+      id1 = page_id(a, it, 32 * (ahead + step) + 16);
+    }
+    acc.take(sc, x.vr, it, 32 * u, good, a.scale2);
+    if (!more) return;
+    x.load_v(a, vlo, vhi);
+    good = upper ? vhi.known : vlo.known;
+    u = next;
+    slot ^= kSlot;
+  }
+}
+
+// Bytes of a wavefront's two key slots.
+constexpr uint32_t key_slots(int d) { return 2 * 64 * d; }
+// Whether W wavefronts' slots fit beside what else lies in LDS.
+constexpr bool keys_fit(int d, int waves) { return waves * key_slots(d) <= (waves == 4 ? 96u : 128u) * 1024; }
+
+template <int D, int NT, int W>
+__device__ __forceinline__ void walk_units(const AttendArgs& a, const Segment& it, uint32_t u, uint32_t step, uint8_t* slots,
+                                           Sums<D, NT>& acc) {
+  if constexpr (keys_fit(D, W))
+    walk_lds<D, NT>(a, it, u, step, slots, acc);
+  else
+    walk<D, NT>(a, it, u, step, acc);
+}
+
 // LDS of a workgroup: the fixed part, then the plan, then the ring of slots or
 // the sums that the wavefronts exchange (never both).
 struct LdsFixed {
@@ -760,14 +860,15 @@ using Join = float[W][16][AttendShape<D>::kJLd];
 // An item of at most 16 NT columns by a workgroup of W wavefronts, which take its
 // units in turn; their sums are brought to one maximum and added in order.
 template <int D, int NT, int W>
-__device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment& it, LdsFixed& s, Join<D, W>& join) {
+__device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment& it, LdsFixed& s, uint8_t* big) {
   constexpr int kDt = AttendShape<D>::kDt;
+  Join<D, W>& join = *reinterpret_cast<Join<D, W>*>(big);  // in the place of the key slots
   const uint32_t wave = uniform(threadIdx.x / kWave), tid = threadIdx.x;
   const uint32_t n = __lane_id() % 16, g = __lane_id() / 16;
   Sums<D, NT> acc;
-  walk<D, NT>(a, it, it.u0 + wave, W, acc);
+  __syncthreads();  // the last readers of what lies there are done
+  walk_units<D, NT, W>(a, it, it.u0 + wave, W, big + wave * key_slots(D), acc);
   acc.finish();
-  __syncthreads();  // the exchange's last readers are done
   if (g == 0)
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
@@ -992,7 +1093,6 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
   const uint32_t rows = a.pages.rows, G = a.n_groups;
   const Plan p(reinterpret_cast<uint32_t*>(lds + sizeof(LdsFixed)), rows, G);
   uint8_t* big = lds + sizeof(LdsFixed) + (Plan::words(rows, G) * 4 + 15) / 16 * 16;
-  Join<D, 4>& join = *reinterpret_cast<Join<D, 4>*>(big);
   const Split split = make_plan(a, p, s.carry);
   const uint32_t prefix_units = split.prefix_units, own_units = split.own_units;
   if (prefix_units) {
@@ -1008,7 +1108,7 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
       const uint32_t head = static_cast<uint32_t>(at / prefix_units);
       const Segment it = prefix_segment(a, p, head, static_cast<uint32_t>(at % prefix_units), end - at, wg);
       if (it.cols <= 16)
-        attend_turns<D, 1, 4>(a, it, s, join);
+        attend_turns<D, 1, 4>(a, it, s, big);
       else if (it.cols <= 64)
         attend_shared<D, 1>(a, it, big);
       else
@@ -1022,6 +1122,8 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
     // from the last workgroup down
     const uint32_t wg = gridDim.x - 1 - blockIdx.x;
     if (wg >= a.own_wgs) return;
+    __syncthreads();  // the prefixes' last readers of LDS are done
+    uint8_t* slots = big + uniform(threadIdx.x / kWave) * key_slots(D);
     const uint64_t worker = a.ratio <= kWaveRatio ? static_cast<uint64_t>(uniform(threadIdx.x / kWave)) * a.own_wgs + wg : wg;
     const uint64_t end = min(worker * quota + quota, total);
     for (uint64_t at = worker * quota; at < end;) {
@@ -1029,12 +1131,12 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
       const Segment it = own_segment(a, p, head, static_cast<uint32_t>(at % own_units), end - at, worker);
       if (a.ratio <= 16) {
         Sums<D, 1> acc;
-        walk<D, 1>(a, it, it.u0, 1, acc);
+        walk_units<D, 1, 4>(a, it, it.u0, 1, slots, acc);
         acc.finish();
         acc.store(a, it, 0);
       } else if (a.ratio <= kWaveRatio) {
         Sums<D, 2> acc;
-        walk<D, 2>(a, it, it.u0, 1, acc);
+        walk_units<D, 2, 4>(a, it, it.u0, 1, slots, acc);
         acc.finish();
         acc.store(a, it, 0);
       } else {
@@ -1053,7 +1155,6 @@ __global__ __launch_bounds__(AttendShape<D>::kRowWaves * kWave) void k_attend_ro
   constexpr int kRowWaves = AttendShape<D>::kRowWaves;
   __shared__ LdsFixed s;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  Join<D, kRowWaves>& join = *reinterpret_cast<Join<D, kRowWaves>*>(lds);
   const uint32_t r = blockIdx.x / a.hkv;
   const int32_t len = sload(a.lengths, r);
   if (len < 0) return;  // padding
@@ -1070,9 +1171,9 @@ __global__ __launch_bounds__(AttendShape<D>::kRowWaves * kWave) void k_attend_ro
   it.direct = true;
   it.slot = 0;
   if (it.cols <= 16)
-    attend_turns<D, 1, kRowWaves>(a, it, s, join);
+    attend_turns<D, 1, kRowWaves>(a, it, s, lds);
   else
-    attend_turns<D, 2, kRowWaves>(a, it, s, join);
+    attend_turns<D, 2, kRowWaves>(a, it, s, lds);
 }
 
 // One workgroup per row and query head: the partial sums of its column, prefix
@@ -1298,7 +1399,7 @@ nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
   const uint32_t covers = a.pages.cols << a.pages.shift;
   if (!a.n_groups && covers <= (2 * a.pages.rows * a.hkv >= a.own_wgs ? kRowsMostMany : kRowsMost)) {
     constexpr int kRowWaves = AttendShape<D>::kRowWaves;
-    constexpr size_t lds = sizeof(Join<D, kRowWaves>);
+    constexpr size_t lds = std::max(sizeof(Join<D, kRowWaves>), keys_fit(D, kRowWaves) ? size_t{kRowWaves * key_slots(D)} : 0);
     static_assert(sizeof(LdsFixed) + lds <= kMaxLds, "LDS");
     if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend_rows<D>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds)) != hipSuccess)
@@ -1307,7 +1408,7 @@ nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
                   dim3(kRowWaves * kWave), lds, s, a);
   }
   const size_t fixed = sizeof(LdsFixed) + (static_cast<size_t>(Plan::words(a.pages.rows, a.n_groups)) * 4 + 15) / 16 * 16;
-  constexpr size_t big = std::max(sizeof(Join<D, 4>), size_t{AttendShape<D>::kRing * 128 * D});
+  constexpr size_t big = std::max({sizeof(Join<D, 4>), size_t{AttendShape<D>::kRing * 128 * D}, keys_fit(D, 4) ? size_t{4 * key_slots(D)} : 0});
   static_assert(sizeof(LdsFixed) + 4 * Plan::words(kAttendMaxRows, kAttendMaxGroups) + 16 + big <= kMaxLds, "LDS");
   const size_t lds = fixed + big;
   if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<D>), hipFuncAttributeMaxDynamicSharedMemorySize,
