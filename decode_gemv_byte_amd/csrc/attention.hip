@@ -1385,19 +1385,23 @@ nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uin
 
 
 
-// Positions that a table may cover for k_attend_rows to take it: any call up to
-// 512, calls with a workgroup for half the compute units up to 1024.  Measured
-// (32 / 8 heads of 128, all rows full, us a call in a graph, k_attend_rows and
-// k_attend + k_attend_join): 1 row of 256: 6.1 and 7.9, 512: 8.5 and 8.4, 1024:
-// 12.8 and 8.4; 16 rows of 512: 9.9 and 14.2, 1024: 14.9 and 18.8; 64 rows of
-// 1024: 50.8 and 55.9.  Longer ones win less and lose more where one row is
-// much longer than the others.
-constexpr uint32_t kRowsMost = 512, kRowsMostMany = 1024;
+// Positions that a table may cover for k_attend_rows to take it, by the number of
+// its workgroups (rows times key-value heads) against the compute units.
+// Measured (32 / 8 heads of 128, us a call in a graph, k_attend_rows and k_attend
+// + k_attend_join): 1 row of 512: 5.7 and 7.7, 1024: 8.2 and 7.7; 4 rows of 1024:
+// 9.4 and 10.5, 2048: 14.4 and 12.6; 16 rows of 2048: 28.4 and 30.7, ragged to
+// 2048: 16.0 and 18.3, to 4096: 46.4 and 33.3; 64 rows of 2048: 95.5 and 100.1.
+// Heads of 192 and 256, whose keys do not go by LDS here, keep few wavefronts:
+// 1 row of 512 (8 / 2 heads of 256): 13.2 and 10.3.
+uint32_t rows_most(uint32_t d, uint64_t groups, uint32_t cus) {
+  if (d > 128) return 128;
+  return 2 * groups >= cus ? 2048 : 8 * groups >= cus ? 1024 : 512;
+}
 
 template <int D>
 nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
-  const uint32_t covers = a.pages.cols << a.pages.shift;
-  if (!a.n_groups && covers <= (2 * a.pages.rows * a.hkv >= a.own_wgs ? kRowsMostMany : kRowsMost)) {
+  const uint64_t items = static_cast<uint64_t>(a.pages.rows) * a.hkv;
+  if (!a.n_groups && a.pages.cols << a.pages.shift <= rows_most(D, items, a.own_wgs)) {
     constexpr int kRowWaves = AttendShape<D>::kRowWaves;
     constexpr size_t lds = std::max(sizeof(Join<D, kRowWaves>), keys_fit(D, kRowWaves) ? size_t{kRowWaves * key_slots(D)} : 0);
     static_assert(sizeof(LdsFixed) + lds <= kMaxLds, "LDS");
