@@ -91,8 +91,9 @@ __device__ __forceinline__ float head_sum(float v) {
 // a lane needs 4 angles, and those serve all heads of the token. A wavefront
 // takes U passes at a time, their loads together; `split` wavefronts share a
 // token, so that few tokens still fill the GPU.
-// 16384 tokens of 32 + 8 heads of 128 (336 MB): see the measurements at
-// launch_heads.
+// 16384 tokens of 32 + 8 heads of 128, 336 MB read and written: 73 us, 4.6 TB/s
+// of the 4.9 that a large copy moves; one token: 2.6 us.  (With 8 neighbouring
+// components a lane, their partners by a lane permute and 8 angles: 94 and 3.7.)
 template <int G, int U>
 __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
   constexpr uint32_t kHeads = kWave / G;  // heads of a pass
@@ -231,20 +232,29 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
 // any lengths.  An item cut between ranges, or a row with both kinds, leaves
 // partial sums in the workspace, which k_attend_join adds.
 //
-// A unit is computed by one wavefront in registers.  S^T = K Q^T on the matrix
-// cores, the keys straight from the page (lane: one position, 8 components);
-// with the positions of the two 16-row tiles interleaved (tile t, row m is
+// A unit is computed by one wavefront.  S^T = K Q^T on the matrix cores (a lane's
+// keys: one position, 8 components); with the positions of the two 16-row tiles interleaved (tile t, row m is
 // position 8 (m / 4) + 4 t + m % 4) the result leaves each lane the 8
 // neighbouring positions 8 g .. 8 g + 7 of one column, g = lane / 16, which is
 // just the operand that O^T = V^T P^T takes.  Of the values a lane takes D / 16
 // neighbouring components of its 8 positions and turns that block by one byte
 // permute per operand register.  No value crosses lanes in the loop but the
-// column's maximum, and that only when it grows by more than 2^8.
+// column's maximum, and that only when the weights have outgrown it by 2^11.
+//
+// What bounds it, 32 / 8 heads of 128 on one MI355X (large copies move 4.9 TB/s,
+// large reads 6.2 TB/s):
+//  * own positions: HBM.  131071 positions of one row, 537 MB: 96 us, 5.6 TB/s;
+//    the wavefronts' ranges are equal but end between 70 and 91 us.
+//  * a prefix of 128 columns: a wavefront's chain of LDS reads, products, weights
+//    and products, some 1900 clocks a unit, with HBM half idle (64 rows behind
+//    16384 positions and up to 1024 of their own, 202 MB: 55 us).
+//  * short calls: launch, the lengths, page numbers, keys and values one after
+//    the other (512 positions of one row: 6.2 us).
 
 constexpr uint32_t kCap = 128;        // columns of a prefix block: 4 wavefronts of 2 16-column tiles
 constexpr uint32_t kWaveRatio = 32;   // most query heads per key-value head that one wavefront takes
 constexpr int kAttendThreads = 256;
-constexpr float kNoMax = -1e30f;      // the maximum of nothing: finite, so that exp2(-inf - it) is 0
+constexpr float kNoMax = -1e30f;      // the maximum of nothing: finite, so that exp2(-inf - it) is 0 (scores below it weigh 0)
 
 template <int D>
 struct AttendShape {
@@ -1405,7 +1415,7 @@ nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
     constexpr int kRowWaves = AttendShape<D>::kRowWaves;
     constexpr size_t lds = std::max(sizeof(Join<D, kRowWaves>), keys_fit(D, kRowWaves) ? size_t{kRowWaves * key_slots(D)} : 0);
     static_assert(sizeof(LdsFixed) + lds <= kMaxLds, "LDS");
-    if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend_rows<D>),
+    if (lds + sizeof(LdsFixed) > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend_rows<D>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds)) != hipSuccess)
       return NWC_ERR_HIP;
     return launch(k_attend_rows<D>, dim3(a.pages.rows * a.hkv, (a.ratio + kWaveRatio - 1) / kWaveRatio),
@@ -1494,7 +1504,7 @@ nwc_status nwc_attend_workspace_size(const nwc_cache* cache, uint32_t rows, uint
 nwc_status nwc_attend(const nwc_cache* cache, const nwc_page_table* table, const nwc_groups* groups, const int32_t* lengths_dev,
                       const uint16_t* q_dev, uint64_t ldq, uint32_t q_heads, float scale, uint16_t* out_dev, uint64_t ldo,
                       void* ws, size_t ws_bytes, void* stream) {
-  if (!cache || !table || !lengths_dev || !q_dev || !out_dev || !ws || !std::isfinite(scale) || scale <= 0.f)
+  if (!cache || !table || !lengths_dev || !q_dev || !out_dev || !ws || !std::isfinite(scale * kLog2e) || !(scale > 0.f))
     return NWC_ERR_INVALID_ARG;
   const uint32_t n_groups = groups ? groups->count : 0;
   if (groups && (groups->reserved || (n_groups && (!groups->start || !groups->len)))) return NWC_ERR_INVALID_ARG;

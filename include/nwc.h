@@ -456,7 +456,7 @@ typedef struct {
  * positions p < lengths_dev[r] (device, int32) of key-value head
  * h / (q_heads / kv_heads).  q_dev and out_dev [rows, q_heads, head_dim],
  * rows ldq / ldo elements apart (multiples of 8, 16-byte aligned), rows =
- * table->rows.  Length 0 gives zeros; a negative length marks a padding row,
+ * table->rows, the two apart in memory.  Length 0 gives zeros; a negative length marks a padding row,
  * whose output is left as it was; a length past the table's cols *
  * page_len is cut to it.  Several tokens of one sequence are several rows
  * with the same pages and lengths one apart, in one group.  groups NULL or

@@ -242,12 +242,12 @@ def _check_attend(got, ref, what):
 class _Batch:
     """Rows of `lengths` tokens over a fresh cache; groups: (first row, end, shared length)."""
 
-    def __init__(self, lengths, hq, hk, d, page, groups=(), seed=0, interleaved=False, spread=1.0, extra=2):
+    def __init__(self, lengths, hq, hk, d, page, groups=(), seed=0, interleaved=False, spread=1.0, extra=2, covers=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
         rnd = np.random.default_rng(seed)
         self.lengths = np.asarray(lengths)
         B = len(lengths)
-        cols = max(1, -(-max(int(self.lengths.max()), 1) // page))
+        cols = -(-max(int(self.lengths.max()), 1, covers) // page)
         need = np.maximum(0, -(-self.lengths // page))
         n_pages = int(need.sum()) + 5 + sum(-(-s // page) for _, _, s in groups)
         free = list(rnd.permutation(n_pages))
@@ -295,20 +295,22 @@ SHAPES = [(32, 8, 128, 64), (28, 4, 128, 16), (64, 8, 64, 32), (8, 1, 256, 16), 
           (40, 1, 128, 16), (64, 1, 64, 64), (3, 3, 64, 1024), (33, 1, 256, 32)]
 
 
+@pytest.mark.parametrize("covers", [0, 2049, 20000])            # tables as long as the rows, and longer ones
 @pytest.mark.parametrize("hq,hk,d,page", SHAPES)
-def test_attend_ragged(hq, hk, d, page):
-    _say("attend ragged %d %d %d %d" % (hq, hk, d, page))
-    b = _Batch([1, 0, 31, 32, 33, -1, 64, 65, 127, 129, 300, 1000, 16, 17, 2, -7], hq, hk, d, page, seed=d + hq)
+def test_attend_ragged(hq, hk, d, page, covers):
+    _say("attend ragged %d %d %d %d %d" % (hq, hk, d, page, covers))
+    b = _Batch([1, 0, 31, 32, 33, -1, 64, 65, 127, 129, 300, 1000, 16, 17, 2, -7], hq, hk, d, page, seed=d + hq, covers=covers)
     nwc.nwc_attend(b.call())
     torch.cuda.synchronize()
     b.check("ragged")
     assert bool((b.out[1] == 0).all())                         # nothing to see: zeros
 
 
+@pytest.mark.parametrize("covers", [0, 4096])
 @pytest.mark.parametrize("length", [1, 2, 15, 16, 17, 511, 512, 513, 5000, 40001])
-def test_attend_single(length):
-    _say("attend single %d" % length)
-    b = _Batch([length], 32, 8, 128, 64, seed=length, interleaved=length % 2 == 1)
+def test_attend_single(length, covers):
+    _say("attend single %d %d" % (length, covers))
+    b = _Batch([length], 32, 8, 128, 64, seed=length, interleaved=length % 2 == 1, covers=covers)
     nwc.nwc_attend(b.call())
     torch.cuda.synchronize()
     b.check("single")
@@ -510,3 +512,66 @@ def test_decode_loop_in_a_graph():
             assert all(torch.equal(a, b) for a, b in zip(outs, first))
         first = outs
     other.check("the other caller")
+
+
+@pytest.mark.parametrize("covers", [0, 5000])
+def test_attend_graph_and_streams(covers):
+    """Captured once, replayed with other lengths, queries and pages in the same buffers, against eager calls; two streams
+    with a workspace each at once."""
+    b = _Batch([300, 40, 511, 1], 16, 4, 128, 32, seed=9, covers=covers)
+    lengths, table = _i32(b.lengths), _i32(b.table)
+    call = nwc.Attend(b.cache, table, lengths, b.q, b.out[:4], b.ws, b.scale)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    nwc.nwc_attend(call, stream=side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        nwc.nwc_attend(call)                                    # the current stream: the one being captured
+    torch.cuda.synchronize()
+    for n, order in (([300, 40, 511, 1], [0, 1, 2, 3]), ([7, 40, 0, 1], [0, 1, 2, 3]), ([500, 33, 299, -1], [2, 1, 0, 3])):
+        b.out.fill_(7.0)
+        lengths.copy_(_i32(n))
+        table.copy_(_i32(b.table[order]))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+        n, live = np.array(n), torch.from_numpy(np.array(n) >= 0).cuda()
+        out, size = _ref_attend(b.kp, b.vp, b.table[order], n, b.q, b.scale)
+        _check_attend(b.out[:4][live], (out[live], size[live]), "replay")
+        got = b.out.clone()
+        nwc.nwc_attend(nwc.Attend(b.cache, _i32(b.table[order]), _i32(n), b.q, b.out[:4], b.ws, b.scale))
+        torch.cuda.synchronize()
+        assert torch.equal(got, b.out)
+    other = _Batch([900, 77], 8, 2, 64, 16, seed=10, covers=covers)
+    calls = [x.call() for x in (b, other)]
+    streams = [torch.cuda.Stream() for _ in calls]
+    for x in (b, other):
+        x.out.fill_(7.0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s in zip(calls, streams):
+            nwc.nwc_attend(c, stream=s)
+    torch.cuda.synchronize()
+    b.check("first stream")
+    other.check("second stream")
+
+
+def test_calls_refuse_mixed_tensors():
+    b = _Batch([5], 8, 2, 64, 16, seed=1)
+    good = dict(cache=b.cache, table=_i32(b.table), lengths=_i32([5]), q=b.q, out=b.out[:1], ws=b.ws)
+    for name, bad in (("q", b.q.float()), ("q", b.q[:, :, :32]), ("q", b.q.cpu()), ("out", b.out), ("lengths", _i32([5, 6])),
+                      ("lengths", torch.tensor([5], device="cuda")), ("table", _i32(b.table).long()), ("ws", b.ws.cpu())):
+        with pytest.raises(ValueError):
+            nwc.Attend(**dict(good, **{name: bad}))
+    with pytest.raises(ValueError):
+        nwc.Attend(**good, group_start=_i32([0, 1]))
+    with pytest.raises(nwc.NwcError):
+        nwc.nwc_attend(nwc.Attend(**dict(good, ws=b.ws[:256])))
+    with pytest.raises(nwc.NwcError):
+        nwc.nwc_attend(nwc.Attend(**good, scale=0.0))
+    with pytest.raises(ValueError):
+        nwc.QkNormRope(b.q, None, _i32([0]), freqs=_freqs(32), style="thirds")
+    with pytest.raises(nwc.NwcError):
+        nwc.nwc_qk_norm_rope(nwc.QkNormRope(b.q, None, _i32([0]), freqs=_freqs(128)))   # more than the head has
