@@ -430,11 +430,12 @@ __device__ Split make_plan(const AttendArgs& a, const Plan& p, uint32_t* carry) 
   s.prefix_units = uniform(p.g_pre[G]);
   s.own_units = uniform(p.row_pre[rows]);
   const uint64_t prefix = static_cast<uint64_t>(s.prefix_units) * a.hkv, own = static_cast<uint64_t>(s.own_units) * a.hkv;
-  // prefixes to the first half of the workgroups, own positions to the second
-  // (one of each per compute unit); all take part in the prefixes where there is
-  // little else.  At least four units, one per wavefront, for a workgroup's
-  // part of a prefix.
-  s.prefix_wgs = own < prefix / 2 ? gridDim.x : gridDim.x - a.own_wgs;
+  // prefixes to the first half of the workgroups, own positions to the second:
+  // one of each per compute unit.  (Prefixes on both halves, where there is
+  // little else, were slower: more partial sums, and no faster a unit; 16 rows
+  // behind 16384 positions 29.2 us against 24.7, 64 rows 49.7 against 46.7.)  At
+  // least four units, one per wavefront, for a workgroup's part of a prefix.
+  s.prefix_wgs = gridDim.x - a.own_wgs;
   const uint32_t owners = a.own_wgs * (a.ratio <= kWaveRatio ? 4 : 1);
   s.prefix_quota = s.prefix_wgs ? max((prefix + s.prefix_wgs - 1) / s.prefix_wgs, uint64_t{4}) : 4;
   s.own_quota = max((own + owners - 1) / owners, uint64_t{1});
@@ -1374,7 +1375,7 @@ AttendLayout attend_layout(uint32_t rows, uint32_t q_heads, uint32_t ratio, uint
   const uint64_t cols = static_cast<uint64_t>(rows) * q_heads;
   L.cap_p = groups ? std::min(kCap, rows * ratio) : 0;
   L.cap_o = ratio;
-  L.own_slot = groups ? cols + 2 * static_cast<uint64_t>(cus) * L.cap_p : 0;
+  L.own_slot = groups ? cols + static_cast<uint64_t>(cus) * L.cap_p : 0;
   const uint64_t slots = L.own_slot + cols + static_cast<uint64_t>(cus) * (ratio <= kWaveRatio ? 4 : 1) * L.cap_o;
   auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
   L.ml = up(slots * d * 4);
