@@ -1404,15 +1404,19 @@ nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uin
 // 2048: 16.0 and 18.3, to 4096: 46.4 and 33.3; 64 rows of 2048: 95.5 and 100.1.
 // Heads of 192 and 256, whose keys do not go by LDS here, keep few wavefronts:
 // 1 row of 512 (8 / 2 heads of 256): 13.2 and 10.3.
-uint32_t rows_most(uint32_t d, uint64_t groups, uint32_t cus) {
-  if (d > 128) return 128;
-  return 2 * groups >= cus ? 2048 : 8 * groups >= cus ? 1024 : 512;
+// Rows that share a prefix read it each for itself here, from the caches, which
+// is faster while that is little: 16 rows behind 384 positions with 100 of their
+// own 6.6 and 13.0, 64 rows behind 896 18.1 and 21.7.
+bool by_rows(uint32_t d, uint64_t groups, uint32_t covers, bool shared, uint32_t cus) {
+  if (d > 128) return covers <= 128;
+  if (shared) return covers <= 1024 && groups * covers <= 1 << 19;
+  return covers <= (2 * groups >= cus ? 2048u : 8 * groups >= cus ? 1024u : 512u);
 }
 
 template <int D>
 nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
   const uint64_t items = static_cast<uint64_t>(a.pages.rows) * a.hkv;
-  if (!a.n_groups && a.pages.cols << a.pages.shift <= rows_most(D, items, a.own_wgs)) {
+  if (by_rows(D, items, a.pages.cols << a.pages.shift, a.n_groups != 0, a.own_wgs)) {
     constexpr int kRowWaves = AttendShape<D>::kRowWaves;
     constexpr size_t lds = std::max(sizeof(Join<D, kRowWaves>), keys_fit(D, kRowWaves) ? size_t{kRowWaves * key_slots(D)} : 0);
     static_assert(sizeof(LdsFixed) + lds <= kMaxLds, "LDS");

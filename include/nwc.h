@@ -438,12 +438,12 @@ nwc_status nwc_kv_append(const nwc_cache *cache, const nwc_page_table *table, co
 
 /* Rows that share a prefix: group i is rows start[i] .. start[i + 1] - 1,
  * whose first len[i] positions hold the same tokens (start: device, count + 1
- * int32, ascending; len: device, count int32).  The positions are read once
- * for the whole group, through the table row of the group's first row that is
- * long enough; a row shorter than len[i] takes no part and is read alone, as
- * is a row of no group.  len need not be a multiple of page_len.  Groups
- * only say what may be read once: where the tables agree the result is that
- * of no groups, up to rounding. */
+ * int32, ascending; len: device, count int32).  Groups only say what may be
+ * read once, for the whole group: every row's table names pages that hold
+ * those tokens (the same pages, or copies), a call may read them through any
+ * of the rows, and the result is that of no groups, up to rounding.  A row
+ * shorter than len[i] takes no part and is read alone, as is a row of no
+ * group.  len need not be a multiple of page_len. */
 typedef struct {
   const int32_t *start;
   const int32_t *len;

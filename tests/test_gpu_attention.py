@@ -327,12 +327,13 @@ GROUPS = {
 }
 
 
+@pytest.mark.parametrize("covers", [0, 5000])                     # short tables take a launch of their own
 @pytest.mark.parametrize("name", list(GROUPS))
-@pytest.mark.parametrize("hq,hk,d,page", [SHAPES[0], SHAPES[1], SHAPES[3], SHAPES[5], SHAPES[7]])
-def test_attend_groups(name, hq, hk, d, page):
-    _say("attend groups %s %d %d %d %d" % (name, hq, hk, d, page))
+@pytest.mark.parametrize("hq,hk,d,page", [SHAPES[0], SHAPES[1], SHAPES[3], SHAPES[4], SHAPES[5], SHAPES[7]])
+def test_attend_groups(name, hq, hk, d, page, covers):
+    _say("attend groups %s %d %d %d %d %d" % (name, hq, hk, d, page, covers))
     lengths, groups = GROUPS[name]
-    b = _Batch(lengths, hq, hk, d, page, groups, seed=len(lengths) + d)
+    b = _Batch(lengths, hq, hk, d, page, groups, seed=len(lengths) + d, covers=covers)
     nwc.nwc_attend(b.call())
     torch.cuda.synchronize()
     b.check(name)
@@ -347,11 +348,12 @@ def test_attend_groups(name, hq, hk, d, page):
     assert torch.equal(b.out, first), "not the same bits"
 
 
-def test_attend_any_group_numbers():
+@pytest.mark.parametrize("covers", [0, 4000])
+def test_attend_any_group_numbers(covers):
     # starts out of order or range, lengths negative or too long: never out of bounds; since all rows have the same pages,
     # whatever is read once is right for every row
     lengths = [200] * 12
-    b = _Batch(lengths, 8, 2, 64, 16, [(0, 12, 192)], seed=3)
+    b = _Batch(lengths, 8, 2, 64, 16, [(0, 12, 192)], seed=3, covers=covers)
     for start, shared in (([-5, 4, 100], [192, 64]), ([8, 2, 12], [192, 100]), ([0, 20, 3], [10 ** 9, -4]),
                           ([12, 12, 12], [5, 5]), ([-2 ** 31, 2 ** 31 - 1, 0], [128, 128])):
         _say("any group numbers %s %s" % (start, shared))
@@ -363,8 +365,9 @@ def test_attend_any_group_numbers():
         b.check(str(start))
 
 
-def test_attend_pages_that_do_not_exist():
-    b = _Batch([300, 64, 500], 8, 2, 128, 16, seed=5)
+@pytest.mark.parametrize("covers", [0, 4000])
+def test_attend_pages_that_do_not_exist(covers):
+    b = _Batch([300, 64, 500], 8, 2, 128, 16, seed=5, covers=covers)
     n = b.kp.shape[0]
     b.table[0, 2], b.table[0, 18], b.table[2, 0], b.table[2, 7] = -1, n, 2 ** 31 - 1, -2 ** 31
     b.table[1, :4] = -1                                         # the whole row
@@ -381,10 +384,11 @@ def test_attend_pages_that_do_not_exist():
     b.check("cut")
 
 
-def test_attend_sharp_and_flat_softmax():
+@pytest.mark.parametrize("covers", [0, 4000])
+def test_attend_sharp_and_flat_softmax(covers):
     # scores far apart (one position takes all), all equal, growing along the row (the running maximum moves in every
     # unit), and an infinite one
-    b = _Batch([700, 700, 700], 4, 1, 64, 32, seed=8, spread=30.0)
+    b = _Batch([700, 700, 700], 4, 1, 64, 32, seed=8, spread=30.0, covers=covers)
     b.q[1] = 0
     t = torch.from_numpy(b.table).cuda()
     at = torch.arange(700, device="cuda")
@@ -408,7 +412,8 @@ def test_attend_sharp_and_flat_softmax():
     assert not bool(b.out[2].isnan().any())
 
 
-def test_attend_strided_rows_and_far_pages():
+@pytest.mark.parametrize("more", [0, 300])
+def test_attend_strided_rows_and_far_pages(more):
     # queries inside a joint projection's rows, outputs inside a wider buffer, pages more than 2^32 elements apart
     d, hq, hk, page = 128, 8, 2, 16
     far = (1 << 32) + 8 * 1024
@@ -419,7 +424,7 @@ def test_attend_strided_rows_and_far_pages():
     vp.copy_(_randn(g, 3, hk, page, d))
     x, wide = _randn(g, 2, (hq + 2 * hk) * d), torch.full((2, hq * d + 40), 7.0, dtype=torch.bfloat16, device="cuda")
     q, out = x[:, :hq * d].view(2, hq, d), wide[:, 8:8 + hq * d].view(2, hq, d)
-    table, lengths = np.array([[2, 1], [0, 2]]), np.array([32, 21])
+    table, lengths = np.array([[2, 1] + [-1] * more, [0, 2] + [7] * more]), np.array([32, 21])
     cache = nwc.PagedCache(kp, vp)
     ws = torch.empty(nwc.nwc_attend_workspace_size(cache, 2, hq), dtype=torch.uint8, device="cuda")
     new = _randn(g, 1, 2 * hk * d)
@@ -440,7 +445,8 @@ def test_attend_many_rows():
     b.check("4096 rows")
 
 
-def test_decode_loop_in_a_graph():
+@pytest.mark.parametrize("covers", [0, 4000])
+def test_decode_loop_in_a_graph(covers):
     """A prompt appended to two sequences, a shared copy for four continuations, then steps of append and attention
     as one captured graph whose positions and lengths move on the device; a second workspace user in between."""
     hq, hk, d, page, prompt, steps = 8, 2, 128, 16, 45, 6
@@ -453,6 +459,7 @@ def test_decode_loop_in_a_graph():
     cols = -(-(prompt + steps) // page)
     table = np.random.default_rng(0).permutation(n_pages)[:4 * cols].reshape(4, cols)
     table[1:, :prompt // page] = table[0, :prompt // page]      # whole pages of the prompt are shared
+    table = np.concatenate([table, np.full((4, -(-covers // page)), -1, np.int64)], 1)
     x = _randn(g, prompt, 2 * hk * d)
     rows, pos = _i32([0] * prompt), _i32(range(prompt))
     tab = _i32(table)
