@@ -1280,13 +1280,9 @@ nwc_status launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipSt
              : NWC_ERR_HIP;
 }
 
-uint32_t cu_count() {
-  int dev = 0, n = 0;
-  if (hipGetDevice(&dev) != hipSuccess ||
-      hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1)
-    return 0;
-  return static_cast<uint32_t>(n);
-}
+// Compute units of an MI355X.  Launches are cut for them; nothing needs them to
+// be there, so they are not asked for (two runtime calls less in a call of 4 us).
+constexpr uint32_t kCus = 256;
 
 // Most heads of one tensor, and strides that fit 32 bits in pieces of 8 elements.
 constexpr uint32_t kMaxHeads = 65535;
@@ -1336,14 +1332,12 @@ nwc_status check_cache(const nwc_cache* c, const nwc_page_table* t, PageArgs* p)
 
 nwc_status launch_heads(HeadsArgs& a, hipStream_t s) {
   const uint32_t all = a.hq + a.hk + a.hv, lanes = a.d / 8u;
-  const uint32_t cus = cu_count();
-  if (cus == 0) return NWC_ERR_HIP;
   const uint32_t g = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
   const uint32_t passes = (all + kWave / g - 1) / (kWave / g);
   // one pass per wavefront while that leaves compute units idle, else four at a
   // time, a token's passes over as many wavefronts as it takes to have 16 per
   // compute unit
-  const uint32_t want = cus * 16;
+  const uint32_t want = kCus * 16;
   const bool few = static_cast<uint64_t>(a.tokens) * passes < want;
   a.split = few ? passes : std::min((passes + 3) / 4, std::max(1u, want / a.tokens));
   const uint64_t waves = static_cast<uint64_t>(a.tokens) * a.split;
@@ -1370,13 +1364,13 @@ struct AttendLayout {
   uint64_t own_slot, ml, plan, bytes;
   uint32_t cap_p, cap_o;
 };
-AttendLayout attend_layout(uint32_t rows, uint32_t q_heads, uint32_t ratio, uint32_t groups, uint32_t d, uint32_t cus) {
+AttendLayout attend_layout(uint32_t rows, uint32_t q_heads, uint32_t ratio, uint32_t groups, uint32_t d) {
   AttendLayout L;
   const uint64_t cols = static_cast<uint64_t>(rows) * q_heads;
   L.cap_p = groups ? std::min(kCap, rows * ratio) : 0;
   L.cap_o = ratio;
-  L.own_slot = groups ? cols + static_cast<uint64_t>(cus) * L.cap_p : 0;
-  const uint64_t slots = L.own_slot + cols + static_cast<uint64_t>(cus) * (ratio <= kWaveRatio ? 4 : 1) * L.cap_o;
+  L.own_slot = groups ? cols + uint64_t{kCus} * L.cap_p : 0;
+  const uint64_t slots = L.own_slot + cols + uint64_t{kCus} * (ratio <= kWaveRatio ? 4 : 1) * L.cap_o;
   auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
   L.ml = up(slots * d * 4);
   L.plan = L.ml + up(slots * 8);
@@ -1407,16 +1401,16 @@ nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uin
 // Rows that share a prefix read it each for itself here, from the caches, which
 // is faster while that is little: 16 rows behind 384 positions with 100 of their
 // own 6.6 and 13.0, 64 rows behind 896 18.1 and 21.7.
-bool by_rows(uint32_t d, uint64_t groups, uint32_t covers, bool shared, uint32_t cus) {
+bool by_rows(uint32_t d, uint64_t groups, uint32_t covers, bool shared) {
   if (d > 128) return covers <= 128;
   if (shared) return covers <= 1024 && groups * covers <= 1 << 19;
-  return covers <= (2 * groups >= cus ? 2048u : 8 * groups >= cus ? 1024u : 512u);
+  return covers <= (2 * groups >= kCus ? 2048u : 8 * groups >= kCus ? 1024u : 512u);
 }
 
 template <int D>
 nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
   const uint64_t items = static_cast<uint64_t>(a.pages.rows) * a.hkv;
-  if (by_rows(D, items, a.pages.cols << a.pages.shift, a.n_groups != 0, a.own_wgs)) {
+  if (by_rows(D, items, a.pages.cols << a.pages.shift, a.n_groups != 0)) {
     constexpr int kRowWaves = AttendShape<D>::kRowWaves;
     constexpr size_t lds = std::max(sizeof(Join<D, kRowWaves>), keys_fit(D, kRowWaves) ? size_t{kRowWaves * key_slots(D)} : 0);
     static_assert(sizeof(LdsFixed) + lds <= kMaxLds, "LDS");
@@ -1502,7 +1496,7 @@ nwc_status nwc_attend_workspace_size(const nwc_cache* cache, uint32_t rows, uint
   if (!bytes) return NWC_ERR_INVALID_ARG;
   const nwc_status st = attend_shape(cache, rows, q_heads, n_groups);
   if (st) return st;
-  *bytes = attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, cache->head_dim, 256).bytes;
+  *bytes = attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, cache->head_dim).bytes;
   return NWC_OK;
 }
 
@@ -1524,11 +1518,9 @@ nwc_status nwc_attend(const nwc_cache* cache, const nwc_page_table* table, const
   if (!aligned(q_dev, 16) || !aligned(out_dev, 16) || ldq % 8 || ldo % 8 || !aligned(lengths_dev, 4) || !aligned(ws, 256) ||
       (n_groups && (!aligned(groups->start, 4) || !aligned(groups->len, 4))))
     return NWC_ERR_ALIGNMENT;
-  if (ws_bytes < attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d, 256).bytes) return NWC_ERR_BUFFER_TOO_SMALL;
-  const uint32_t cus = std::min(cu_count(), 256u);
-  if (cus == 0) return NWC_ERR_HIP;
-  const uint32_t grid = n_groups ? 2 * cus : cus;
-  const AttendLayout L = attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d, cus);
+  if (ws_bytes < attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d).bytes) return NWC_ERR_BUFFER_TOO_SMALL;
+  const uint32_t grid = n_groups ? 2 * kCus : kCus;
+  const AttendLayout L = attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d);
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.k = cache->k;
   a.v = cache->v;
@@ -1550,7 +1542,7 @@ nwc_status nwc_attend(const nwc_cache* cache, const nwc_page_table* table, const
   a.part_ml = reinterpret_cast<float*>(w + L.ml);
   a.plan = reinterpret_cast<uint32_t*>(w + L.plan);
   a.own_slot = L.own_slot;
-  a.own_wgs = cus;
+  a.own_wgs = kCus;
   a.cap_p = L.cap_p;
   a.cap_o = L.cap_o;
   const hipStream_t s = static_cast<hipStream_t>(stream);
