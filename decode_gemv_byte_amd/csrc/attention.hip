@@ -1396,15 +1396,16 @@ nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uin
 // + k_attend_join): 1 row of 512: 5.7 and 7.7, 1024: 8.2 and 7.7; 4 rows of 1024:
 // 9.4 and 10.5, 2048: 14.4 and 12.6; 16 rows of 2048: 28.4 and 30.7, ragged to
 // 2048: 16.0 and 18.3, to 4096: 46.4 and 33.3; 64 rows of 2048: 95.5 and 100.1.
-// Heads of 192 and 256, whose keys do not go by LDS here, keep few wavefronts:
-// 1 row of 512 (8 / 2 heads of 256): 13.2 and 10.3.
+// Heads of 256, whose keys have no room in LDS, gain less: 1 row of 256 positions
+// (8 / 4 heads) 8.7 and 10.3, of 512 13.2 and 10.2; 32 rows of 1024 35.8 and 40.8.
 // Rows that share a prefix read it each for itself here, from the caches, which
 // is faster while that is little: 16 rows behind 384 positions with 100 of their
 // own 6.6 and 13.0, 64 rows behind 896 18.1 and 21.7.
 bool by_rows(uint32_t d, uint64_t groups, uint32_t covers, bool shared) {
-  if (d > 128) return covers <= 128;
-  if (shared) return covers <= 1024 && groups * covers <= 1 << 19;
-  return covers <= (2 * groups >= kCus ? 2048u : 8 * groups >= kCus ? 1024u : 512u);
+  const bool many = 2 * groups >= kCus;
+  if (shared) return covers <= (d == 256 ? 256 : 1024) && groups * covers * d <= 1 << 26;
+  if (d == 256) return covers <= (many ? 1024 : 256);
+  return covers <= (many ? 2048 : 8 * groups >= kCus ? 1024 : 512);
 }
 
 template <int D>

@@ -464,8 +464,7 @@ typedef struct {
  * scale finite and > 0.  head_dim 64, 96, 128, 192 or 256; q_heads a multiple of kv_heads, at most
  * 64 times it; at most 4096 rows and 512 groups; cols * page_len <= 2^22.
  * Softmax statistics and sums in FP32; the weights w are rounded to BF16 for
- * the matrix cores (relative error 2^-9 each, the size of the output's own
- * rounding).  Repeated calls give the same bits.  ws (device, 256-byte
+ * the matrix cores (each by at most 2^-8 of itself, as the output is).  Repeated calls give the same bits.  ws (device, 256-byte
  * aligned, at least nwc_attend_workspace_size bytes for these rows, q_heads
  * and group count; no initial content needed); calls that share it must not
  * run concurrently.  Async.
