@@ -1341,7 +1341,8 @@ nwc_status launch_heads(HeadsArgs& a, hipStream_t s) {
   const bool few = static_cast<uint64_t>(a.tokens) * passes < want;
   a.split = few ? passes : std::min((passes + 3) / 4, std::max(1u, want / a.tokens));
   const uint64_t waves = static_cast<uint64_t>(a.tokens) * a.split;
-  const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>((waves + 3) / 4, uint64_t{1} << 24));
+  // a launch holds fewer than 2^32 threads; more tokens go round
+  const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>((waves + 3) / 4, uint64_t{1} << 22));
   auto go = [&](auto one, auto four) { return launch(few ? one : four, dim3(grid), dim3(256), 0, s, a); };
   if (g == 8) return go(k_heads<8, 1>, k_heads<8, 4>);
   if (g == 16) return go(k_heads<16, 1>, k_heads<16, 4>);
@@ -1360,6 +1361,7 @@ void set_rope(HeadsArgs* a, const nwc_rope* rope) {
 
 // Workspace of nwc_attend: partial sums, maxima and sums, the plan.
 constexpr uint32_t kAttendMaxRows = 4096, kAttendMaxGroups = 512, kAttendMaxRatio = 64, kAttendMaxLen = 1u << 22;
+constexpr uint64_t kAttendMaxCols = 1u << 22;  // rows times query heads: a workgroup each, of 2^32 - 1 threads a launch
 struct AttendLayout {
   uint64_t own_slot, ml, plan, bytes;
   uint32_t cap_p, cap_o;
@@ -1383,12 +1385,11 @@ nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uin
   const uint32_t d = c->head_dim;
   if (d != 64 && d != 96 && d != 128 && d != 192 && d != 256) return NWC_ERR_UNSUPPORTED;
   if (q_heads % c->kv_heads) return NWC_ERR_INVALID_ARG;
-  if (rows > kAttendMaxRows || groups > kAttendMaxGroups || q_heads / c->kv_heads > kAttendMaxRatio || q_heads > kMaxHeads)
+  if (rows > kAttendMaxRows || groups > kAttendMaxGroups || q_heads / c->kv_heads > kAttendMaxRatio || q_heads > kMaxHeads ||
+      static_cast<uint64_t>(rows) * q_heads > kAttendMaxCols)
     return NWC_ERR_UNSUPPORTED;
   return NWC_OK;
 }
-
-
 
 // Positions that a table may cover for k_attend_rows to take it, by the number of
 // its workgroups (rows times key-value heads) against the compute units.
@@ -1519,9 +1520,10 @@ nwc_status nwc_attend(const nwc_cache* cache, const nwc_page_table* table, const
   if (!aligned(q_dev, 16) || !aligned(out_dev, 16) || ldq % 8 || ldo % 8 || !aligned(lengths_dev, 4) || !aligned(ws, 256) ||
       (n_groups && (!aligned(groups->start, 4) || !aligned(groups->len, 4))))
     return NWC_ERR_ALIGNMENT;
-  if (ws_bytes < attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d).bytes) return NWC_ERR_BUFFER_TOO_SMALL;
-  const uint32_t grid = n_groups ? 2 * kCus : kCus;
   const AttendLayout L = attend_layout(rows, q_heads, q_heads / cache->kv_heads, n_groups, d);
+  if (ws_bytes < L.bytes) return NWC_ERR_BUFFER_TOO_SMALL;
+  if (out_dev == q_dev) return NWC_ERR_INVALID_ARG;  // workgroups read queries that others have answered
+  const uint32_t grid = n_groups ? 2 * kCus : kCus;
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.k = cache->k;
   a.v = cache->v;

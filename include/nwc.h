@@ -456,18 +456,20 @@ typedef struct {
  * positions p < lengths_dev[r] (device, int32) of key-value head
  * h / (q_heads / kv_heads).  q_dev and out_dev [rows, q_heads, head_dim],
  * rows ldq / ldo elements apart (multiples of 8, 16-byte aligned), rows =
- * table->rows, the two apart in memory.  Length 0 gives zeros; a negative length marks a padding row,
- * whose output is left as it was; a length past the table's cols *
- * page_len is cut to it.  Several tokens of one sequence are several rows
- * with the same pages and lengths one apart, in one group.  groups NULL or
- * count 0: nothing shared.
- * scale finite and > 0.  head_dim 64, 96, 128, 192 or 256; q_heads a multiple of kv_heads, at most
- * 64 times it; at most 4096 rows and 512 groups; cols * page_len <= 2^22.
+ * table->rows, the two apart in memory (the same pointer is refused).
+ * Length 0 gives zeros; a negative length marks a padding row, whose output
+ * is left as it was; a length past the table's cols * page_len is cut to it.
+ * Several tokens of one sequence are several rows with the same pages and
+ * lengths one apart, in one group.  groups NULL or count 0: nothing shared.
+ * scale finite and > 0.  head_dim 64, 96, 128, 192 or 256; q_heads a
+ * multiple of kv_heads, at most 64 times it; at most 4096 rows, 2^22 rows *
+ * q_heads and 512 groups; cols * page_len <= 2^22.
  * Softmax statistics and sums in FP32; the weights w are rounded to BF16 for
- * the matrix cores (each by at most 2^-8 of itself, as the output is).  Repeated calls give the same bits.  ws (device, 256-byte
- * aligned, at least nwc_attend_workspace_size bytes for these rows, q_heads
- * and group count; no initial content needed); calls that share it must not
- * run concurrently.  Async.
+ * the matrix cores (each by at most 2^-8 of itself, as the output is).
+ * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
+ * nwc_attend_workspace_size bytes for these rows, q_heads and group count;
+ * no initial content needed); calls that share it must not run concurrently.
+ * Async.
  * Errors: INVALID_ARG, BUFFER_TOO_SMALL (ws), ALIGNMENT, UNSUPPORTED, HIP. */
 nwc_status nwc_attend_workspace_size(const nwc_cache *cache, uint32_t rows, uint32_t q_heads,
                                      uint32_t n_groups, size_t *bytes);

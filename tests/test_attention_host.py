@@ -154,6 +154,16 @@ def test_attend_refusals():
     assert L.nwc_attend_workspace_size(_ref(_cache()), 2, 32, 2, ctypes.byref(size)) == nwc.NWC_OK and size.value >= before
 
 
+def test_attend_refuses_output_over_queries_and_oversized_launches():
+    assert _attend(q=A, out=A) == nwc.NWC_ERR_INVALID_ARG
+    # a launch holds fewer than 2^32 threads: rows times query heads up to 2^22
+    size = ctypes.c_size_t()
+    many = _cache(kv_heads=1024, page_stride=1024 * 64 * 128)
+    assert L.nwc_attend_workspace_size(_ref(many), 4096, 1024, 0, ctypes.byref(size)) == nwc.NWC_OK
+    assert L.nwc_attend_workspace_size(_ref(many), 4096, 2048, 0, ctypes.byref(size)) == nwc.NWC_ERR_UNSUPPORTED
+    assert _attend(cache=many, table=_table(rows=4096), hq=2048, ldq=1 << 20, ldo=1 << 20, out=1 << 40) == nwc.NWC_ERR_UNSUPPORTED
+
+
 def test_binding_refuses_host_tensors_and_odd_layouts():
     pages = torch.zeros((2, 1, 16, 64), dtype=torch.bfloat16)
     cache = nwc.PagedCache(pages, pages.clone())

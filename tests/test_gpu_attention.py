@@ -109,6 +109,25 @@ def test_norm_rope(case):
         assert torch.equal(x[-1], before[-1])
 
 
+def test_norm_rope_more_tokens_than_a_launch_has_wavefronts():
+    t, d = (1 << 26) + 5, 8
+    _say("norm_rope %d tokens of one head of %d" % (t, d))
+    g = torch.Generator(device="cuda").manual_seed(26)
+    x = torch.empty((t, 1, d), dtype=torch.bfloat16, device="cuda").uniform_(-2, 2, generator=g)
+    w = (1 + 0.3 * torch.randn(d, generator=g, device="cuda")).clamp(0, 2).to(torch.bfloat16)
+    pos = torch.arange(t, dtype=torch.int32, device="cuda") % 4096
+    freqs = _freqs(d)
+    out = torch.full_like(x, 7.0)
+    nwc.nwc_qk_norm_rope(nwc.QkNormRope(x, None, pos, q_out=out, q_weight=w, eps=EPS, freqs=freqs))
+    torch.cuda.synchronize()
+    for first in (0, 1 << 22, 1 << 24, (1 << 26) - 1000, t - 4096):
+        some = slice(first, min(first + 4096, t))
+        ref, size = _ref_heads(x[some], w, pos[some], freqs, "half")
+        _check_heads(out[some], ref, size, "tokens from %d" % first)
+    # a normed head of 8 has length sqrt 8, so a turned pair of it, weighted by at most 2, stays below 6
+    assert not bool((out == 7.0).any()), "a token was left out"
+
+
 def test_norm_rope_special_values():
     # a head of zeros stays zero; infinities and NaN stay in their head; large and tiny values keep the norm's range
     x = torch.ones((6, 1, 64), dtype=torch.bfloat16, device="cuda")
