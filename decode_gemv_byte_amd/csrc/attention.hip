@@ -233,9 +233,9 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
 // partial sums in the workspace, which k_attend_join adds.
 //
 // A unit is computed by one wavefront.  S^T = K Q^T on the matrix cores (a lane's
-// keys: one position, 8 components); with the positions of the two 16-row tiles interleaved (tile t, row m is
-// position 8 (m / 4) + 4 t + m % 4) the result leaves each lane the 8
-// neighbouring positions 8 g .. 8 g + 7 of one column, g = lane / 16, which is
+// keys: one position, 8 components); with the positions of the two 16-row tiles
+// interleaved (tile t, row m is position 8 (m / 4) + 4 t + m % 4) the result
+// leaves each lane the 8 neighbouring positions 8 g .. 8 g + 7 of one column, g = lane / 16, which is
 // just the operand that O^T = V^T P^T takes.  Of the values a lane takes D / 16
 // neighbouring components of its 8 positions and turns that block by one byte
 // permute per operand register.  No value crosses lanes in the loop but the
@@ -246,8 +246,9 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
 //  * own positions: HBM.  131071 positions of one row, 537 MB: 96 us, 5.6 TB/s;
 //    the wavefronts' ranges are equal but end between 70 and 91 us.
 //  * a prefix of 128 columns: a wavefront's chain of LDS reads, products, weights
-//    and products, some 1900 clocks a unit, with HBM half idle (64 rows behind
-//    16384 positions and up to 1024 of their own, 202 MB: 55 us).
+//    and products, 1.1 us a unit, and 1.4 beside own positions, behind whose
+//    loads its own wait (64 rows behind 16384 positions and up to 1024 of their
+//    own, 202 MB: 55 us).
 //  * short calls: launch, the lengths, page numbers, keys and values one after
 //    the other (512 positions of one row: 6.2 us).
 
@@ -945,9 +946,10 @@ __device__ __forceinline__ void wait_and_meet() {
 // LDS, loaded straight from the pages (a quarter of a unit's rows per
 // wavefront, kRing - 1 units ahead), so a unit is read once per workgroup.
 // One barrier per unit i: behind it unit i + 1 has landed for all, so that its
-// keys can be read while unit i is weighed, and the slot of unit i - 1 is free.  A slot holds 32 rows of keys, then of values; the
-// 16-byte pieces of a key row are permuted by the row, so that the 16 rows
-// that one operand read touches lie in 64 different banks.
+// keys can be read while unit i is weighed, and the slot of unit i - 1 is free.
+// A slot holds 32 rows of keys, then of values; the 16-byte pieces of a key row
+// are permuted by the row, so that the 16 rows that one operand read touches lie
+// in 64 different banks.
 template <int D, int NT>
 __device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment& it, uint8_t* slots) {
   using S = AttendShape<D>;
