@@ -464,8 +464,10 @@ typedef struct {
  * scale finite and > 0.  head_dim 64, 96, 128, 192 or 256; q_heads a
  * multiple of kv_heads, at most 64 times it; at most 4096 rows, 2^22 rows *
  * q_heads and 512 groups; cols * page_len <= 2^22.
- * Softmax statistics and sums in FP32; the weights w are rounded to BF16 for
- * the matrix cores (each by at most 2^-8 of itself, as the output is).
+ * Softmax statistics and sums in FP32.  The weights w enter the matrix cores
+ * with 16 bits (each off by at most 2^-16 of itself), or with 8 (2^-8, as the
+ * output's own rounding) where a group's prefix has more than 64 query heads
+ * of one key-value head in all its rows, or a key-value head has more than 16.
  * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
  * nwc_attend_workspace_size bytes for these rows, q_heads and group count;
  * no initial content needed); calls that share it must not run concurrently.

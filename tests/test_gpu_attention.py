@@ -431,6 +431,36 @@ def test_attend_sharp_and_flat_softmax(covers):
     assert not bool(b.out[2].isnan().any())
 
 
+@pytest.mark.parametrize("covers", [0, 4000])
+@pytest.mark.parametrize("hq,hk,d,page", [(32, 8, 128, 64), (16, 1, 64, 16), (5, 5, 96, 32), (8, 1, 256, 16), (10, 5, 192, 32)])
+def test_attend_weights_of_16_bits(hq, hk, d, page, covers):
+    # up to 16 columns a wavefront a weight is two BF16 values: the first leaves at most 2^-8 of it, the second 2^-8 of that
+    _say("attend 16-bit weights %d %d %d %d %d" % (hq, hk, d, page, covers))
+    groups = [(0, 4, 70), (6, 8, 33)] if 4 * hq // hk <= 64 else []
+    b = _Batch([75, 90, 71, 104, 2, 3, 40, 35, 17, 64, 333], hq, hk, d, page, groups, seed=hq + d, covers=covers)
+    nwc.nwc_attend(b.call())
+    torch.cuda.synchronize()
+    out, size = _ref_attend(b.kp, b.vp, b.table, b.lengths, b.q, b.scale)
+    err = (b.out[:len(b.lengths)].double() - out).abs()
+    tol = 2.0 ** -8 * out.abs() + (2.0 ** -16 + 2.0 ** -10) * size
+    assert bool((err <= tol).all()), "%g over its tolerance" % float((err - tol).max())
+
+
+@pytest.mark.parametrize("covers", [0, 4000])
+@pytest.mark.parametrize("hq,hk,d,page", SHAPES + [(20, 1, 128, 16), (32, 1, 64, 32)])
+def test_attend_of_equal_values_is_the_value(hq, hk, d, page, covers):
+    # the weights that the products take add up to the sum that they are divided by, to 2^-16 and FP32's 2^-24 a term
+    # (1100 terms: 2^-13): far less than half a step of BF16, so what every position holds comes back as it is
+    _say("attend equal values %d %d %d %d %d" % (hq, hk, d, page, covers))
+    b = _Batch([600, 640, 555, 1100, 700, 600, 1, 33], hq, hk, d, page, [(0, 6, 550)], seed=hq * d, spread=3.0, covers=covers)
+    value = _randn(torch.Generator(device="cuda").manual_seed(5), 1, hk, 1, d)
+    b.vp.copy_(value.expand_as(b.vp))
+    nwc.nwc_attend(b.call())
+    torch.cuda.synchronize()
+    want = value[0, :, 0].repeat_interleave(hq // hk, 0)
+    assert torch.equal(b.out[:8], want.expand(8, hq, d))
+
+
 @pytest.mark.parametrize("more", [0, 300])
 def test_attend_strided_rows_and_far_pages(more):
     # queries inside a joint projection's rows, outputs inside a wider buffer, pages more than 2^32 elements apart
