@@ -1418,14 +1418,14 @@ nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uin
 // Positions that a table may cover for k_attend_rows to take it, by the number of
 // its workgroups (rows times key-value heads) against the compute units.
 // Measured (32 / 8 heads of 128, us a call in a graph, k_attend_rows and k_attend
-// + k_attend_join): 1 row of 512: 5.7 and 7.7, 1024: 8.2 and 7.7; 4 rows of 1024:
-// 9.4 and 10.5, 2048: 14.4 and 12.6; 16 rows of 2048: 28.4 and 30.7, ragged to
-// 2048: 16.0 and 18.3, to 4096: 46.4 and 33.3; 64 rows of 2048: 95.5 and 100.1.
+// + k_attend_join): 1 row of 512: 6.2 and 7.7, 1024: 8.6 and 7.6; 4 rows of 1024:
+// 9.8 and 10.9, 2048: 15.1 and 12.7; 16 rows of 2048: 28.7 and 31.2, ragged to
+// 2048: 16.6 and 19.1, to 4096: 45.0 and 33.0; 64 rows of 2048: 92.9 and 97.8.
 // Heads of 256, whose keys have no room in LDS, gain less: 1 row of 256 positions
-// (8 / 4 heads) 8.7 and 10.3, of 512 13.2 and 10.2; 32 rows of 1024 35.8 and 40.8.
+// (8 / 4 heads) 8.8 and 10.4, of 512 13.4 and 10.3; 32 rows of 1024 38.1 and 39.9.
 // Rows that share a prefix read it each for itself here, from the caches, which
 // is faster while that is little: 16 rows behind 384 positions with 100 of their
-// own 6.6 and 13.0, 64 rows behind 896 18.1 and 21.7.
+// own 7.0 and 13.5, 64 rows behind 896 19.7 and 21.9.
 bool by_rows(uint32_t d, uint64_t groups, uint32_t covers, bool shared) {
   const bool many = 2 * groups >= kCus;
   if (shared) return covers <= (d == 256 ? 256 : 1024) && groups * covers * d <= 1 << 26;
