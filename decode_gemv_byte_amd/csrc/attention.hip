@@ -565,32 +565,20 @@ struct Sums {
     // Weights relative to the maximum so far.  They may grow to 2^11 before the
     // maximum moves (BF16 and FP32 keep their relative precision), so the common
     // unit looks at no maximum at all: a lane's sum of 8 says whether one grew.
-    // The matrix cores take them as BF16.  With 16 columns a wavefront what that
-    // rounding leaves goes through a second product, so the weights keep 16 bits
-    // (512 positions of one row 5.9 -> 6.2 us, 8 rows behind 4096 14.2 -> 14.6,
-    // long rows the same; the error from 1.3 to 1.4 times the output's rounding to
-    // that alone).  With 32 the weights are rounded once, by at most 2^-8 each, and
-    // their sum is of the rounded ones, so that they add up to one (the second
-    // product there: 64 rows behind 16384 positions 61 -> 65 us).
-    constexpr bool kTwice = NT == 1;
+    // The matrix cores take them as BF16, and what that rounding leaves goes
+    // through a second product, so the weights keep 16 bits: the error against 64
+    // bits is the output's own rounding alone, with one product 1.3 to 1.4 times
+    // that.  (512 positions of one row 5.9 -> 6.2 us, 64 rows behind 16384 61 ->
+    // 64, six groups of 16 49 -> 50, 32 rows behind 4096 with heads of 256 32 ->
+    // 33, long rows the same.)
     float p[NT][8], sum[NT];
-    u32x4_t w[NT];
     auto weigh = [&] {
       bool grown = false;
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
-        float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[c][j] = x[j] = __builtin_amdgcn_exp2f(fmaf(sc[j / 4][c][j % 4], scale2, -m[c]));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          w[c][j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-          if (!kTwice) {
-            x[2 * j] = bf16_lo(w[c][j]);
-            x[2 * j + 1] = bf16_hi(w[c][j]);
-          }
-        }
-        sum[c] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+        for (int j = 0; j < 8; ++j) p[c][j] = __builtin_amdgcn_exp2f(fmaf(sc[j / 4][c][j % 4], scale2, -m[c]));
+        sum[c] = ((p[c][0] + p[c][1]) + (p[c][2] + p[c][3])) + ((p[c][4] + p[c][5]) + (p[c][6] + p[c][7]));
         grown |= !(sum[c] <= 2048.f);
       }
       return grown;
@@ -613,26 +601,28 @@ struct Sums {
     }
 #pragma unroll
     for (int c = 0; c < NT; ++c) l[c] += sum[c];
+    u32x4_t w[NT], rest[NT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[c][j] = pack_bf16(p[c][2 * j], p[c][2 * j + 1]);
+        rest[c][j] = pack_bf16(p[c][2 * j] - bf16_lo(w[c][j]), p[c][2 * j + 1] - bf16_hi(w[c][j]));
+      }
     auto add = [&](int d, int c, u32x4_t v, u32x4_t y) {
       o[d][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, y),
                                                         o[d][c], 0, 0, 0);
     };
-    u32x4_t v[kDt];
 #pragma unroll
     for (int d = 0; d < kDt; ++d) {
+      u32x4_t v;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        v[d][j] = __builtin_amdgcn_perm(vr[2 * j + 1][d / 2], vr[2 * j][d / 2], d % 2 ? 0x07060302 : 0x05040100);
+        v[j] = __builtin_amdgcn_perm(vr[2 * j + 1][d / 2], vr[2 * j][d / 2], d % 2 ? 0x07060302 : 0x05040100);
 #pragma unroll
-      for (int c = 0; c < NT; ++c) add(d, c, v[d], w[c]);
-    }
-    if constexpr (kTwice) {
-      u32x4_t rest;
+      for (int c = 0; c < NT; ++c) add(d, c, v, w[c]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        rest[j] = pack_bf16(p[0][2 * j] - bf16_lo(w[0][j]), p[0][2 * j + 1] - bf16_hi(w[0][j]));
-#pragma unroll
-      for (int d = 0; d < kDt; ++d) add(d, 0, v[d], rest);
+      for (int c = 0; c < NT; ++c) add(d, c, v, rest[c]);
     }
   }
 

@@ -465,9 +465,7 @@ typedef struct {
  * multiple of kv_heads, at most 64 times it; at most 4096 rows, 2^22 rows *
  * q_heads and 512 groups; cols * page_len <= 2^22.
  * Softmax statistics and sums in FP32.  The weights w enter the matrix cores
- * with 16 bits (each off by at most 2^-16 of itself), or with 8 (2^-8, as the
- * output's own rounding) where a group's prefix has more than 64 query heads
- * of one key-value head in all its rows, or a key-value head has more than 16.
+ * with 16 bits (each off by at most 2^-16 of itself).
  * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
  * nwc_attend_workspace_size bytes for these rows, q_heads and group count;
  * no initial content needed); calls that share it must not run concurrently.

@@ -1,0 +1,66 @@
+"""What attention over the paged cache makes of its numbers: how exactly a weight
+is kept, scores and values at the ends of their range, infinities.
+
+Tolerances, from the roundings (BF16: half a step, 2^-8 of the value): the
+output's, 2^-8 |out|; a weight that the products take as two BF16 values, 2^-8
+of what the first leaves, 2^-16 sum w |v|; scores, exponentials and sums in FP32
+below 2^-10 sum w |v| (at |score| <= 64: 64 2^-24 from the exponent, head_dim
+2^-24 from the sum).
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+import decode_gemv_byte_amd as nwc  # noqa: E402
+from test_gpu_attention import SHAPES, _Batch, _ref_attend, _say  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def _run(b):
+    nwc.nwc_attend(b.call())
+    torch.cuda.synchronize()
+
+
+def _reference(b):
+    """(out, sum w |v|) in 64 bits of the rows that are no padding."""
+    live = torch.from_numpy(b.lengths >= 0).cuda()
+    out, size = _ref_attend(b.kp, b.vp, b.table, b.lengths, b.q, b.scale)
+    return live, out[live], size[live]
+
+
+def _check(b, what):
+    """Every finite component within the tolerance, every other one the reference's."""
+    live, out, size = _reference(b)
+    got = b.out[:len(b.lengths)][live].double()
+    same = got == out
+    assert bool((got.isnan() == out.isnan()).all()), "%s: NaN in other places" % what
+    assert bool((same | ~out.isinf()).all()), "%s: other infinities" % what
+    err = torch.where(out.isfinite(), (got - out).abs(), 0.0)
+    tol = 2.0 ** -8 * out.abs() + (2.0 ** -16 + 2.0 ** -10) * size
+    assert bool((err <= tol)[out.isfinite()].all()), "%s: %g over its tolerance" % (what, float((err - tol)[out.isfinite()].max()))
+
+
+def _slots(b, r):
+    """Pages and slots of a row's positions."""
+    page = b.kp.shape[2]
+    at = np.arange(max(0, int(b.lengths[r])))
+    return torch.from_numpy(b.table[r, at // page]).cuda(), torch.from_numpy(at % page).cuda()
+
+
+@pytest.mark.parametrize("covers", [0, 4000])
+@pytest.mark.parametrize("hq,hk,d,page", SHAPES + [(20, 1, 128, 16), (32, 1, 64, 32)])
+def test_attend_every_weight_keeps_16_bits(hq, hk, d, page, covers):
+    # position p holds 1 in component p alone, so that component is its weight, and no other weight's rounding averages
+    # with its own; a weight rounded once would be off by 2^-8 before the output's rounding.  20 rows behind one prefix: blocks
+    # of up to 128 columns
+    _say("every weight %d %d %d %d %d" % (hq, hk, d, page, covers))
+    shared = d // 2 + 3
+    lengths = [shared + r % (d - shared) + 1 for r in range(20)] + [d, d - 1, 33, 5, 2, 1]
+    b = _Batch(lengths, hq, hk, d, page, [(0, 20, shared)], seed=hq + d, spread=1.5, covers=covers)
+    one = torch.eye(d, dtype=torch.bfloat16, device="cuda")
+    for r, n in enumerate(lengths):
+        pages, slots = _slots(b, r)
+        b.vp[pages, :, slots] = one[:n, None].expand(n, hk, d)
+    _run(b)
+    _check(b, "weights")
