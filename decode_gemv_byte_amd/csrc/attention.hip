@@ -255,7 +255,7 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
 constexpr uint32_t kCap = 128;        // columns of a prefix block: 4 wavefronts of 2 16-column tiles
 constexpr uint32_t kWaveRatio = 32;   // most query heads per key-value head that one wavefront takes
 constexpr int kAttendThreads = 256;
-constexpr float kNoMax = -1e30f;      // the maximum of nothing: finite, so that exp2(-inf - it) is 0 (scores below it weigh 0)
+constexpr float kNoMax = -3.402823466e+38f;  // the maximum of nothing, no greater than any score and finite, so that exp2(-inf - it) is 0
 
 template <int D>
 struct AttendShape {
@@ -275,7 +275,7 @@ struct AttendArgs {
   uint32_t hq, hkv, ratio, n_groups;
   float scale2;             // scale * log2(e)
   float* part_o;            // workspace: partial sums [column slot][D]
-  float* part_ml;           // their maxima (log2 domain) and weight sums
+  float* part_ml;           // their maxima and weight sums
   uint32_t* plan;           // the plan for k_attend_join
   uint64_t own_slot;        // first column slot of the own positions' parts
   uint32_t cap_p, cap_o;    // column slots of a worker's part: prefixes, own positions
@@ -524,8 +524,11 @@ __device__ __forceinline__ void load_queries(const AttendArgs& a, const Segment&
 
 // A wavefront's running sums for NT tiles of 16 columns: lane (n, g) holds column
 // n, components kDt (4 g + i) + t of O (tile t, i = 0 .. 3), the maximum of the
-// scores so far (log2 domain, the same in a column's four lanes) and its own
-// part of the sum of the weights.
+// scores so far (as the product gives them, the same in a column's four lanes)
+// and its own part of the sum of the weights.  A weight is exp2((score - maximum)
+// scale2): the difference first, since a scaled maximum's rounding alone would
+// pass 2^7, FP32's largest exponent, where it stands at 2^31 and beyond.  (An
+// instruction more a score: 64 rows behind 16384 positions 64.2 -> 65.2 us.)
 template <int D, int NT>
 struct Sums {
   static constexpr int kDt = AttendShape<D>::kDt;
@@ -577,7 +580,7 @@ struct Sums {
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[c][j] = __builtin_amdgcn_exp2f(fmaf(sc[j / 4][c][j % 4], scale2, -m[c]));
+        for (int j = 0; j < 8; ++j) p[c][j] = __builtin_amdgcn_exp2f((sc[j / 4][c][j % 4] - m[c]) * scale2);
         sum[c] = ((p[c][0] + p[c][1]) + (p[c][2] + p[c][3])) + ((p[c][4] + p[c][5]) + (p[c][6] + p[c][7]));
         grown |= !(sum[c] <= 2048.f);
       }
@@ -587,11 +590,11 @@ struct Sums {
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
         float x = fmaxf(fmaxf(sc[0][c][0], sc[0][c][1]), fmaxf(sc[0][c][2], sc[0][c][3]));
-        x = fmaxf(x, fmaxf(fmaxf(sc[1][c][0], sc[1][c][1]), fmaxf(sc[1][c][2], sc[1][c][3]))) * scale2;
+        x = fmaxf(x, fmaxf(fmaxf(sc[1][c][0], sc[1][c][1]), fmaxf(sc[1][c][2], sc[1][c][3])));
         x = fmaxf(x, lane_xor(x, 16));
         x = fmaxf(x, lane_xor(x, 32));
         x = fmaxf(x, m[c]);
-        const float f = __builtin_amdgcn_exp2f(m[c] - x);
+        const float f = __builtin_amdgcn_exp2f((m[c] - x) * scale2);
         m[c] = x;
         l[c] *= f;
 #pragma unroll
@@ -905,7 +908,7 @@ __device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment&
     float top = acc.m[c];
 #pragma unroll
     for (int w = 0; w < W; ++w) top = fmaxf(top, s.m[w][16 * c + n]);
-    const float f = __builtin_amdgcn_exp2f(acc.m[c] - top);
+    const float f = __builtin_amdgcn_exp2f((acc.m[c] - top) * a.scale2);
     if (c) __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -924,7 +927,7 @@ __device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment&
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         sum += *reinterpret_cast<const f32x4_t*>(&join[w][col][e]);
-        total += s.l[w][cc] * __builtin_amdgcn_exp2f(s.m[w][cc] - best);
+        total += s.l[w][cc] * __builtin_amdgcn_exp2f((s.m[w][cc] - best) * a.scale2);
       }
       if (it.direct) {
         const float r = total == 0.f ? 0.f : 1.f / total;
@@ -1246,7 +1249,8 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs
       const uint64_t at = i < n0 ? slot0 + static_cast<uint64_t>(i) * a.cap_p : slot1 + static_cast<uint64_t>(i - n0) * a.cap_o;
       const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
       const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part_o + at * D + e);
-      const float top = fmaxf(best, ml.x), f = __builtin_amdgcn_exp2f(best - top), f2 = __builtin_amdgcn_exp2f(ml.x - top);
+      const float top = fmaxf(best, ml.x);
+      const float f = __builtin_amdgcn_exp2f((best - top) * a.scale2), f2 = __builtin_amdgcn_exp2f((ml.x - top) * a.scale2);
       sum = sum * f + x * f2;
       total = total * f + ml.y * f2;
       best = top;
@@ -1264,7 +1268,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs
   total = 0.f;
 #pragma unroll
   for (uint32_t i = 0; i < kLines; ++i) {
-    const float f = __builtin_amdgcn_exp2f(ms[i] - best);
+    const float f = __builtin_amdgcn_exp2f((ms[i] - best) * a.scale2);
     sum += sums[i][e / 4] * f;
     total += ls[i] * f;
   }

@@ -464,7 +464,8 @@ typedef struct {
  * scale finite and > 0.  head_dim 64, 96, 128, 192 or 256; q_heads a
  * multiple of kv_heads, at most 64 times it; at most 4096 rows, 2^22 rows *
  * q_heads and 512 groups; cols * page_len <= 2^22.
- * Softmax statistics and sums in FP32.  The weights w enter the matrix cores
+ * Softmax statistics and sums in FP32, scores and their differences of any
+ * size that FP32 holds.  The weights w enter the matrix cores
  * with 16 bits (each off by at most 2^-16 of itself).
  * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
  * nwc_attend_workspace_size bytes for these rows, q_heads and group count;

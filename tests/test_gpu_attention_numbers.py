@@ -64,3 +64,21 @@ def test_attend_every_weight_keeps_16_bits(hq, hk, d, page, covers):
         b.vp[pages, :, slots] = one[:n, None].expand(n, hk, d)
     _run(b)
     _check(b, "weights")
+
+
+@pytest.mark.parametrize("covers", [0, 4000])
+@pytest.mark.parametrize("hq,hk,d,page", SHAPES)
+def test_attend_scores_of_any_size(hq, hk, d, page, covers):
+    # finite scores far from zero: below -1e30 (all equal: the values' mean), above 1e30, and so far apart that the largest
+    # takes all, of either sign; keys and queries are powers of two times at most 8 bits, so FP32 holds each score exactly
+    _say("scores of any size %d %d %d %d %d" % (hq, hk, d, page, covers))
+    b = _Batch([300, 77, 300, 300, 1], hq, hk, d, page, seed=hq * d, covers=covers)
+    rnd = np.random.default_rng(d)
+    for r, (q, k, steps) in enumerate(((2.0 ** 50, -2.0 ** 50, 0), (2.0 ** 50, 2.0 ** 50, 0), (2.0 ** 18, 2.0 ** 18, 127),
+                                       (2.0 ** 18, -2.0 ** 18, 127), (2.0 ** 20, -2.0 ** 20, 0))):
+        pages, slots = _slots(b, r)
+        b.q[r] = q
+        key = k * (1 + rnd.integers(0, steps + 1, int(b.lengths[r])) / 128)
+        b.kp[pages, :, slots] = torch.tensor(key, device="cuda").to(torch.bfloat16)[:, None, None].expand(len(key), hk, d)
+    _run(b)
+    _check(b, "scores")
