@@ -463,6 +463,9 @@ struct Segment {
   uint32_t u0, u1;      // units (position / 32)
   uint32_t p0, p1;      // positions that the item sees
   bool direct;          // the whole of its row's positions: the output itself, no partial sums
+  bool prefix;          // a group's: of its rows those count that share it, where groups[row] == group
+  uint32_t group;
+  const uint32_t* groups;
   uint64_t slot;        // first column slot of the partial sums
 };
 
@@ -474,6 +477,11 @@ __device__ __forceinline__ uint64_t part_slot(const AttendArgs& a, bool prefix, 
                                               uint64_t worker) {
   return (prefix ? 0 : a.own_slot) + (static_cast<uint64_t>(head) * a.pages.rows + row) * a.ratio + col0 +
          worker * (prefix ? a.cap_p : a.cap_o);
+}
+
+// Whether a column is one of the item's, of a row that takes part in it.
+__device__ __forceinline__ bool counts(const AttendArgs& a, const Segment& it, uint32_t col) {
+  return col < it.cols && (!it.prefix || it.groups[it.row0 + (it.col0 + col) / a.ratio] == it.group);
 }
 
 // A wave-uniform read of an array that this grid does not write (scalar load).
@@ -503,7 +511,8 @@ __device__ __forceinline__ PagePart page_part(const AttendArgs& a, const Segment
 }
 
 // The queries of NT tiles of 16 columns from col on: lane (n, g) has column n,
-// components 32 k + 8 g .. of step k; zeros past the item's last column.
+// components 32 k + 8 g .. of step k; zeros past the item's last column and for
+// rows that take no part (a padding row's may be anything).
 template <int D, int NT>
 __device__ __forceinline__ void load_queries(const AttendArgs& a, const Segment& it, uint32_t col,
                                              u32x4_t (&qf)[AttendShape<D>::kKs][NT]) {
@@ -511,7 +520,7 @@ __device__ __forceinline__ void load_queries(const AttendArgs& a, const Segment&
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
     const uint32_t x = col + 16 * c + n;
-    const bool live = x < it.cols;
+    const bool live = counts(a, it, x);
     const uint32_t at = it.col0 + (live ? x : 0), row = it.row0 + at / a.ratio, h = it.head * a.ratio + at % a.ratio;
     const uint16_t* p = a.q + row * a.ldq + static_cast<uint64_t>(h) * D + 8 * g;
 #pragma unroll
@@ -629,6 +638,30 @@ struct Sums {
     }
   }
 
+  // Which of the wavefront's columns, that count, from col on have a sum that is
+  // no finite number (0 times an infinity or a NaN is NaN): a bit each.
+  __device__ __forceinline__ uint32_t lost(const AttendArgs& a, const Segment& it, uint32_t col) const {
+    bool bad[NT], any = false;
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      f32x4_t t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int d = 0; d < kDt; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = fmaf(o[d][c][i], 0.f, t[i]);
+      any |= bad[c] = !((t[0] + t[1]) + (t[2] + t[3]) == 0.f);
+    }
+    if (__builtin_expect(!__any(any), 1)) return 0;
+    uint32_t which = 0;
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      uint64_t lanes = __ballot(bad[c] && counts(a, it, col + 16 * c + __lane_id() % 16));
+      lanes |= lanes >> 32;
+      which |= static_cast<uint32_t>((lanes | lanes >> 16) & 0xFFFF) << (16 * c);
+    }
+    return which;
+  }
+
   // The columns' weight sums complete in all four lanes.
   __device__ __forceinline__ void finish() {
 #pragma unroll
@@ -638,13 +671,14 @@ struct Sums {
     }
   }
 
-  // The wavefront's columns from col on, complete: outputs or partial sums.
-  __device__ __forceinline__ void store(const AttendArgs& a, const Segment& it, uint32_t col) const {
+  // The wavefront's columns from col on but those in skip, complete: outputs or
+  // partial sums.
+  __device__ __forceinline__ void store(const AttendArgs& a, const Segment& it, uint32_t col, uint32_t skip) const {
     const uint32_t n = __lane_id() % 16, g = __lane_id() / 16;
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
       const uint32_t cc = col + 16 * c + n;
-      if (cc >= it.cols) continue;
+      if (cc >= it.cols || skip >> (16 * c + n) & 1) continue;
       const float r = l[c] == 0.f ? 0.f : 1.f / l[c];
       const uint32_t cl = it.col0 + cc, row = it.row0 + cl / a.ratio, h = it.head * a.ratio + cl % a.ratio;
 #pragma unroll
@@ -670,6 +704,82 @@ struct Sums {
     }
   }
 };
+
+// Columns of an item once more, those with a bit in `which` (of column col), by
+// one wavefront, for sums that came out infinite or NaN: the products with both
+// parts of a weight lose an infinite value's place, since the second part may be
+// zero or negative.  Here the maximum and the sum of the weights come first, then the
+// values, each once with its share of one, in FP32, so that an infinite value
+// gives its infinity (NaN where two signs meet).  A lane has one position of 64 at
+// a time, then D / 64 components.  (Asking for it costs the others at most 0.4
+// us a call, and 1.5 of 34 where heads of 256 spill; with an infinite value in
+// every row 512 positions of one row take 160 us, 131071 1.9 ms.)
+template <int D>
+__device__ void redo(const AttendArgs& a, const Segment& it, uint32_t col, uint32_t which) {
+  constexpr uint32_t kPer = (D + 63) / 64;
+  const uint32_t lane = __lane_id();
+  const uint32_t first = max(32 * it.u0, it.p0), last = min(32 * it.u1, it.p1);
+  for (; which; ++col, which >>= 1) {
+    if (!(which & 1)) continue;
+    const uint32_t cl = it.col0 + col, row = it.row0 + cl / a.ratio, h = it.head * a.ratio + cl % a.ratio;
+    const uint16_t* q = a.q + row * a.ldq + static_cast<uint64_t>(h) * D;
+    uint64_t off;  // of the lane's position; all ones: not seen
+    auto score = [&](uint32_t pos) {
+      const int32_t id = pos < last ? it.ids[pos >> a.pages.shift] : -1;
+      const PagePart p = page_part(a, it, id, pos, D);
+      off = p.known ? p.off : ~uint64_t{0};
+      if (!p.known) return -INFINITY;
+      float s = 0.f;
+#pragma unroll 1
+      for (uint32_t e = 0; e < D; e += 8) {
+        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(q + e), y = *reinterpret_cast<const u32x4_t*>(a.k + p.off + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fmaf(bf16_hi(x[j]), bf16_hi(y[j]), fmaf(bf16_lo(x[j]), bf16_lo(y[j]), s));
+      }
+      return s;
+    };
+    float best = kNoMax, total = 0.f, o[kPer];
+    for (uint32_t pos = first + lane; pos < last; pos += kWave) best = fmaxf(best, score(pos));
+    for (int x = 32; x; x /= 2) best = fmaxf(best, lane_xor(best, x));
+    auto weight = [&](float s) { return __builtin_amdgcn_exp2f((s - best) * a.scale2); };
+    for (uint32_t pos = first + lane; pos < last; pos += kWave) total += weight(score(pos));
+    for (int x = 32; x; x /= 2) total += lane_xor(total, x);
+    const float r = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+    for (uint32_t i = 0; i < kPer; ++i) o[i] = 0.f;
+    for (uint32_t pos = first; pos < last; pos += kWave) {
+      const float s = score(pos + lane), w = weight(s) * r;
+      for (uint32_t j = 0; j < kWave; ++j) {
+        auto of = [&](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), j)); };
+        const float sj = __builtin_bit_cast(float, of(__builtin_bit_cast(uint32_t, s)));
+        const float wj = __builtin_bit_cast(float, of(__builtin_bit_cast(uint32_t, w)));
+        const uint64_t at = of(static_cast<uint32_t>(off)) | static_cast<uint64_t>(of(off >> 32)) << 32;
+        if (at == ~uint64_t{0}) continue;
+        const uint16_t* v = a.v + at;
+#pragma unroll
+        for (uint32_t i = 0; i < kPer; ++i)
+          if (D % kWave == 0 || lane + kWave * i < D) {
+            const float x = bf16_lo(v[lane + kWave * i]);
+            // a weight too small for FP32 is yet above zero
+            o[i] += wj == 0.f && sj != -INFINITY && __builtin_isinf(x) ? x : wj * x;
+          }
+      }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kPer; ++i) {
+      const uint32_t e = lane + kWave * i;
+      if (D % kWave && e >= D) continue;
+      if (it.direct)
+        a.out[row * a.ldo + static_cast<uint64_t>(h) * D + e] = static_cast<uint16_t>(pack_bf16(o[i], 0.f));
+      else
+        a.part_o[(it.slot + col) * D + e] = o[i] * total;
+    }
+    if (!it.direct && lane == 0) {
+      a.part_ml[2 * (it.slot + col)] = best;
+      a.part_ml[2 * (it.slot + col) + 1] = total;
+    }
+  }
+}
 
 // Where piece c of key row `row` (0 .. 31 of a unit) lies in its slot row, and
 // (INVERSE) which piece lies at c.  An operand read takes one piece of the rows
@@ -875,11 +985,23 @@ __device__ __forceinline__ void walk_units(const AttendArgs& a, const Segment& i
     walk<D, NT>(a, it, u, step, acc);
 }
 
+// A wavefront's part of an item of at most 16 NT columns.
+template <int D, int NT>
+__device__ __forceinline__ void attend_alone(const AttendArgs& a, const Segment& it, uint8_t* slots) {
+  Sums<D, NT> acc;
+  walk_units<D, NT, 4>(a, it, it.u0, 1, slots, acc);
+  const uint32_t lost = acc.lost(a, it, 0);
+  acc.finish();
+  if (__builtin_expect(lost == 0, 1)) return acc.store(a, it, 0, 0);
+  acc.store(a, it, 0, lost);
+  redo<D>(a, it, 0, lost);
+}
+
 // LDS of a workgroup: the fixed part, then the plan, then the ring of slots or
 // the sums that the wavefronts exchange (never both).
 struct LdsFixed {
   float m[8][32], l[8][32];  // [wavefront][column]
-  uint32_t carry[8];
+  uint32_t carry[8], lost[8];
 };
 template <int D, int W>
 using Join = float[W][16][AttendShape<D>::kJLd];
@@ -895,6 +1017,8 @@ __device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment&
   Sums<D, NT> acc;
   __syncthreads();  // the last readers of what lies there are done
   walk_units<D, NT, W>(a, it, it.u0 + wave, W, big + wave * key_slots(D), acc);
+  const uint32_t lost = acc.lost(a, it, 0);
+  if (__lane_id() == 0) s.lost[wave] = lost;
   acc.finish();
   if (g == 0)
 #pragma unroll
@@ -903,6 +1027,10 @@ __device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment&
       s.l[wave][16 * c + n] = acc.l[c];
     }
   __syncthreads();
+  uint32_t any = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) any |= s.lost[w];
+  any = uniform(any);
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
     float top = acc.m[c];
@@ -919,7 +1047,7 @@ __device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment&
     __syncthreads();
     for (uint32_t i = tid; i < 16 * (D / 4); i += W * kWave) {
       const uint32_t col = i / (D / 4), e = i % (D / 4) * 4, cc = 16 * c + col;
-      if (cc >= it.cols) continue;
+      if (cc >= it.cols || any >> cc & 1) continue;
       f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
       float total = 0.f, best = s.m[0][cc];
 #pragma unroll
@@ -943,6 +1071,8 @@ __device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment&
       }
     }
   }
+  static_assert(W == 4 || W == 8, "the wavefronts' bits");
+  if (__builtin_expect(any != 0, 0)) redo<D>(a, it, 0, any & (W == 4 ? 0x11111111u : 0x01010101u) << wave);
 }
 
 // Wait until at most N of this wavefront's vector memory operations are left
@@ -1056,8 +1186,12 @@ __device__ __forceinline__ void attend_shared(const AttendArgs& a, const Segment
     acc.take(sc, x.vr, it, 32 * (it.u0 + i), (seen >> (2 * (i % 16) + g / 2) & 1) != 0, a.scale2);
     at = after;
   }
+  const uint32_t col = wave * (16 * NT);
+  const uint32_t lost = acc.lost(a, it, col);
   acc.finish();
-  acc.store(a, it, wave * (16 * NT));
+  if (__builtin_expect(lost == 0, 1)) return acc.store(a, it, col, 0);
+  acc.store(a, it, col, lost);
+  redo<D>(a, it, col, lost);
 }
 
 // Largest i in [0, n) with pre[i] <= x (pre ascending, pre[0] = 0).
@@ -1088,6 +1222,7 @@ __device__ __forceinline__ Segment own_segment(const AttendArgs& a, const Plan& 
   it.u0 = first + done;
   it.u1 = it.u0 + static_cast<uint32_t>(min(static_cast<uint64_t>(units - done), left));
   it.direct = it.p0 == 0 && it.u1 - it.u0 == units;
+  it.prefix = false;
   it.slot = part_slot(a, false, head, r, 0, worker);
   return it;
 }
@@ -1110,6 +1245,9 @@ __device__ __forceinline__ Segment prefix_segment(const AttendArgs& a, const Pla
   it.u0 = done;
   it.u1 = done + static_cast<uint32_t>(min(static_cast<uint64_t>(units - done), left));
   it.direct = false;
+  it.prefix = true;
+  it.group = i;
+  it.groups = p.row_group;
   it.slot = part_slot(a, true, head, it.row0, it.col0, worker);
   return it;
 }
@@ -1158,15 +1296,9 @@ __global__ __launch_bounds__(kAttendThreads, D <= 128 ? 2 : 1) void k_attend(con
       const uint32_t head = static_cast<uint32_t>(at / own_units);
       const Segment it = own_segment(a, p, head, static_cast<uint32_t>(at % own_units), end - at, worker);
       if (a.ratio <= 16) {
-        Sums<D, 1> acc;
-        walk_units<D, 1, 4>(a, it, it.u0, 1, slots, acc);
-        acc.finish();
-        acc.store(a, it, 0);
+        attend_alone<D, 1>(a, it, slots);
       } else if (a.ratio <= kWaveRatio) {
-        Sums<D, 2> acc;
-        walk_units<D, 2, 4>(a, it, it.u0, 1, slots, acc);
-        acc.finish();
-        acc.store(a, it, 0);
+        attend_alone<D, 2>(a, it, slots);
       } else {
         attend_shared<D, 1>(a, it, big);
       }
@@ -1197,6 +1329,7 @@ __global__ __launch_bounds__(AttendShape<D>::kRowWaves * kWave) void k_attend_ro
   it.u0 = 0;
   it.u1 = (it.p1 + 31) / 32;
   it.direct = true;
+  it.prefix = false;
   it.slot = 0;
   if (it.cols <= 16)
     attend_turns<D, 1, kRowWaves>(a, it, s, lds);

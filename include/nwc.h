@@ -466,7 +466,11 @@ typedef struct {
  * q_heads and 512 groups; cols * page_len <= 2^22.
  * Softmax statistics and sums in FP32, scores and their differences of any
  * size that FP32 holds.  The weights w enter the matrix cores
- * with 16 bits (each off by at most 2^-16 of itself).
+ * with 16 bits (each off by at most 2^-16 of itself).  An infinity among the
+ * values that a row sees is its component's result (NaN where two signs meet),
+ * a NaN stays in its component; a score of +infinity or NaN makes the head's
+ * output NaN, and a row whose scores are all -infinity gives zeros.  Rows with
+ * results that are not finite take longer.
  * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
  * nwc_attend_workspace_size bytes for these rows, q_heads and group count;
  * no initial content needed); calls that share it must not run concurrently.

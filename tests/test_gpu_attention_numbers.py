@@ -82,3 +82,40 @@ def test_attend_scores_of_any_size(hq, hk, d, page, covers):
         b.kp[pages, :, slots] = torch.tensor(key, device="cuda").to(torch.bfloat16)[:, None, None].expand(len(key), hk, d)
     _run(b)
     _check(b, "scores")
+
+
+@pytest.mark.parametrize("covers", [0, 4000])
+@pytest.mark.parametrize("hq,hk,d,page", SHAPES + [(20, 1, 128, 16), (32, 1, 64, 32)])
+def test_attend_infinite_values(hq, hk, d, page, covers):
+    # an infinity among the seen values is its component's result, NaN where two signs meet; the other components keep their
+    # exactness, and a padding row inside a group, whose queries may be anything, changes nothing (rows that share a prefix get the
+    # same values there, in copied pages too)
+    _say("infinite values %d %d %d %d %d" % (hq, hk, d, page, covers))
+    lengths = [75, 90, -1, 104, 2, 1, 40, 35, 35, 5, 1] + [640] * 9 + [500, 1300, 64, 333]
+    b = _Batch(lengths, hq, hk, d, page, [(0, 7, 70), (7, 11, 17), (11, 20, 600)], seed=hq + d, covers=covers)
+    b.q[2] = float("nan")
+    b.q[5] = 0
+    inf = float("inf")
+    for r, n in enumerate(lengths):
+        if n > 0:
+            pages, slots = _slots(b, r)
+            for component, at, value in ((3, 0, inf), (5, n - 1, -inf), (7, 0, -inf), (7, n // 2, inf), (d - 1, n // 3, -inf)):
+                b.vp[pages[at], :, slots[at], component] = value
+    _run(b)
+    live, out, size = _reference(b)
+    assert bool(out[:, :, 3].isposinf().all()) and bool(out[:, :, 5].isneginf().all()) and bool(out[:, :, 9].isfinite().all())
+    _check(b, "infinite values")
+    assert bool((b.out[:len(lengths)][~live] == 7.0).all())
+
+
+@pytest.mark.parametrize("covers", [0, 4000])
+@pytest.mark.parametrize("hq,hk,d,page", SHAPES)
+def test_attend_nan_queries_stay_in_their_head(hq, hk, d, page, covers):
+    # its output is NaN; the columns beside it, which the same wavefront computes, are as they are without it
+    _say("nan queries %d %d %d %d %d" % (hq, hk, d, page, covers))
+    b = _Batch([640] * 9 + [75, 33, 1, 1300], hq, hk, d, page, [(0, 9, 600)], seed=hq + d, covers=covers)
+    for r, h in ((3, hq // 2), (4, 0), (9, hq - 1), (11, 0), (12, 0)):
+        b.q[r, h, d // 3] = float("nan")
+    _run(b)
+    _check(b, "nan queries")
+    assert int(b.out.isnan().sum()) == 5 * d
