@@ -274,7 +274,7 @@ struct AttendArgs {
   PageArgs pages;
   uint32_t hq, hkv, ratio, n_groups;
   float scale2;             // scale * log2(e)
-  float* part_o;            // workspace: partial sums [column slot][D]
+  float* part_o;            // workspace: means over a part of a column's positions [column slot][D]
   float* part_ml;           // their maxima and weight sums
   uint32_t* plan;           // the plan for k_attend_join
   uint64_t own_slot;        // first column slot of the own positions' parts
@@ -693,7 +693,7 @@ struct Sums {
         } else {
           float x[kDt];
 #pragma unroll
-          for (int d = 0; d < kDt; ++d) x[d] = o[d][c][i];
+          for (int d = 0; d < kDt; ++d) x[d] = o[d][c][i] * r;
           __builtin_memcpy(a.part_o + (it.slot + cc) * D + e, x, 4 * kDt);
         }
       }
@@ -706,14 +706,16 @@ struct Sums {
 };
 
 // Columns of an item once more, those with a bit in `which` (of column col), by
-// one wavefront, for sums that came out infinite or NaN: the products with both
-// parts of a weight lose an infinite value's place, since the second part may be
-// zero or negative.  Here the maximum and the sum of the weights come first, then the
-// values, each once with its share of one, in FP32, so that an infinite value
-// gives its infinity (NaN where two signs meet).  A lane has one position of 64 at
-// a time, then D / 64 components.  (Asking for it costs the others at most 0.4
-// us a call, and 1.5 of 34 where heads of 256 spill; with an infinite value in
-// every row 512 positions of one row take 160 us, 131071 1.9 ms.)
+// one wavefront, for sums that came out infinite or NaN: weights of up to 2^11,
+// and many of them, take finite values past FP32's range, and the products with
+// both parts of a weight lose an infinite value's place, since the second part
+// may be zero or negative.  Here the maximum and the sum of the weights come
+// first, then the values, each once with its share of one, in FP32, so that an
+// infinite value gives its infinity (NaN where two signs meet).  A lane has one
+// position of 64 at a time, then D / 64 components.  (Asking for it costs the
+// others at most 0.4 us a call, and 1.5 of 34 where heads of 256 spill; with an
+// infinite value in every row 512 positions of one row take 160 us, 131071 1.9
+// ms.)
 template <int D>
 __device__ void redo(const AttendArgs& a, const Segment& it, uint32_t col, uint32_t which) {
   constexpr uint32_t kPer = (D + 63) / 64;
@@ -772,7 +774,7 @@ __device__ void redo(const AttendArgs& a, const Segment& it, uint32_t col, uint3
       if (it.direct)
         a.out[row * a.ldo + static_cast<uint64_t>(h) * D + e] = static_cast<uint16_t>(pack_bf16(o[i], 0.f));
       else
-        a.part_o[(it.slot + col) * D + e] = o[i] * total;
+        a.part_o[(it.slot + col) * D + e] = o[i];
     }
     if (!it.direct && lane == 0) {
       a.part_ml[2 * (it.slot + col)] = best;
@@ -1007,7 +1009,9 @@ template <int D, int W>
 using Join = float[W][16][AttendShape<D>::kJLd];
 
 // An item of at most 16 NT columns by a workgroup of W wavefronts, which take its
-// units in turn; their sums are brought to one maximum and added in order.
+// units in turn; their sums are divided by the whole of the weights, at one
+// maximum, and then added in order, so that finite values never pass FP32's range
+// on the way.
 template <int D, int NT, int W>
 __device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment& it, LdsFixed& s, uint8_t* big) {
   constexpr int kDt = AttendShape<D>::kDt;
@@ -1031,12 +1035,19 @@ __device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment&
 #pragma unroll
   for (int w = 0; w < W; ++w) any |= s.lost[w];
   any = uniform(any);
+  auto whole = [&](uint32_t col, float& best, float& total) {  // a column's maximum and sum of the weights
+    best = s.m[0][col];
+#pragma unroll
+    for (int w = 1; w < W; ++w) best = fmaxf(best, s.m[w][col]);
+    total = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) total += s.l[w][col] * __builtin_amdgcn_exp2f((s.m[w][col] - best) * a.scale2);
+  };
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
-    float top = acc.m[c];
-#pragma unroll
-    for (int w = 0; w < W; ++w) top = fmaxf(top, s.m[w][16 * c + n]);
-    const float f = __builtin_amdgcn_exp2f((acc.m[c] - top) * a.scale2);
+    float best, total;
+    whole(16 * c + n, best, total);
+    const float f = total == 0.f ? 0.f : __builtin_amdgcn_exp2f((acc.m[c] - best) * a.scale2) / total;
     if (c) __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -1049,23 +1060,18 @@ __device__ __forceinline__ void attend_turns(const AttendArgs& a, const Segment&
       const uint32_t col = i / (D / 4), e = i % (D / 4) * 4, cc = 16 * c + col;
       if (cc >= it.cols || any >> cc & 1) continue;
       f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-      float total = 0.f, best = s.m[0][cc];
 #pragma unroll
-      for (int w = 1; w < W; ++w) best = fmaxf(best, s.m[w][cc]);
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        sum += *reinterpret_cast<const f32x4_t*>(&join[w][col][e]);
-        total += s.l[w][cc] * __builtin_amdgcn_exp2f((s.m[w][cc] - best) * a.scale2);
-      }
+      for (int w = 0; w < W; ++w) sum += *reinterpret_cast<const f32x4_t*>(&join[w][col][e]);
       if (it.direct) {
-        const float r = total == 0.f ? 0.f : 1.f / total;
         const uint32_t cl = it.col0 + cc, row = it.row0 + cl / a.ratio, h = it.head * a.ratio + cl % a.ratio;
-        const u32x2_t w = {pack_bf16(sum[0] * r, sum[1] * r), pack_bf16(sum[2] * r, sum[3] * r)};
+        const u32x2_t w = {pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
         *reinterpret_cast<u32x2_t*>(a.out + row * a.ldo + static_cast<uint64_t>(h) * D + e) = w;
         continue;
       }
       *reinterpret_cast<f32x4_t*>(a.part_o + (it.slot + cc) * D + e) = sum;
       if (e == 0) {
+        float best, total;
+        whole(cc, best, total);
         a.part_ml[2 * (it.slot + cc)] = best;
         a.part_ml[2 * (it.slot + cc) + 1] = total;
       }
@@ -1337,9 +1343,14 @@ __global__ __launch_bounds__(AttendShape<D>::kRowWaves * kWave) void k_attend_ro
     attend_turns<D, 2, kRowWaves>(a, it, s, lds);
 }
 
-// One workgroup per row and query head: the partial sums of its column, prefix
-// first.  D / 4 threads hold a column's components; the parts go round kLines
-// such lines, each keeps a running maximum, and the lines are added in order.
+// One workgroup per row and query head: the parts of its column, prefix first,
+// each the mean of its values, its maximum and the sum of its weights.  D / 4
+// threads hold a column's components; the parts go round kLines such lines, each
+// keeps a running maximum, and the lines are added in order.  Sums that come out
+// infinite or NaN are taken once more by each part's share of one, which keeps
+// means of finite values in their range and an infinity what it is, however small
+// its weight.  (A running mean from the start, a division a part: 5000 positions of
+// one row with heads of 256 18 -> 30 us.)
 template <int D>
 __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs a) {
   constexpr uint32_t kLine = D / 4, kLines = kAttendThreads / kLine;
@@ -1374,18 +1385,22 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs
     if (!shares && n1 == 1) return;  // k_attend wrote the output itself
   }
   const uint32_t line = threadIdx.x / kLine, e = threadIdx.x % kLine * 4, parts = n0 + n1;
+  auto load = [&](uint32_t i, float2& ml) {
+    const uint64_t at = i < n0 ? slot0 + static_cast<uint64_t>(i) * a.cap_p : slot1 + static_cast<uint64_t>(i - n0) * a.cap_o;
+    ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
+    return *reinterpret_cast<const f32x4_t*>(a.part_o + at * D + e);
+  };
   f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
   float best = kNoMax, total = 0.f;
   if (line < kLines) {
 #pragma unroll 4
     for (uint32_t i = line; i < parts; i += kLines) {
-      const uint64_t at = i < n0 ? slot0 + static_cast<uint64_t>(i) * a.cap_p : slot1 + static_cast<uint64_t>(i - n0) * a.cap_o;
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
-      const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part_o + at * D + e);
+      float2 ml;
+      const f32x4_t x = load(i, ml);
       const float top = fmaxf(best, ml.x);
-      const float f = __builtin_amdgcn_exp2f((best - top) * a.scale2), f2 = __builtin_amdgcn_exp2f((ml.x - top) * a.scale2);
+      const float f = __builtin_amdgcn_exp2f((best - top) * a.scale2), f2 = ml.y * __builtin_amdgcn_exp2f((ml.x - top) * a.scale2);
       sum = sum * f + x * f2;
-      total = total * f + ml.y * f2;
+      total = total * f + f2;
       best = top;
     }
     sums[line][e / 4] = sum;
@@ -1406,9 +1421,20 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs
     total += ls[i] * f;
   }
   const float f = total == 0.f ? 0.f : 1.f / total;
+  const float zero = (sum[0] * 0.f + sum[1] * 0.f) + (sum[2] * 0.f + sum[3] * 0.f);
+  sum *= f;
+  if (__builtin_expect(!(zero == 0.f), 0)) {
+    sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (uint32_t i = 0; i < parts; ++i) {
+      float2 ml;
+      const f32x4_t x = load(i, ml);
+      const float w = ml.y * __builtin_amdgcn_exp2f((ml.x - best) * a.scale2) * f;
+      for (int j = 0; j < 4; ++j) sum[j] += w == 0.f && __builtin_isinf(x[j]) ? x[j] : x[j] * w;
+    }
+  }
   uint2 w;
-  w.x = pack_bf16(sum[0] * f, sum[1] * f);
-  w.y = pack_bf16(sum[2] * f, sum[3] * f);
+  w.x = pack_bf16(sum[0], sum[1]);
+  w.y = pack_bf16(sum[2], sum[3]);
   *reinterpret_cast<uint2*>(a.out + r * a.ldo + static_cast<uint64_t>(h) * D + e) = w;
 }
 

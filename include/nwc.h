@@ -465,12 +465,14 @@ typedef struct {
  * multiple of kv_heads, at most 64 times it; at most 4096 rows, 2^22 rows *
  * q_heads and 512 groups; cols * page_len <= 2^22.
  * Softmax statistics and sums in FP32, scores and their differences of any
- * size that FP32 holds.  The weights w enter the matrix cores
- * with 16 bits (each off by at most 2^-16 of itself).  An infinity among the
- * values that a row sees is its component's result (NaN where two signs meet),
- * a NaN stays in its component; a score of +infinity or NaN makes the head's
- * output NaN, and a row whose scores are all -infinity gives zeros.  Rows with
- * results that are not finite take longer.
+ * size that FP32 holds.  The weights w enter the matrix cores with 16 bits (each
+ * off by at most 2^-16 of itself).  Finite values give finite results, up to
+ * BF16's largest.  An infinity among the values that a row sees is its
+ * component's result (NaN where two signs meet), a NaN stays in its component; a
+ * score of +infinity or NaN makes the head's output NaN, and a row whose scores
+ * are all -infinity gives zeros.  Heads with results that are not finite, or
+ * whose weighted sums pass FP32's range on the way, take longer (up to 150
+ * times).
  * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
  * nwc_attend_workspace_size bytes for these rows, q_heads and group count;
  * no initial content needed); calls that share it must not run concurrently.

@@ -119,3 +119,33 @@ def test_attend_nan_queries_stay_in_their_head(hq, hk, d, page, covers):
     _run(b)
     _check(b, "nan queries")
     assert int(b.out.isnan().sum()) == 5 * d
+
+
+@pytest.mark.parametrize("covers", [0, 4000])
+@pytest.mark.parametrize("hq,hk,d,page", SHAPES + [(20, 1, 128, 16), (32, 1, 64, 32)])
+def test_attend_values_at_the_end_of_their_range(hq, hk, d, page, covers):
+    # finite values give a finite result: up to the largest, of one sign (whose weighted sum is n times as large) and of both, with
+    # flat scores and with scores that grow along the row, so that weights stand above the running maximum; and the smallest
+    _say("large values %d %d %d %d %d" % (hq, hk, d, page, covers))
+    lengths = [640] * 9 + [75, 1, 33, 1300, 500, 5]
+    b = _Batch(lengths, hq, hk, d, page, [(0, 9, 600)], seed=hq + d, covers=covers)
+    g = torch.Generator(device="cuda").manual_seed(d)
+    most = torch.finfo(torch.bfloat16).max
+    v = torch.rand(b.vp.shape, generator=g, device="cuda").mul_(most / 2).add_(most / 2).to(torch.bfloat16)
+    v[..., 1::2] *= torch.randint(0, 2, v[..., 1::2].shape, generator=g, device="cuda").mul_(2).sub_(1).to(torch.bfloat16)
+    v[..., 4] = most
+    v[..., 6] = -most
+    v[..., 8:12] *= 2.0 ** -235                                   # 2^-108 and less
+    b.vp.copy_(v)
+    first = [x[:600] for x in _slots(b, 0)]
+    for r in range(1, 9):                                         # the prefix's values, in copied pages too
+        pages, slots = (x[:600] for x in _slots(b, r))
+        b.vp[pages, :, slots] = b.vp[first[0], :, first[1]]
+    for r in (12, 13):                                            # 10 powers of two over the row
+        pages, slots = _slots(b, r)
+        b.q[r] = 1
+        grow = torch.arange(lengths[r], device="cuda") * (10 * 0.6931 / lengths[r] / d / b.scale)
+        b.kp[pages, :, slots] = grow.to(torch.bfloat16)[:, None, None].expand(lengths[r], hk, d)
+    _run(b)
+    assert bool(b.out.isfinite().all())
+    _check(b, "large values")
