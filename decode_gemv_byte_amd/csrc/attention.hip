@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <tuple>
@@ -1457,6 +1458,23 @@ nwc_status launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipSt
              : NWC_ERR_HIP;
 }
 
+// Lets a kernel take up to MOST bytes of dynamic LDS on the current device.  What
+// is allowed belongs to the kernel, for all threads: so the most that it ever
+// takes, once, and never less for another call.
+template <auto KERNEL, size_t MOST>
+bool allow_lds() {
+  static std::atomic<uint64_t> done{0};  // a bit per device
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return false;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return true;
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize,
+                          static_cast<int>(MOST)) != hipSuccess)
+    return false;
+  done.fetch_or(bit, std::memory_order_release);
+  return true;
+}
+
 // Compute units of an MI355X.  Launches are cut for them; nothing needs them to
 // be there, so they are not asked for (two runtime calls less in a call of 4 us).
 constexpr uint32_t kCus = 256;
@@ -1593,19 +1611,16 @@ nwc_status launch_attend(AttendArgs& a, uint32_t grid, hipStream_t s) {
     constexpr int kRowWaves = AttendShape<D>::kRowWaves;
     constexpr size_t lds = std::max(sizeof(Join<D, kRowWaves>), keys_fit(D, kRowWaves) ? size_t{kRowWaves * key_slots(D)} : 0);
     static_assert(sizeof(LdsFixed) + lds <= kMaxLds, "LDS");
-    if (lds + sizeof(LdsFixed) > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend_rows<D>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds)) != hipSuccess)
-      return NWC_ERR_HIP;
+    if (lds + sizeof(LdsFixed) > 65536 && !allow_lds<k_attend_rows<D>, lds>()) return NWC_ERR_HIP;
     return launch(k_attend_rows<D>, dim3(a.pages.rows * a.hkv, (a.ratio + kWaveRatio - 1) / kWaveRatio),
                   dim3(kRowWaves * kWave), lds, s, a);
   }
   const size_t fixed = sizeof(LdsFixed) + (static_cast<size_t>(Plan::words(a.pages.rows, a.n_groups)) * 4 + 15) / 16 * 16;
   constexpr size_t big = std::max({sizeof(Join<D, 4>), size_t{AttendShape<D>::kRing * 128 * D}, keys_fit(D, 4) ? size_t{4 * key_slots(D)} : 0});
-  static_assert(sizeof(LdsFixed) + 4 * Plan::words(kAttendMaxRows, kAttendMaxGroups) + 16 + big <= kMaxLds, "LDS");
+  constexpr size_t most = sizeof(LdsFixed) + 4 * Plan::words(kAttendMaxRows, kAttendMaxGroups) + 16 + big;
+  static_assert(most <= kMaxLds, "LDS");
   const size_t lds = fixed + big;
-  if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<D>), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(lds)) != hipSuccess)
-    return NWC_ERR_HIP;
+  if (lds > 65536 && !allow_lds<k_attend<D>, most>()) return NWC_ERR_HIP;
   const nwc_status st = launch(k_attend<D>, dim3(grid), dim3(kAttendThreads), lds, s, a);
   if (st) return st;
   return launch(k_attend_join<D>, dim3(a.pages.rows * a.hq), dim3(kAttendThreads), 0, s, a);
