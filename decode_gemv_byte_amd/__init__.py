@@ -538,7 +538,8 @@ class PagedCache:
             if t.dim() != 4 or tuple(t.shape) != tuple(k_pages.shape):
                 raise ValueError("%s: expected [n_pages, kv_heads, page_len, head_dim], the same for keys and values" % name)
             _, h, n, d = t.shape
-            if (t.stride(3), t.stride(2), t.stride(1)) != (1, d, n * d):
+            # a single head has no stride of its own
+            if (t.stride(3), t.stride(2)) != (1, d) or (h > 1 and t.stride(1) != n * d):
                 raise ValueError("%s: the slots of a page must be contiguous" % name)
             if t.shape[0] > 1 and t.stride(0) != k_pages.stride(0):
                 raise ValueError("key and value pages must be the same distance apart")

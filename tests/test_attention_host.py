@@ -187,3 +187,19 @@ def test_binding_refuses_host_tensors_and_odd_layouts():
         nwc.KvAppend(cache, torch.zeros((1, 2), dtype=torch.int32), q, q, pos)
     with pytest.raises(ValueError):
         nwc.Attend(cache, torch.zeros((3, 2), dtype=torch.int32), pos, q, q, torch.zeros(8, dtype=torch.uint8))
+
+
+def test_paged_cache_takes_any_stride_of_one_head():
+    # a head's share of a joint allocation for several: the stride of a dimension of one entry means nothing
+    joint = torch.zeros((3, 4, 16, 64), dtype=torch.bfloat16)
+    cache = nwc.PagedCache(joint[:, :1], joint[:, 2:3])
+    assert (cache.struct.kv_heads, cache.struct.page_stride) == (1, 4 * 16 * 64)
+    assert cache.struct.v - cache.struct.k == 2 * 16 * 64 * 2
+    moved = joint.as_strided((3, 1, 16, 64), (4 * 16 * 64, 7, 64, 1))
+    assert nwc.PagedCache(moved, moved).struct.page_stride == 4 * 16 * 64
+    with pytest.raises(ValueError):
+        nwc.PagedCache(joint[:, ::2], joint[:, ::2])           # two heads, not side by side
+    with pytest.raises(ValueError):
+        nwc.PagedCache(joint[:, :, ::2], joint[:, :, ::2])     # every second slot
+    with pytest.raises(ValueError):
+        nwc.PagedCache(joint[..., ::2], joint[..., ::2])
