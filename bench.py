@@ -64,6 +64,7 @@ def settle(torch, stream, launch, ms=SETTLE_MS):
     of load run up to ~15% slower (gate+up of the Llama step: 42.9 us per
     launch over its first ~9 ms of launches, 36.7-36.9 us afterwards, eager
     or graph-replayed alike).  Returns the launches run."""
+    torch.cuda.synchronize()   # `stream` waits for no other: what the launches read is there
     e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     n, done, batch = 0, 0.0, 4
     while done < ms:
@@ -248,6 +249,7 @@ def model_step(args):
     res = {}
     outs = {}
     replays_match = {}
+    torch.cuda.synchronize()   # inputs and zeroed workspaces are there: `stream` does not wait for the default one
     for dense in (False, True):
         with torch.cuda.stream(stream):
             x.copy_(x0)
@@ -416,6 +418,7 @@ def model_step_paged(args):
             x.add_(buf["down"])
 
     ms, outs, match = {}, {}, {}
+    torch.cuda.synchronize()   # inputs and zeroed workspaces are there: `stream` does not wait for the default one
     for ours in (True, False):
         with torch.cuda.stream(stream):
             x.copy_(x0)
@@ -754,6 +757,7 @@ def main():
                 print("bench: %s outside tolerance %s" % (k, when), file=sys.stderr)
                 sys.exit(1)
 
+    torch.cuda.synchronize()   # inputs and zeroed workspaces are there: `stream` does not wait for the default one
     with torch.cuda.stream(stream):
         step(0)
     torch.cuda.synchronize()
@@ -963,6 +967,7 @@ def bf16_comparators(torch, nwc, args, keys, info, wbf, xs, ys, batch, bytes_u, 
     wsb = {k: zeroed(nwc.nwc_bf16_workspace_size(info[k].rows, info[k].cols)) for k in keys}
 
     def graphs_of(fn):
+        torch.cuda.synchronize()   # as before the first step
         with torch.cuda.stream(stream):
             fn(0)
         torch.cuda.synchronize()
