@@ -170,12 +170,24 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
         const bool is_q = head[u] < a.hq, is_k = !is_q && head[u] < a.hq + a.hk;
         float y[8] = {bf16_lo(xa[u][0]), bf16_hi(xa[u][0]), bf16_lo(xa[u][1]), bf16_hi(xa[u][1]),
                       bf16_lo(xb[u][0]), bf16_hi(xb[u][0]), bf16_lo(xb[u][1]), bf16_hi(xb[u][1])};
-        float sum = 0.f;
+        auto squares = [&] {
+          float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
-        sum = head_sum<G>(sum);
+          for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
+          return head_sum<G>(sum);
+        };
+        float sum = squares(), eps = a.eps;
         if (is_q ? a.q_weight != nullptr : is_k && a.k_weight != nullptr) {
-          const float r = 1.f / sqrtf(fmaf(sum, inv_d, a.eps));
+          // squares past FP32's range, or below it with no eps beside them: the
+          // head first times a power of two, which leaves its direction
+          if (__builtin_expect(!(sum < INFINITY) || (sum < 0x1p-96f && eps < 0x1p-96f), 0)) {
+            const float s = sum < 1.f ? 0x1p100f : 0x1p-70f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] *= s;
+            sum = squares();
+            eps = eps * s * s;
+          }
+          const float r = 1.f / sqrtf(fmaf(sum, inv_d, eps));
           const float g[8] = {bf16_lo(wa[u][0]), bf16_hi(wa[u][0]), bf16_lo(wa[u][1]), bf16_hi(wa[u][1]),
                               bf16_lo(wb[u][0]), bf16_hi(wb[u][0]), bf16_lo(wb[u][1]), bf16_hi(wb[u][1])};
 #pragma unroll

@@ -364,6 +364,8 @@ nwc_status nwc_read_probe(const void *buf_dev, size_t bytes, uint32_t *sink_dev,
  * aligned).  At most 65535 heads.
  * weight (device, head_dim BF16, 16-byte aligned): each head is divided by
  * the root of its mean square (+ eps) and multiplied by it; NULL: no norm.
+ * Finite heads of any size keep their direction; one of zeros gives NaN where
+ * eps is 0.
  * dst may be src itself with the same ld (each head is read before it is
  * written); any other overlap is an error the library does not see. */
 typedef struct {
