@@ -145,9 +145,9 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
       if (first) {
         first = false;
         if (pos < 0) break;  // a padding token
-        // angles in turns, reduced in FP64: position (31 bits) times frequency
-        // (24 bits) is exact to 2^-53 of its size, so after the whole turns are
-        // gone at most 2^31 / (2 pi) 2^-52, 8e-8 turns, is lost
+        // angles in turns, reduced in FP64: three roundings of 2^-53 (1 / (2 pi),
+        // and two products), so 3 2^-53 |position freq| / (2 pi) turns are lost at
+        // most: 1.1e-7 for the farthest position at a frequency of one radian
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const double turns = static_cast<double>(pos) * (static_cast<double>(freq[j]) * 0.15915494309189533577);

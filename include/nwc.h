@@ -380,9 +380,10 @@ typedef struct {
 /* Rotation by position: pair i of a head's first `dims` components turns by
  * position * freqs[i] radians (freqs: device, dims / 2 floats, 4-byte
  * aligned; the product and its reduction to one turn in FP64, so far
- * positions keep their angle).  style NWC_ROPE_HALF: pair i is (i, i + dims
- * / 2); NWC_ROPE_PAIRS: (2 i, 2 i + 1).  dims a multiple of 8, at most
- * head_dim; 0 (freqs may be NULL): no rotation. */
+ * positions keep their angle: it is off by at most 3 2^-53 of itself, its sine
+ * and cosine by 2^-17 more).  style NWC_ROPE_HALF: pair i is (i, i + dims / 2);
+ * NWC_ROPE_PAIRS: (2 i, 2 i + 1).  dims a multiple of 8, at most head_dim; 0
+ * (freqs may be NULL): no rotation. */
 typedef enum { NWC_ROPE_HALF = 0, NWC_ROPE_PAIRS = 1 } nwc_rope_style;
 typedef struct {
   const float *freqs;

@@ -4,6 +4,7 @@ Tolerances as for ordinary heads, from the roundings: the result's, 2^-8 |out|
 (BF16: half a step), and 2^-16 of the pair's two components for about ten
 roundings in FP32 and the hardware's sine and cosine, allowed 2^-17 each.
 """
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -33,3 +34,28 @@ def test_norm_of_heads_of_any_size(d, eps):
     # eps as the call takes it, an FP32 number
     ref, size = _ref_heads(x, w, pos, freqs, "half", eps=float(torch.tensor(eps, dtype=torch.float32)))
     _check_heads(out, ref, size, "heads")
+
+
+@pytest.mark.parametrize("style", ["half", "pairs"])
+def test_angles_of_frequencies_above_one(style):
+    # position * frequency to 2^31 * 1000 radians: the stated 3 2^-53 of it, in sine and cosine both, of the pair's components
+    _say("angles of frequencies above one %s" % style)
+    d = 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((300, 2, d), generator=g, device="cuda").to(torch.bfloat16)
+    freqs = torch.rand(d // 2, generator=g, device="cuda") * torch.tensor([1.0, 30.0, 1000.0, 1e-3], device="cuda").repeat(d // 8)
+    pos = torch.randint(0, 2 ** 31 - 1, (300,), generator=g, device="cuda").to(torch.int32)
+    pos[:2] = _i32([2 ** 31 - 1, 0])
+    out = torch.empty_like(x)
+    nwc.nwc_qk_norm_rope(nwc.QkNormRope(x, None, pos, q_out=out, freqs=freqs, style=style))
+    torch.cuda.synchronize()
+    # the product exactly (55 bits) and its reduction with 64 bits of 2 pi, 2^-64 of the angle
+    angle = np.outer(pos.cpu().numpy().astype(np.longdouble), freqs.cpu().numpy().astype(np.longdouble))
+    two_pi = 2 * np.longdouble("3.14159265358979323846264338327950288")
+    turn = torch.from_numpy(np.float64(angle - np.rint(angle / two_pi) * two_pi)).cuda()[:, None]
+    i, j = (slice(0, d // 2), slice(d // 2, d)) if style == "half" else (slice(0, d, 2), slice(1, d, 2))
+    a, b = x.double()[..., i], x.double()[..., j]
+    off = 3 * 2.0 ** -53 * torch.from_numpy(np.float64(angle)).cuda()[:, None]
+    for part, ref in ((i, a * turn.cos() - b * turn.sin()), (j, b * turn.cos() + a * turn.sin())):
+        tol = 2.0 ** -8 * ref.abs() + (2.0 ** -16 + off) * (a.abs() + b.abs())
+        assert bool(((out.double()[..., part] - ref).abs() <= tol).all())
