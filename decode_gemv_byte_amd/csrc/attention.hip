@@ -92,7 +92,7 @@ __device__ __forceinline__ float head_sum(float v) {
 // a lane needs 4 angles, and those serve all heads of the token. A wavefront
 // takes U passes at a time, their loads together; `split` wavefronts share a
 // token, so that few tokens still fill the GPU.
-// 16384 tokens of 32 + 8 heads of 128, 336 MB read and written: 73 us, 4.6 TB/s
+// 16384 tokens of 32 + 8 heads of 128, 336 MB read and written: 70 us, 4.8 TB/s
 // of the 4.9 that a large copy moves; one token: 2.6 us.  (With 8 neighbouring
 // components a lane, their partners by a lane permute and 8 angles: 94 and 3.7.)
 template <int G, int U>
@@ -256,14 +256,15 @@ __global__ __launch_bounds__(256) void k_heads(const HeadsArgs a) {
 //
 // What bounds it, 32 / 8 heads of 128 on one MI355X (large copies move 4.9 TB/s,
 // large reads 6.2 TB/s):
-//  * own positions: HBM.  131071 positions of one row, 537 MB: 96 us, 5.6 TB/s;
-//    the wavefronts' ranges are equal but end between 70 and 91 us.
+//  * own positions: HBM.  131071 positions of one row, 537 MB: 97 us, 5.5 TB/s;
+//    the wavefronts' ranges are equal but end some 20 us apart.
 //  * a prefix of 128 columns: a wavefront's chain of LDS reads, products, weights
-//    and products, 1.1 us a unit, and 1.4 beside own positions, behind whose
-//    loads its own wait (64 rows behind 16384 positions and up to 1024 of their
-//    own, 202 MB: 55 us).
+//    and products, 1.1 us a unit (64 rows behind 16384 and 32768 positions: 53
+//    and 87 us, 32 units a workgroup apart), and its loads wait behind those of
+//    the own positions (64 rows behind 16384 and up to 1024 of their own, 202 MB:
+//    60 us).
 //  * short calls: launch, the lengths, page numbers, keys and values one after
-//    the other (512 positions of one row: 6.2 us).
+//    the other (512 positions of one row: 6.0 us a call in a graph).
 
 constexpr uint32_t kCap = 128;        // columns of a prefix block: 4 wavefronts of 2 16-column tiles
 constexpr uint32_t kWaveRatio = 32;   // most query heads per key-value head that one wavefront takes
@@ -595,7 +596,8 @@ struct Sums {
     // bits is the output's own rounding alone, with one product 1.3 to 1.4 times
     // that.  (512 positions of one row 5.9 -> 6.2 us, 64 rows behind 16384 61 ->
     // 64, six groups of 16 49 -> 50, 32 rows behind 4096 with heads of 256 32 ->
-    // 33, long rows the same.)
+    // 33, long rows the same; where a prefix of 128 columns is all there is it
+    // shows most, 64 rows behind 16384 with one position each 48 -> 53.)
     float p[NT][8], sum[NT];
     auto weigh = [&] {
       bool grown = false;
@@ -1601,14 +1603,14 @@ nwc_status attend_shape(const nwc_cache* c, uint32_t rows, uint32_t q_heads, uin
 // Positions that a table may cover for k_attend_rows to take it, by the number of
 // its workgroups (rows times key-value heads) against the compute units.
 // Measured (32 / 8 heads of 128, us a call in a graph, k_attend_rows and k_attend
-// + k_attend_join): 1 row of 512: 6.2 and 7.7, 1024: 8.6 and 7.6; 4 rows of 1024:
-// 9.8 and 10.9, 2048: 15.1 and 12.7; 16 rows of 2048: 28.7 and 31.2, ragged to
-// 2048: 16.6 and 19.1, to 4096: 45.0 and 33.0; 64 rows of 2048: 92.9 and 97.8.
+// + k_attend_join): 1 row of 512: 6.1 and 8.1, 1024: 8.3 and 8.1; 4 rows of 1024:
+// 9.7 and 11.3, 2048: 15.0 and 12.9; 16 rows of 2048: 28.7 and 31.6, ragged to
+// 2048: 16.5 and 19.1, to 4096: 44.8 and 33.1; 64 rows of 2048: 92.5 and 98.4.
 // Heads of 256, whose keys have no room in LDS, gain less: 1 row of 256 positions
-// (8 / 4 heads) 8.8 and 10.4, of 512 13.4 and 10.3; 32 rows of 1024 38.1 and 39.9.
+// (8 / 4 heads) 9.0 and 10.8, of 512 13.4 and 10.7; 32 rows of 1024 37.6 and 40.6.
 // Rows that share a prefix read it each for itself here, from the caches, which
 // is faster while that is little: 16 rows behind 384 positions with 100 of their
-// own 7.0 and 13.5, 64 rows behind 896 19.7 and 21.9.
+// own 7.0 and 13.8, 64 rows behind 896 19.4 and 23.1.
 bool by_rows(uint32_t d, uint64_t groups, uint32_t covers, bool shared) {
   const bool many = 2 * groups >= kCus;
   if (shared) return covers <= (d == 256 ? 256 : 1024) && groups * covers * d <= 1 << 26;
