@@ -654,7 +654,8 @@ struct Sums {
   }
 
   // Which of the wavefront's columns, that count, from col on have a sum that is
-  // no finite number (0 times an infinity or a NaN is NaN): a bit each.
+  // no finite number (0 times an infinity or a NaN is NaN): a bit each.  Not those
+  // whose weights are NaN already, and every output with them.
   __device__ __forceinline__ uint32_t lost(const AttendArgs& a, const Segment& it, uint32_t col) const {
     bool bad[NT], any = false;
 #pragma unroll
@@ -670,9 +671,12 @@ struct Sums {
     uint32_t which = 0;
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
-      uint64_t lanes = __ballot(bad[c] && counts(a, it, col + 16 * c + __lane_id() % 16));
-      lanes |= lanes >> 32;
-      which |= static_cast<uint32_t>((lanes | lanes >> 16) & 0xFFFF) << (16 * c);
+      auto columns = [](uint64_t lanes) {
+        lanes |= lanes >> 32;
+        return static_cast<uint32_t>((lanes | lanes >> 16) & 0xFFFF);
+      };
+      const uint32_t here = columns(__ballot(bad[c] && counts(a, it, col + 16 * c + __lane_id() % 16)));
+      which |= (here & ~columns(__ballot(l[c] != l[c]))) << (16 * c);
     }
     return which;
   }
@@ -730,7 +734,8 @@ struct Sums {
 // position of 64 at a time, then D / 64 components.  (Asking for it costs the
 // others at most 0.4 us a call, and 1.5 of 34 where heads of 256 spill; with an
 // infinite value in every row 512 positions of one row take 160 us, 131071 1.9
-// ms.)
+// ms, 64 rows behind 16384 10 ms.  One pass for both maximum and sum, and four of
+// a position's key pieces at a time, were no faster.)
 template <int D>
 __device__ void redo(const AttendArgs& a, const Segment& it, uint32_t col, uint32_t which) {
   constexpr uint32_t kPer = (D + 63) / 64;
@@ -1438,7 +1443,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend_join(const AttendArgs
   const float f = total == 0.f ? 0.f : 1.f / total;
   const float zero = (sum[0] * 0.f + sum[1] * 0.f) + (sum[2] * 0.f + sum[3] * 0.f);
   sum *= f;
-  if (__builtin_expect(!(zero == 0.f), 0)) {
+  if (__builtin_expect(!(zero == 0.f), 0) && total == total) {
     sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
     for (uint32_t i = 0; i < parts; ++i) {
       float2 ml;

@@ -473,8 +473,8 @@ typedef struct {
  * BF16's largest.  An infinity among the values that a row sees is its
  * component's result (NaN where two signs meet), a NaN stays in its component; a
  * score of +infinity or NaN makes the head's output NaN, and a row whose scores
- * are all -infinity gives zeros.  Heads with results that are not finite, or
- * whose weighted sums pass FP32's range on the way, take longer (up to 150
+ * are all -infinity gives zeros.  Heads that see an infinite or NaN value, or
+ * whose weighted sums pass FP32's range on the way, take longer (up to 180
  * times).
  * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
  * nwc_attend_workspace_size bytes for these rows, q_heads and group count;

@@ -149,3 +149,27 @@ def test_attend_values_at_the_end_of_their_range(hq, hk, d, page, covers):
     _run(b)
     assert bool(b.out.isfinite().all())
     _check(b, "large values")
+
+
+@pytest.mark.parametrize("covers", [0, 4000])
+@pytest.mark.parametrize("hq,hk,d,page", SHAPES)
+def test_attend_nan_and_infinite_keys(hq, hk, d, page, covers):
+    # a NaN key, or an infinite one whose score is +infinity, among a row's own positions or in the prefix: NaN for the heads that
+    # see it, whatever else the row holds (an infinite value too), and for no others
+    _say("nan keys %d %d %d %d %d" % (hq, hk, d, page, covers))
+    b = _Batch([640] * 9 + [75, 33, 1, 1300], hq, hk, d, page, [(0, 9, 600)], seed=hq + d, covers=covers)
+    inf = float("inf")
+    for r, at, head, value in ((5, 620, 0, float("nan")), (9, 74, hk - 1, float("nan")), (12, 1000, 0, inf), (12, 3, hk - 1, float("nan")),
+                               (0, 100, hk // 2, float("nan"))):
+        pages, slots = _slots(b, r)
+        b.q[r, head * (hq // hk):(head + 1) * (hq // hk), 1] = 1.0
+        b.kp[pages[at], head, slots[at], 1] = value
+        b.vp[pages[at - 1], head, slots[at - 1], 2] = inf
+        if at < 600 and r < 9:                                    # the prefix, in copied pages too
+            for x in range(1, 9):
+                pages, slots = _slots(b, x)
+                b.kp[pages[at], head, slots[at], 1] = value
+                b.vp[pages[at - 1], head, slots[at - 1], 2] = inf
+    _run(b)
+    _check(b, "nan keys")
+    assert bool(b.out[0, hk // 2 * (hq // hk)].isnan().all())
