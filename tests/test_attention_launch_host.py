@@ -65,7 +65,7 @@ def test_a_smaller_call_between_allowance_and_launch(tmp_path):
     src, so = tmp_path / "shim.c", tmp_path / "shim.so"
     src.write_text(SHIM)
     subprocess.run(["gcc", "-shared", "-fPIC", "-O1", "-o", str(so), str(src)], check=True)
-    env = dict(os.environ, LD_PRELOAD=str(so))
+    env = dict(os.environ, LD_PRELOAD=":".join([str(so)] + [x for x in [os.environ.get("LD_PRELOAD")] if x]))
     r = subprocess.run([sys.executable, "-c", SCRIPT, str(so), nwc.LIB_PATH], env=env, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr
     # every call got its LDS, and calls after the first ask for nothing

@@ -59,3 +59,29 @@ def test_angles_of_frequencies_above_one(style):
     for part, ref in ((i, a * turn.cos() - b * turn.sin()), (j, b * turn.cos() + a * turn.sin())):
         tol = 2.0 ** -8 * ref.abs() + (2.0 ** -16 + off) * (a.abs() + b.abs())
         assert bool(((out.double()[..., part] - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("d", [8, 64, 72, 128, 256])
+def test_norm_of_heads_of_different_sizes_in_a_token(d, eps):
+    # heads that one wavefront takes together, some of them past the range and some not; queries and keys, with and without norm
+    _say("norm of different heads %d %g" % (d, eps))
+    g = torch.Generator(device="cuda").manual_seed(d + 1)
+    exponents = torch.tensor([0, 100, -120, 3, 64, -64, -5, 120, 1, -100, 80], device="cuda").double()
+    x = torch.randn((70, 11, d), generator=g, device="cuda").clamp(-3, 3).double()
+    turn = (torch.arange(70, device="cuda")[:, None] + torch.arange(11, device="cuda")) % 11
+    x = (x * 2.0 ** exponents[turn][..., None]).to(torch.bfloat16)
+    q, k = x[:, :7].contiguous(), x[:, 7:].contiguous()
+    w = (1 + 0.3 * torch.randn(d, generator=g, device="cuda")).to(torch.bfloat16)
+    pos, freqs = _i32(range(70)), _freqs(8)
+    for weights in ((w, w), (w, None), (None, w)):
+        q_out, k_out = torch.empty_like(q), torch.empty_like(k)
+        nwc.nwc_qk_norm_rope(nwc.QkNormRope(q, k, pos, q_out=q_out, k_out=k_out, q_weight=weights[0], k_weight=weights[1], eps=eps,
+                                            freqs=freqs))
+        torch.cuda.synchronize()
+        for name, src, out, weight in (("q", q, q_out, weights[0]), ("k", k, k_out, weights[1])):
+            ref, size = _ref_heads(src, weight, pos, freqs, "half", eps=float(torch.tensor(eps, dtype=torch.float32)))
+            # heads that are not normed reach below 2^-126, where BF16's numbers are 2^-133 apart: half of that beside the
+            # relative bounds
+            err = (out.double() - ref).abs()
+            assert bool((err <= 2.0 ** -8 * ref.abs() + 2.0 ** -16 * size + 2.0 ** -134).all()), name
