@@ -95,6 +95,14 @@ class nwc_groups(ctypes.Structure):
                 ("reserved", ctypes.c_uint32)]
 
 
+class nwc_residual(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_out", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_weight", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ld_x", ctypes.c_uint64),
+                ("ld_x_out", ctypes.c_uint64), ("ld_y", ctypes.c_uint64), ("ld_gate", ctypes.c_uint64),
+                ("ld_out", ctypes.c_uint64), ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("x_type", ctypes.c_int),
+                ("reserved", ctypes.c_uint32)]
+
+
 class NwcError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -140,11 +148,19 @@ _lib.nwc_kv_append.argtypes = [ctypes.POINTER(nwc_cache), ctypes.POINTER(nwc_pag
 _lib.nwc_attend_workspace_size.argtypes = [ctypes.POINTER(nwc_cache), _u32, _u32, _u32, ctypes.POINTER(_sz)]
 _lib.nwc_attend.argtypes = [ctypes.POINTER(nwc_cache), ctypes.POINTER(nwc_page_table), ctypes.POINTER(nwc_groups), _vp,
                             _vp, _u64, _u32, _f32, _vp, _u64, _vp, _sz, _vp]
+_lib.nwc_attend_chunk_workspace_size.argtypes = [ctypes.POINTER(nwc_cache), _u32, _u32, _u32, ctypes.POINTER(_sz)]
+_lib.nwc_attend_chunk.argtypes = [ctypes.POINTER(nwc_cache), ctypes.POINTER(nwc_page_table), _vp, _vp, _vp, _u64, _u32, _u32,
+                                  _f32, _vp, _u64, _vp, _sz, _vp]
+_lib.nwc_residual_norm.argtypes = [ctypes.POINTER(nwc_residual), _u32, _u32, _vp]
+_lib.nwc_token_logprobs_workspace_size.argtypes = [_u32, _u32, _u32, ctypes.POINTER(_sz)]
+_lib.nwc_token_logprobs.argtypes = [_vp, _u64, _i, _u32, _u32, _f32, _vp, _u32, _vp, _vp, _u32, _vp, _vp, _vp, _sz, _vp]
 for _f in ("nwc_encode_bound", "nwc_encode", "nwc_inspect", "nwc_decode", "nwc_workspace_size", "nwc_gemv",
            "nwc_gemm_skinny", "nwc_bf16_workspace_size", "nwc_gemv_bf16", "nwc_gemv_batched", "nwc_decode_batched",
            "nwc_blas_create", "nwc_blas_destroy", "nwc_prefill_workspace_size", "nwc_gemm_prefill",
            "nwc_gather_rows", "nwc_read_probe", "nwc_noalloc_scratch_bytes", "nwc_gemv_noalloc",
-           "nwc_set_wait_limit", "nwc_qk_norm_rope", "nwc_kv_append", "nwc_attend_workspace_size", "nwc_attend"):
+           "nwc_set_wait_limit", "nwc_qk_norm_rope", "nwc_kv_append", "nwc_attend_workspace_size", "nwc_attend",
+           "nwc_attend_chunk_workspace_size", "nwc_attend_chunk", "nwc_residual_norm",
+           "nwc_token_logprobs_workspace_size", "nwc_token_logprobs"):
     getattr(_lib, _f).restype = _st
 
 # the exported C symbols, for checks against include/nwc.h
@@ -153,7 +169,9 @@ EXPORTS = ("nwc_status_str", "nwc_encode_bound", "nwc_encode", "nwc_inspect", "n
            "nwc_gemv_batched", "nwc_decode_batched", "nwc_blas_create", "nwc_blas_destroy",
            "nwc_prefill_workspace_size", "nwc_gemm_prefill", "nwc_gather_rows", "nwc_read_probe",
            "nwc_noalloc_scratch_bytes", "nwc_gemv_noalloc", "nwc_set_wait_limit", "nwc_qk_norm_rope",
-           "nwc_kv_append", "nwc_attend_workspace_size", "nwc_attend")
+           "nwc_kv_append", "nwc_attend_workspace_size", "nwc_attend",
+           "nwc_attend_chunk_workspace_size", "nwc_attend_chunk", "nwc_residual_norm", "nwc_token_logprobs_workspace_size",
+           "nwc_token_logprobs")
 
 
 def _check(st: int, where: str):
@@ -652,6 +670,163 @@ class Attend(_Call):
 def nwc_attend(call: Attend, stream=None):
     """Attention of one query token per row over the paged cache (see Attend)."""
     call._run(_direct.nwc_attend, "nwc_attend", stream)
+
+
+def nwc_attend_chunk_workspace_size(cache: PagedCache, rows: int, tokens: int, q_heads: int) -> int:
+    out = _sz(0)
+    _check(_lib.nwc_attend_chunk_workspace_size(ctypes.byref(cache.struct), rows, tokens, q_heads, ctypes.byref(out)),
+           "nwc_attend_chunk_workspace_size")
+    return out.value
+
+
+class AttendChunk(_Call):
+    """Arguments of nwc_attend_chunk: new tokens query_start[r] .. query_start[r + 1]
+    - 1 (int32 [rows + 1]) of q [tokens, q_heads, head_dim] are the last ones of
+    the lengths[r] (int32 [rows]) positions of page table row r, which the cache
+    holds already; each sees its own position and those before it.  out like q;
+    a negative length leaves its row's outputs as they were; ws a device byte
+    tensor of nwc_attend_chunk_workspace_size bytes.  scale defaults to head_dim
+    ** -0.5."""
+
+    def __init__(self, cache: PagedCache, table, query_start, lengths, q, out, ws, scale: Optional[float] = None):
+        super().__init__()
+        c, t = self._cache(cache), self._table(table)
+        rows, d = int(t.rows), int(c.head_dim)
+        qp, ldq = self._rows(q, "q", None, d)
+        if tuple(out.shape) != tuple(q.shape):
+            raise ValueError("out: expected the shape of q")
+        op, ldo = self._rows(out, "out", None, d)
+        sp = self._vector(query_start, "query_start", rows + 1, torch.int32)
+        lp = self._vector(lengths, "lengths", rows, torch.int32)
+        wp = self._tensor(ws, "ws", (torch.uint8,))
+        if not ws.is_contiguous():
+            raise ValueError("ws: expected a contiguous tensor")
+        self.table = t
+        self.args = (ctypes.byref(c), ctypes.byref(t), _vp(sp), _vp(lp), _vp(qp), _u64(ldq), _u32(q.shape[0]),
+                     _u32(q.shape[1]), _f32(d ** -0.5 if scale is None else scale), _vp(op), _u64(ldo), _vp(wp),
+                     _sz(ws.numel()))
+
+
+def nwc_attend_chunk(call: AttendChunk, stream=None):
+    """Attention of a chunk of new tokens per row over the paged cache (see AttendChunk)."""
+    call._run(_direct.nwc_attend_chunk, "nwc_attend_chunk", stream)
+
+
+# ------------------------------------- the residual stream and the logits ---
+
+class ResidualNorm(_Call):
+    """Arguments of nwc_residual_norm: x [tokens, cols] (BF16 or float32), the
+    residual stream, and y [tokens, cols] BF16, a block's output or None: x_out =
+    x + scale * gate * norm(y; y_weight), out = norm(x_out; weight).  Weights BF16
+    [cols] or None (no norm); gate BF16 [cols] or [tokens, cols] or None.  x_out
+    defaults to x (in place); keep=False: the sum is not kept.  Rows may be any
+    stride apart."""
+
+    def __init__(self, x, y=None, x_out=None, out=None, weight=None, y_weight=None, gate=None, scale: float = 1.0,
+                 eps: float = 1e-6, keep: bool = True):
+        super().__init__()
+        a = nwc_residual()
+        types = (torch.float32,) if getattr(x, "dtype", None) == torch.float32 else (torch.bfloat16,)
+        a.x, a.ld_x = self._matrix(x, "x", types, None)
+        tokens, cols = int(x.shape[0]), int(x.shape[1])
+        a.x_type = NWC_OUT_F32 if x.dtype == torch.float32 else NWC_OUT_BF16
+        bf = (torch.bfloat16,)
+        if y is None and (y_weight is not None or gate is not None or x_out is not None):
+            raise ValueError("y_weight, gate and x_out go with y")
+        if (out is None) != (weight is None):
+            raise ValueError("out and weight come together")
+        if y is not None:
+            a.y, a.ld_y = self._matrix(y, "y", bf, x.shape)
+            if keep:
+                a.x_out, a.ld_x_out = self._matrix(x if x_out is None else x_out, "x_out", types, x.shape)
+            elif x_out is not None:
+                raise ValueError("x_out: the sum is not kept")
+        if y_weight is not None:
+            a.y_weight = self._vector(y_weight, "y_weight", cols, torch.bfloat16)
+        if gate is not None:
+            if getattr(gate, "dim", lambda: 0)() == 1:
+                a.gate = self._vector(gate, "gate", cols, torch.bfloat16)
+            else:
+                a.gate, a.ld_gate = self._matrix(gate, "gate", bf, x.shape)
+        if out is not None:
+            a.weight = self._vector(weight, "weight", cols, torch.bfloat16)
+            a.out, a.ld_out = self._matrix(out, "out", bf, x.shape)
+        a.scale, a.eps = float(scale), float(eps)
+        self.struct = a
+        self.args = (ctypes.byref(a), _u32(tokens), _u32(cols))
+
+    def _matrix(self, t, name: str, types, shape):
+        p = self._tensor(t, name, types, 2)
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError("%s: unexpected shape %s" % (name, tuple(t.shape)))
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError("%s: rows must be contiguous" % name)
+        # a single row has no stride of its own
+        return p, (int(t.stride(0)) if t.shape[0] > 1 else (int(t.shape[1]) + 7) // 8 * 8)
+
+
+def nwc_residual_norm(call: ResidualNorm, stream=None):
+    """The residual sum with the norms before and after a block (see ResidualNorm)."""
+    call._run(_direct.nwc_residual_norm, "nwc_residual_norm", stream)
+
+
+def nwc_token_logprobs_workspace_size(rows: int, vocab: int, k: int = 0) -> int:
+    out = _sz(0)
+    _check(_lib.nwc_token_logprobs_workspace_size(rows, vocab, k, ctypes.byref(out)), "nwc_token_logprobs_workspace_size")
+    return out.value
+
+
+class TokenLogprobs(_Call):
+    """Arguments of nwc_token_logprobs: logits [rows, vocab] (BF16 or float32, rows a
+    multiple of 16 bytes apart), ws a device byte tensor of
+    nwc_token_logprobs_workspace_size bytes; targets int32 [rows, n] with logprobs
+    float32 [rows, n] (a target outside the vocabulary leaves its logprob as it
+    was), entropy float32 [rows], top_ids int32 [rows, k] with top_logprobs float32
+    [rows, k], each or None.  scale multiplies the logits (an inverse temperature)."""
+
+    def __init__(self, logits, ws, targets=None, logprobs=None, entropy=None, top_ids=None, top_logprobs=None,
+                 scale: float = 1.0):
+        super().__init__()
+        xp = self._tensor(logits, "logits", (torch.bfloat16, torch.float32), 2)
+        rows, vocab = int(logits.shape[0]), int(logits.shape[1])
+        f32 = logits.dtype == torch.float32
+        if vocab > 1 and logits.stride(1) != 1:
+            raise ValueError("logits: rows must be contiguous")
+        ld = int(logits.stride(0)) if rows > 1 else (vocab + 7) // 8 * 8
+        if (targets is None) != (logprobs is None):
+            raise ValueError("targets and logprobs come together")
+        if (top_ids is None) != (top_logprobs is None):
+            raise ValueError("top_ids and top_logprobs come together")
+        n = k = 0
+        tp = lp = ep = ip = pp = None
+        if targets is not None:
+            n = self._columns(targets, "targets", rows, None, torch.int32)
+            self._columns(logprobs, "logprobs", rows, n, torch.float32)
+            if n:
+                tp, lp = targets.data_ptr(), logprobs.data_ptr()
+        if entropy is not None:
+            ep = self._vector(entropy, "entropy", rows, torch.float32)
+        if top_ids is not None:
+            k = self._columns(top_ids, "top_ids", rows, None, torch.int32)
+            self._columns(top_logprobs, "top_logprobs", rows, k, torch.float32)
+            if k:
+                ip, pp = top_ids.data_ptr(), top_logprobs.data_ptr()
+        wp = self._tensor(ws, "ws", (torch.uint8,))
+        if not ws.is_contiguous():
+            raise ValueError("ws: expected a contiguous tensor")
+        self.args = (_vp(xp), _u64(ld), _i(NWC_OUT_F32 if f32 else NWC_OUT_BF16), _u32(rows), _u32(vocab), _f32(scale),
+                     _vp(tp), _u32(n), _vp(lp), _vp(ep), _u32(k), _vp(ip), _vp(pp), _vp(wp), _sz(ws.numel()))
+
+    def _columns(self, t, name: str, rows: int, n: Optional[int], dtype) -> int:
+        self._tensor(t, name, (dtype,), 2)
+        if t.shape[0] != rows or (n is not None and t.shape[1] != n) or not t.is_contiguous():
+            raise ValueError("%s: expected %d contiguous rows%s" % (name, rows, "" if n is None else " of %d" % n))
+        return int(t.shape[1])
+
+
+def nwc_token_logprobs(call: TokenLogprobs, stream=None):
+    """Log probabilities of given tokens, entropy and top alternatives (see TokenLogprobs)."""
+    call._run(_direct.nwc_token_logprobs, "nwc_token_logprobs", stream)
 
 
 def info_dict(info: nwc_info) -> dict:

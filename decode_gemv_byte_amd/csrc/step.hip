@@ -1,0 +1,649 @@
+// HIP kernels of libnwc for what a step does between its blocks and behind the
+// last one, for gfx950 (CDNA4), and the C-ABI entry points that launch them:
+//
+//  * k_residual: the residual sum of a block with the norms before and after it.
+//  * k_logprobs, k_logprobs_join: log probabilities of given tokens over a row of
+//    logits, its entropy, and its k largest in order.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "device_common.hpp"
+
+namespace {
+
+// Sum over the wavefront, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+  for (int x = 32; x; x /= 2) v += lane_xor(v, x);
+  return v;
+}
+
+// -------------------------------------------------------------- k_residual ---
+
+struct ResidualArgs {
+  const void* x;
+  void* x_out;
+  const uint16_t *y, *y_weight, *gate, *weight;
+  uint16_t* out;
+  uint64_t ld_x, ld_x_out, ld_y, ld_gate, ld_out;
+  float scale, eps;
+  uint32_t tokens, cols8;  // cols / 8
+};
+
+__device__ __forceinline__ void unpack8(u32x4_t v, float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = bf16_lo(v[j]);
+    f[2 * j + 1] = bf16_hi(v[j]);
+  }
+}
+__device__ __forceinline__ u32x4_t pack8(const float (&f)[8]) {
+  return u32x4_t{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+}
+
+// A token by W wavefronts, P pieces of 8 values a lane, all of a row's values in
+// registers between its loads and its stores: each is read once, before any of
+// its lane's pieces is written.
+template <int W, int P, bool F32>
+__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void k_residual(const ResidualArgs a) {
+  constexpr int kRows = W == 1 ? 4 : 1;  // tokens that a workgroup has at a time
+  __shared__ float sums[W == 1 ? 1 : 4][W];
+  const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave);
+  const uint32_t me = W == 1 ? lane : threadIdx.x;
+  const float inv = 1.f / (8.f * static_cast<float>(a.cols8));
+  int turn = 0;  // of the LDS rows: a sum's is not written again before the next but two
+  auto total = [&](float v) {
+    v = wave_sum(v);
+    if constexpr (W > 1) {
+      float(&s)[W] = sums[turn];
+      turn = (turn + 1) % 4;
+      if (lane == 0) s[wave] = v;
+      __syncthreads();
+      v = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) v += s[i];
+    }
+    return v;
+  };
+  // 1 / sqrt(mean(f^2) + eps) for P pieces, which are multiplied by a power of two
+  // first where their squares leave FP32's range (or fall below it with no eps
+  // beside them)
+  auto rms = [&](float (&f)[P][8]) {
+    auto squares = [&] {
+      float s = 0.f;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = fmaf(f[p][j], f[p][j], s);
+      return total(s);
+    };
+    float sum = squares(), eps = a.eps;
+    if (__builtin_expect(!(sum < INFINITY) || (sum < 0x1p-96f && eps < 0x1p-96f), 0)) {
+      const float s = sum < 1.f ? 0x1p100f : 0x1p-75f;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[p][j] *= s;
+      sum = squares();
+      eps = eps * s * s;
+    }
+    return 1.f / sqrtf(fmaf(sum, inv, eps));
+  };
+  for (uint64_t t = static_cast<uint64_t>(blockIdx.x) * kRows + (W == 1 ? wave : 0); t < a.tokens;
+       t += static_cast<uint64_t>(gridDim.x) * kRows) {
+    float x[P][8];
+    u32x4_t raw[P], gates[P];
+    uint32_t at[P];
+    bool on[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      at[p] = me + p * (W * kWave);
+      on[p] = at[p] < a.cols8;
+      raw[p] = gates[p] = u32x4_t{0, 0, 0, 0};
+    }
+    if constexpr (F32) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        f32x4_t lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+        if (on[p]) {
+          const f32x4_t* src = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.x) + t * a.ld_x + 8 * at[p]);
+          lo = src[0];
+          hi = src[1];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[p][j] = lo[j];
+          x[p][4 + j] = hi[j];
+        }
+      }
+    } else {
+      u32x4_t xr[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        xr[p] = u32x4_t{0, 0, 0, 0};
+        if (on[p]) xr[p] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.x) + t * a.ld_x + 8 * at[p]);
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) unpack8(xr[p], x[p]);
+    }
+    if (a.y) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (on[p]) raw[p] = *reinterpret_cast<const u32x4_t*>(a.y + t * a.ld_y + 8 * at[p]);
+        if (on[p] && a.gate) gates[p] = *reinterpret_cast<const u32x4_t*>(a.gate + t * a.ld_gate + 8 * at[p]);
+      }
+      float u[P][8];
+#pragma unroll
+      for (int p = 0; p < P; ++p) unpack8(raw[p], u[p]);
+      if (a.y_weight) {
+        u32x4_t w[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          w[p] = u32x4_t{0, 0, 0, 0};
+          if (on[p]) w[p] = *reinterpret_cast<const u32x4_t*>(a.y_weight + 8 * at[p]);
+        }
+        const float r = rms(u);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          float g[8];
+          unpack8(w[p], g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[p][j] = u[p][j] * r * g[j];
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        float g[8];
+        unpack8(gates[p], g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[p][j] = fmaf(a.gate ? u[p][j] * g[j] : u[p][j], a.scale, x[p][j]);
+      }
+      if (a.x_out) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          if (!on[p]) continue;
+          if constexpr (F32) {
+            f32x4_t* dst = reinterpret_cast<f32x4_t*>(static_cast<float*>(a.x_out) + t * a.ld_x_out + 8 * at[p]);
+            dst[0] = f32x4_t{x[p][0], x[p][1], x[p][2], x[p][3]};
+            dst[1] = f32x4_t{x[p][4], x[p][5], x[p][6], x[p][7]};
+          } else {
+            *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.x_out) + t * a.ld_x_out + 8 * at[p]) = pack8(x[p]);
+          }
+        }
+      }
+    }
+    if (a.out) {
+      u32x4_t w[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        w[p] = u32x4_t{0, 0, 0, 0};
+        if (on[p]) w[p] = *reinterpret_cast<const u32x4_t*>(a.weight + 8 * at[p]);
+      }
+      // a lane without a piece holds zeros, also where x is infinite or NaN elsewhere
+      const float r = rms(x);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        float g[8];
+        unpack8(w[p], g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = x[p][j] * r * g[j];
+        if (on[p]) *reinterpret_cast<u32x4_t*>(a.out + t * a.ld_out + 8 * at[p]) = pack8(g);
+      }
+    }
+  }
+}
+
+// -------------------------------------------------------------- k_logprobs ---
+//
+// With c = scale log2(e) and M the row's largest logit: e_v = 2^((x_v - M) c), S =
+// sum e_v, log p_v = (x_v - M) scale - ln S and the entropy ln S - ln 2 sum e_v
+// (x_v - M) c / S, whose two terms are both positive.  One pass: every lane holds
+// S and the weighted sum relative to a maximum of its own, which moves only when a
+// logit outgrows it by 2^8, so the common piece rescales nothing.
+//
+// The k largest: each of 64 groups of lanes keeps the largest logit it saw.  The
+// k-th largest of those 64 is a bound that at least k logits reach, and only
+// lanes whose own largest reaches it look at their logits once more.  What they
+// find (little over k for logits in no order; of those equal to the bound each
+// wavefront's k lowest) is ranked by counting, each against all.  Where more is
+// found than LDS has room for, or NaN stands in the row, k rounds of a largest
+// below the last one take its place.
+
+constexpr int kLpThreads = 512, kLpWaves = kLpThreads / kWave;
+constexpr uint32_t kLpMaxK = 64, kLpMaxSplit = 64, kLpFound = 2048;
+constexpr float kLowest = -3.402823466e+38f;
+constexpr float kGrow = 8.f;     // log2 of how far a logit may outgrow its lane's maximum
+constexpr float kNoWeight = -16384.f;  // a power of two that is 0 in FP32, and finite: 0 times it is 0
+
+struct LogprobsArgs {
+  const void* logits;
+  uint64_t ld;
+  const int32_t* targets;
+  float *logprobs, *entropy, *top_logprobs;
+  int32_t* top_ids;
+  uint32_t vocab, n_targets, k;
+  uint32_t split, chunk;  // workgroups of a row, logits of each (a multiple of 8)
+  float scale, c;         // c: scale log2(e)
+  float* stats;           // workspace: {largest, S, weighted sum, 0} of each part
+  uint64_t* tops;         // k keys of each part, descending
+};
+
+// The order of logits: value, the lower index first, NaN above all, -0 as 0.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  if (x != x) return 0xFFFFFFFFu;
+  const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __builtin_bit_cast(float, o & 0x80000000u ? (o == 0xFFFFFFFFu ? 0x7FC00000u : o & 0x7FFFFFFFu) : ~o);
+}
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
+  return static_cast<uint64_t>(ordered(x)) << 32 | (0xFFFFFFFFu - index);
+}
+
+struct Stats {
+  float m, s, a;  // maximum; sum of weights relative to it; sum of weight times log2 weight
+  // relative to another maximum, no smaller
+  __device__ __forceinline__ void move(float to, float c) {
+    const float d = (m - to) * c, f = __builtin_amdgcn_exp2f(d);
+    a = f * fmaf(s, fmaxf(d, kNoWeight), a);
+    s *= f;
+    m = to;
+  }
+};
+
+// What a row's statistics come to.
+struct RowOut {
+  float m, log_s;
+  bool none;  // no weight at all: every logit -infinity
+  __device__ RowOut(const Stats& t) : m(t.m), log_s(logf(t.s)), none(t.s == 0.f) {}
+  __device__ __forceinline__ float logprob(float x, float scale) const { return none ? -INFINITY : fmaf(x - m, scale, -log_s); }
+};
+
+template <bool F32>
+__device__ __forceinline__ float logit(const LogprobsArgs& a, uint64_t row, uint32_t v) {
+  return F32 ? static_cast<const float*>(a.logits)[row * a.ld + v]
+             : __builtin_bit_cast(float, static_cast<uint32_t>(static_cast<const uint16_t*>(a.logits)[row * a.ld + v]) << 16);
+}
+
+template <bool F32>
+__device__ void store_targets(const LogprobsArgs& a, uint64_t row, const RowOut& r, uint32_t threads) {
+  for (uint32_t i = threadIdx.x; i < a.n_targets; i += threads) {
+    const uint64_t at = row * a.n_targets + i;
+    const uint32_t v = static_cast<uint32_t>(a.targets[at]);
+    if (v < a.vocab) a.logprobs[at] = r.logprob(logit<F32>(a, row, v), a.scale);
+  }
+}
+
+// Of n keys in LDS the k largest in order, each to put(rank, key): by counting.
+template <typename F>
+__device__ __forceinline__ void rank_keys(const uint64_t* keys, uint32_t n, uint32_t k, uint32_t threads, F put) {
+  for (uint32_t i = threadIdx.x; i < n; i += threads) {
+    const uint64_t x = keys[i];
+    uint32_t rank = 0;
+    for (uint32_t j = 0; j < n; ++j) rank += keys[j] > x;
+    if (rank < k) put(rank, x);
+  }
+}
+
+// Of 64 values, one a lane, the k-th largest.
+__device__ __forceinline__ float kth_of_wave(float v, uint32_t k) {
+  const uint32_t lane = __lane_id();
+  uint32_t rank = 0;
+#pragma unroll
+  for (int j = 0; j < kWave; ++j) {
+    const float y = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), j));
+    rank += y > v || (y == v && j < static_cast<int>(lane));
+  }
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v),
+                                                             __builtin_ctzll(__ballot(rank == k - 1))));
+}
+
+template <bool F32>
+__global__ __launch_bounds__(kLpThreads) void k_logprobs(const LogprobsArgs a) {
+  __shared__ float groups[kWave];
+  __shared__ Stats waves[kLpWaves];
+  __shared__ uint64_t found[kLpFound];
+  __shared__ uint32_t n_found;
+  __shared__ uint64_t best[2][kLpWaves];
+  const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave);
+  const uint64_t row = blockIdx.x / a.split;
+  const uint32_t part = blockIdx.x % a.split;
+  const uint32_t v0 = part * a.chunk, v1 = min(v0 + a.chunk, a.vocab);  // this workgroup's logits
+  const uint8_t* base = static_cast<const uint8_t*>(a.logits) + (row * a.ld + v0) * (F32 ? 4 : 2);
+  const uint32_t n = v1 - v0, pieces = (n + 7) / 8;
+  if (threadIdx.x == 0) n_found = 0;
+
+  // piece p of the part; past its end -infinity
+  auto load = [&](uint32_t p, float (&x)[8]) {
+    if (8 * p + 8 <= n) {
+      if constexpr (F32) {
+        const f32x4_t lo = reinterpret_cast<const f32x4_t*>(base)[2 * p], hi = reinterpret_cast<const f32x4_t*>(base)[2 * p + 1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[j] = lo[j];
+          x[4 + j] = hi[j];
+        }
+      } else {
+        const u32x4_t v = reinterpret_cast<const u32x4_t*>(base)[p];
+        unpack8(v, x);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = 8 * p + j < n ? logit<F32>(a, row, v0 + 8 * p + j) : -INFINITY;
+    }
+  };
+
+  Stats t = {kLowest, 0.f, 0.f};
+  float most = -INFINITY;  // the lane's largest
+  for (uint32_t p = threadIdx.x; p < pieces; p += kLpThreads) {
+    float x[8];
+    load(p, x);
+    const float pm = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    most = fmaxf(most, pm);
+    if (__any((pm - t.m) * a.c > kGrow)) t.move(fmaxf(t.m, pm), a.c);
+    float s = 0.f, w = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d = (x[j] - t.m) * a.c, e = __builtin_amdgcn_exp2f(d);
+      s += e;
+      w = fmaf(e, fmaxf(d, kNoWeight), w);
+    }
+    t.s += s;
+    t.a += w;
+  }
+  // the workgroup's statistics, relative to its largest logit
+  {
+    float m = fmaxf(most, kLowest), g = most;
+    for (int x = 32; x; x /= 2) {
+      m = fmaxf(m, lane_xor(m, x));
+      if (x < 8) g = fmaxf(g, lane_xor(g, x));
+    }
+    if (lane % 8 == 0) groups[wave * 8 + lane / 8] = g;
+    t.move(m, a.c);
+    t.s = wave_sum(t.s);
+    t.a = wave_sum(t.a);
+    if (lane == 0) waves[wave] = t;
+  }
+  __syncthreads();
+  float m = kLowest;
+#pragma unroll
+  for (int w = 0; w < kLpWaves; ++w) m = fmaxf(m, waves[w].m);
+  t = Stats{m, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < kLpWaves; ++w) {
+    Stats x = waves[w];
+    x.move(m, a.c);
+    t.s += x.s;
+    t.a += x.a;
+  }
+  const RowOut out(t);
+  const bool whole = a.split == 1;
+  if (whole) {
+    store_targets<F32>(a, row, out, kLpThreads);
+    if (threadIdx.x == 0 && a.entropy) a.entropy[row] = out.none ? 0.f : fmaf(-0.69314718055994530942f, t.a / t.s, out.log_s);
+  } else if (threadIdx.x == 0) {
+    float* st = a.stats + 4 * static_cast<uint64_t>(blockIdx.x);
+    st[0] = t.m;
+    st[1] = t.s;
+    st[2] = t.a;
+  }
+  const uint32_t k = a.k;
+  if (k == 0) return;
+  auto put = [&](uint32_t rank, uint64_t key) {
+    if (whole) {
+      a.top_ids[row * k + rank] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+      a.top_logprobs[row * k + rank] = out.logprob(value_of(static_cast<uint32_t>(key >> 32)), a.scale);
+    } else {
+      a.tops[static_cast<uint64_t>(blockIdx.x) * k + rank] = key;
+    }
+  };
+  const bool odd = !(t.s < INFINITY);  // NaN or +infinity among them
+  if (!odd) {
+    const float bound = kth_of_wave(groups[lane], k);
+    const bool mine = most >= bound;
+    uint32_t equal = 0;  // of the wavefront so far
+    if (__any(mine))
+      for (uint32_t p0 = wave * kWave; p0 < pieces; p0 += kLpThreads) {
+        const uint32_t p = p0 + lane;
+        float x[8];
+        uint32_t above = 0, same = 0;
+        if (mine && p < pieces) {
+          load(p, x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const bool here = 8 * p + j < n;
+            above |= (here && x[j] > bound) << j;
+            same |= (here && x[j] == bound) << j;
+          }
+        }
+        if (!__any(above | same)) continue;
+        // of the equal ones those that are among the wavefront's k lowest
+        const uint32_t count = __popc(same);
+        uint32_t upto = count;
+        for (int d = 1; d < kWave; d *= 2) {
+          const uint32_t y = __shfl_up(upto, d, kWave);
+          if (static_cast<int>(lane) >= d) upto += y;
+        }
+        uint32_t before = equal + upto - count;
+        equal += __shfl(upto, kWave - 1, kWave);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool eq = same >> j & 1;
+          if ((above >> j & 1) || (eq && before < k)) {
+            const uint32_t i = atomicAdd(&n_found, 1u);
+            if (i < kLpFound) found[i] = key_of(x[j], v0 + 8 * p + j);
+          }
+          before += eq;
+        }
+      }
+    __syncthreads();
+    if (n_found <= kLpFound) {
+      rank_keys(found, n_found, k, kLpThreads, put);
+      // a last part with fewer logits than k
+      for (uint32_t r = n_found + threadIdx.x; r < k; r += kLpThreads) put(r, 0);
+      return;
+    }
+  }
+  uint64_t last = ~uint64_t{0};
+  for (uint32_t r = 0; r < k; ++r) {
+    uint64_t top = 0;
+    for (uint32_t p = threadIdx.x; p < pieces; p += kLpThreads) {
+      float x[8];
+      load(p, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint64_t key = 8 * p + j < n ? key_of(x[j], v0 + 8 * p + j) : 0;
+        if (key < last && key > top) top = key;
+      }
+    }
+    for (int x = 32; x; x /= 2) {
+      const uint64_t y = __shfl_xor(top, x, kWave);
+      top = y > top ? y : top;
+    }
+    if (lane == 0) best[r % 2][wave] = top;
+    __syncthreads();
+    top = 0;
+    for (int w = 0; w < kLpWaves; ++w) top = best[r % 2][w] > top ? best[r % 2][w] : top;
+    if (threadIdx.x == 0) put(r, top);
+    last = top;
+  }
+}
+
+// The parts of a row, a workgroup each.  The first few of every part's sorted
+// keys, 64 or more together, give the bound.
+template <bool F32>
+__global__ __launch_bounds__(256) void k_logprobs_join(const LogprobsArgs a) {
+  __shared__ uint64_t heads[2 * kWave];
+  __shared__ uint64_t found[kLpMaxSplit * kLpMaxK];
+  __shared__ uint64_t bound;
+  __shared__ uint32_t n_found;
+  const uint64_t row = blockIdx.x;
+  const float* st = a.stats + 4 * row * a.split;
+  if (threadIdx.x == 0) {
+    n_found = 0;
+    bound = 0;
+  }
+  Stats t = {kLowest, 0.f, 0.f};
+  for (uint32_t i = 0; i < a.split; ++i) t.m = fmaxf(t.m, st[4 * i]);
+  for (uint32_t i = 0; i < a.split; ++i) {
+    Stats x = {st[4 * i], st[4 * i + 1], st[4 * i + 2]};
+    x.move(t.m, a.c);
+    t.s += x.s;
+    t.a += x.a;
+  }
+  const RowOut out(t);
+  store_targets<F32>(a, row, out, blockDim.x);
+  if (threadIdx.x == 0 && a.entropy) a.entropy[row] = out.none ? 0.f : fmaf(-0.69314718055994530942f, t.a / t.s, out.log_s);
+  const uint32_t k = a.k;
+  if (k == 0) return;
+  const uint64_t* keys = a.tops + row * a.split * k;
+  const uint32_t each = min(k, (kWave + a.split - 1) / a.split), n_heads = each * a.split;  // at most 64 + split - 1
+  for (uint32_t i = threadIdx.x; i < n_heads; i += blockDim.x) heads[i] = keys[i / each * k + i % each];
+  __syncthreads();
+  // fewer heads than k: no bound
+  for (uint32_t i = threadIdx.x; i < n_heads; i += blockDim.x) {
+    uint32_t rank = 0;
+    for (uint32_t j = 0; j < n_heads; ++j) rank += heads[j] > heads[i] || (heads[j] == heads[i] && j < i);
+    if (rank == k - 1) bound = heads[i];
+  }
+  __syncthreads();
+  const uint64_t least = max(bound, uint64_t{1});  // a key of 0 is none
+  for (uint32_t i = threadIdx.x; i < a.split * k; i += blockDim.x) {
+    const uint64_t key = keys[i];
+    if (key >= least) found[atomicAdd(&n_found, 1u)] = key;
+  }
+  __syncthreads();
+  rank_keys(found, n_found, k, blockDim.x, [&](uint32_t rank, uint64_t key) {
+    a.top_ids[row * k + rank] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+    a.top_logprobs[row * k + rank] = out.logprob(value_of(static_cast<uint32_t>(key >> 32)), a.scale);
+  });
+}
+
+// ------------------------------------------------------------------- host ---
+
+constexpr uint32_t kMaxCols = 32768;  // 16 wavefronts of 4 pieces a lane
+
+template <bool F32>
+nwc_status launch_residual(const ResidualArgs& a, hipStream_t s) {
+  // as few wavefronts a token as hold it in 8 pieces a lane where tokens fill the
+  // GPU, else as many as have a piece for each lane
+  const bool many = a.tokens >= 4 * kCus;
+  const uint32_t wide = many ? 8 : 1;
+  const uint32_t w = a.cols8 <= 64 * wide ? 1 : a.cols8 <= 256 * wide ? 4 : 16;
+  const uint32_t p = (a.cols8 + 64 * w - 1) / (64 * w);
+  auto go = [&](auto waves) {
+    constexpr int W = decltype(waves)::value;
+    const uint64_t groups = (static_cast<uint64_t>(a.tokens) + (W == 1 ? 3 : 0)) / (W == 1 ? 4 : 1);
+    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(groups, 1u << 20))), block(W == 1 ? 256 : W * 64);
+    if (p == 1) return launch(k_residual<W, 1, F32>, grid, block, 0, s, a);
+    if (p == 2) return launch(k_residual<W, 2, F32>, grid, block, 0, s, a);
+    if constexpr (W < 16)
+      if (p > 4) return launch(k_residual<W, 8, F32>, grid, block, 0, s, a);
+    return launch(k_residual<W, 4, F32>, grid, block, 0, s, a);
+  };
+  if (w == 1) return go(std::integral_constant<int, 1>{});
+  if (w == 4) return go(std::integral_constant<int, 4>{});
+  return go(std::integral_constant<int, 16>{});
+}
+
+struct LogprobsLayout {
+  uint32_t split, chunk;
+  uint64_t tops, bytes;
+};
+LogprobsLayout logprobs_layout(uint32_t rows, uint32_t vocab, uint32_t k) {
+  LogprobsLayout L;
+  // two workgroups a compute unit, of 4096 logits at least
+  const uint32_t want = std::min<uint32_t>({(2 * kCus + rows - 1) / rows, (vocab + 4095) / 4096, kLpMaxSplit});
+  L.chunk = ((vocab + want - 1) / want + 7) / 8 * 8;
+  L.split = (vocab + L.chunk - 1) / L.chunk;
+  auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
+  const uint64_t parts = L.split == 1 ? 0 : static_cast<uint64_t>(rows) * L.split;
+  L.tops = up(parts * 16);
+  L.bytes = std::max<uint64_t>(256, L.tops + up(parts * k * 8));
+  return L;
+}
+
+nwc_status logprobs_shape(uint32_t rows, uint32_t vocab, uint32_t k) {
+  if (rows == 0 || vocab == 0 || k > vocab) return NWC_ERR_INVALID_ARG;
+  if (k > kLpMaxK || vocab > 0x7FFFFFFF || rows > 1u << 22) return NWC_ERR_UNSUPPORTED;
+  return NWC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+nwc_status nwc_residual_norm(const nwc_residual* r, uint32_t tokens, uint32_t cols, void* stream) {
+  if (!r || tokens == 0 || cols == 0 || r->reserved || !r->x || !std::isfinite(r->scale) || !(r->eps >= 0.f) ||
+      !std::isfinite(r->eps) || (r->x_type != NWC_OUT_BF16 && r->x_type != NWC_OUT_F32))
+    return NWC_ERR_INVALID_ARG;
+  if ((!r->out && !r->x_out) || !r->out != !r->weight || (!r->y && (r->x_out || r->y_weight || r->gate))) return NWC_ERR_INVALID_ARG;
+  if (cols % 8 || cols > kMaxCols) return NWC_ERR_UNSUPPORTED;
+  const bool f32 = r->x_type == NWC_OUT_F32;
+  auto bad_ld = [&](const void* p, uint64_t ld) { return p && (ld < cols || ld > kMaxStride); };
+  if (bad_ld(r->x, r->ld_x) || bad_ld(r->x_out, r->ld_x_out) || bad_ld(r->y, r->ld_y) || bad_ld(r->out, r->ld_out) ||
+      (r->ld_gate && bad_ld(r->gate, r->ld_gate)))
+    return NWC_ERR_INVALID_ARG;
+  for (const void* p : {r->x, static_cast<const void*>(r->x_out), static_cast<const void*>(r->y), static_cast<const void*>(r->y_weight),
+                        static_cast<const void*>(r->gate), static_cast<const void*>(r->weight), static_cast<const void*>(r->out)})
+    if (!aligned(p, 16)) return NWC_ERR_ALIGNMENT;
+  if (r->ld_x % 8 || (r->x_out && r->ld_x_out % 8) || (r->y && r->ld_y % 8) || (r->gate && r->ld_gate % 8) ||
+      (r->out && r->ld_out % 8))
+    return NWC_ERR_ALIGNMENT;
+  // what may be one buffer: the sum and x, the normed and y, or x of its type that no sum goes to
+  if (r->x_out == r->x && r->ld_x_out != r->ld_x) return NWC_ERR_INVALID_ARG;
+  if (r->out) {
+    const void* o = r->out;
+    if (o == r->x_out || o == r->gate || o == r->weight || o == r->y_weight || (o == r->y && r->ld_out != r->ld_y) ||
+        (o == r->x && (f32 || r->ld_out != r->ld_x)))
+      return NWC_ERR_INVALID_ARG;
+  }
+  if (r->x_out && (r->x_out == r->y || r->x_out == r->gate || r->x_out == r->weight || r->x_out == r->y_weight))
+    return NWC_ERR_INVALID_ARG;
+  const ResidualArgs a = {r->x, r->x_out, r->y, r->y_weight, r->gate, r->weight, r->out, r->ld_x, r->ld_x_out, r->ld_y,
+                          r->ld_gate, r->ld_out, r->scale, r->eps, tokens, cols / 8};
+  return f32 ? launch_residual<true>(a, static_cast<hipStream_t>(stream)) : launch_residual<false>(a, static_cast<hipStream_t>(stream));
+}
+
+nwc_status nwc_token_logprobs_workspace_size(uint32_t rows, uint32_t vocab, uint32_t k, size_t* bytes) {
+  if (!bytes) return NWC_ERR_INVALID_ARG;
+  const nwc_status st = logprobs_shape(rows, vocab, k);
+  if (st) return st;
+  *bytes = logprobs_layout(rows, vocab, k).bytes;
+  return NWC_OK;
+}
+
+nwc_status nwc_token_logprobs(const void* logits_dev, uint64_t ld, nwc_out_type type, uint32_t rows, uint32_t vocab, float scale,
+                              const int32_t* targets_dev, uint32_t n_targets, float* logprobs_dev, float* entropy_dev, uint32_t k,
+                              int32_t* top_ids_dev, float* top_logprobs_dev, void* ws, size_t ws_bytes, void* stream) {
+  if (!logits_dev || !ws || !(scale > 0.f) || !std::isfinite(scale * kLog2e) || (type != NWC_OUT_BF16 && type != NWC_OUT_F32))
+    return NWC_ERR_INVALID_ARG;
+  if (!targets_dev != !logprobs_dev || !targets_dev != !n_targets || !top_ids_dev != !top_logprobs_dev || !top_ids_dev != !k ||
+      (!n_targets && !entropy_dev && !k))
+    return NWC_ERR_INVALID_ARG;
+  const nwc_status st = logprobs_shape(rows, vocab, k);
+  if (st) return st;
+  if (n_targets > 65536) return NWC_ERR_UNSUPPORTED;
+  if (ld < vocab || ld > kMaxStride) return NWC_ERR_INVALID_ARG;
+  if (!aligned(logits_dev, 16) || ld % (type == NWC_OUT_F32 ? 4 : 8) || !aligned(targets_dev, 4) || !aligned(logprobs_dev, 4) ||
+      !aligned(entropy_dev, 4) || !aligned(top_ids_dev, 4) || !aligned(top_logprobs_dev, 4) || !aligned(ws, 256))
+    return NWC_ERR_ALIGNMENT;
+  const LogprobsLayout L = logprobs_layout(rows, vocab, k);
+  if (ws_bytes < L.bytes) return NWC_ERR_BUFFER_TOO_SMALL;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const LogprobsArgs a = {logits_dev, ld, targets_dev, logprobs_dev, entropy_dev, top_logprobs_dev, top_ids_dev, vocab,
+                          n_targets, k, L.split, L.chunk, scale, scale * kLog2e, reinterpret_cast<float*>(w),
+                          reinterpret_cast<uint64_t*>(w + L.tops)};
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const dim3 grid(rows * L.split), block(kLpThreads);
+  const nwc_status first = type == NWC_OUT_F32 ? launch(k_logprobs<true>, grid, block, 0, s, a) : launch(k_logprobs<false>, grid, block, 0, s, a);
+  if (first || L.split == 1) return first;
+  return type == NWC_OUT_F32 ? launch(k_logprobs_join<true>, dim3(rows), dim3(256), 0, s, a)
+                             : launch(k_logprobs_join<false>, dim3(rows), dim3(256), 0, s, a);
+}
+
+}  // extern "C"

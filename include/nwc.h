@@ -488,6 +488,100 @@ nwc_status nwc_attend(const nwc_cache *cache, const nwc_page_table *table, const
                       float scale, uint16_t *out_dev, uint64_t ldo, void *ws, size_t ws_bytes,
                       void *stream);
 
+/* Attention of a chunk of new tokens per row over the paged cache, which holds
+ * their keys and values already (nwc_kv_append): row r of the table has
+ * lengths_dev[r] positions (device, int32), of which the last n are those of the
+ * tokens t = query_start_dev[r] .. query_start_dev[r + 1] - 1 of q (device, rows +
+ * 1 int32, ascending, within 0..tokens), n = their number.  The token of position
+ * P sees positions p <= P: out[t, h] = sum_p w_p v[p], w = softmax_p(scale
+ * q[t, h] . k[p]), key-value head h / (q_heads / kv_heads).  Rows may have any
+ * number of tokens, none too, prompts and single generated tokens side by side.
+ * q_dev and out_dev [tokens, q_heads, head_dim], tokens ldq / ldo elements apart
+ * (multiples of 8, 16-byte aligned), the two apart in memory (the same pointer is
+ * refused).
+ * A negative length marks a padding row, whose tokens' outputs are left as they
+ * were, as are those of tokens that no row names.  Where a row has more tokens
+ * than positions its first tokens see nothing and give zeros; a length past the
+ * table's cols * page_len is cut to it.  A row whose start descends has no
+ * tokens; a token that two rows name has either's result.  Positions on pages
+ * that do not exist are not seen.
+ * scale finite and > 0.  head_dim 64, 96, 128, 192 or 256; q_heads a multiple of
+ * kv_heads, at most 64 times it; at most 4096 rows, 2^22 tokens; cols * page_len
+ * <= 2^22.
+ * Softmax statistics and sums in FP32, scores and their differences of any size
+ * that FP32 holds.  The weights w enter the matrix cores as BF16, rounded to
+ * nearest (each off by at most 2^-8 of itself, half a step).  Infinities, NaN and values whose weighted
+ * sums pass FP32's range as in nwc_attend; what a token does not see (later
+ * positions, slots past a length) may hold anything.  A head whose sums meet an
+ * infinity or a NaN on the way, seen or not, takes longer: it is computed once
+ * more, by itself.
+ * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
+ * nwc_attend_chunk_workspace_size bytes; no initial content needed); calls that
+ * share it must not run concurrently.  Async.
+ * Errors: INVALID_ARG, BUFFER_TOO_SMALL (ws), ALIGNMENT, UNSUPPORTED, HIP. */
+nwc_status nwc_attend_chunk_workspace_size(const nwc_cache *cache, uint32_t rows, uint32_t tokens,
+                                           uint32_t q_heads, size_t *bytes);
+nwc_status nwc_attend_chunk(const nwc_cache *cache, const nwc_page_table *table,
+                            const int32_t *query_start_dev, const int32_t *lengths_dev,
+                            const uint16_t *q_dev, uint64_t ldq, uint32_t tokens, uint32_t q_heads,
+                            float scale, uint16_t *out_dev, uint64_t ldo, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/* ------------------------------------- the residual stream and the logits --- */
+
+/* The residual stream between two blocks, one pass: for each token
+ *   u  = y, or with y_weight y / sqrt(mean(y^2) + eps) * y_weight   (norm after a block)
+ *   x' = x + scale * gate * u                                       (x_out)
+ *   out = x' / sqrt(mean(x'^2) + eps) * weight                      (norm before the next)
+ * x and x_out [tokens, cols] BF16 or FP32 (x_type), y, gate and out BF16, rows
+ * ld_* elements apart (multiples of 8, at least cols; pointers 16-byte aligned).
+ * y NULL: x' = x (y_weight, gate and x_out NULL).  gate NULL: ones; ld_gate 0: one
+ * row of it for all tokens.  out NULL (and weight NULL): no norm behind the sum.
+ * x_out and out not both NULL; x_out NULL: the sum is not kept.  Arithmetic in
+ * FP32, one rounding per output value: out comes from x' before its rounding.
+ * Finite rows of any size keep their direction in a norm; one of zeros gives NaN
+ * where eps is 0.  x_out may be x itself with the same stride, and out may be y or
+ * (BF16) x where x_out is not; any other overlap is an error the library does not
+ * see.  cols a multiple of 8, 8..32768.  scale finite.  Async.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (cols), HIP. */
+typedef struct {
+  const void *x;
+  void *x_out;
+  const uint16_t *y, *y_weight, *gate, *weight;
+  uint16_t *out;
+  uint64_t ld_x, ld_x_out, ld_y, ld_gate, ld_out;
+  float scale, eps;
+  nwc_out_type x_type;
+  uint32_t reserved;               /* 0 */
+} nwc_residual;
+nwc_status nwc_residual_norm(const nwc_residual *args, uint32_t tokens, uint32_t cols, void *stream);
+
+/* Log probabilities of given tokens, with entropy and the most likely tokens:
+ * for each row of logits [rows, vocab] (BF16 or FP32, rows ld elements apart, ld
+ * a multiple of 16 bytes), p = softmax(scale * logits):
+ *   logprobs[r, i] = log p[targets[r, i]]       targets int32 [rows, n_targets]
+ *   entropy[r]     = -sum_v p_v log p_v
+ *   top_ids[r, j], top_logprobs[r, j]           the k largest, j = 0 .. k - 1,
+ *                                               in order; of equal logits the lower index first
+ * all outputs FP32 or int32, contiguous, 4-byte aligned.  targets and logprobs
+ * come together (NULL with n_targets 0), top_ids and top_logprobs too (NULL with k
+ * 0); entropy may be NULL; something has to be asked for.  A target outside
+ * 0..vocab-1 names no token: its logprob is left as it was.  k at most 64 and at
+ * most vocab; n_targets at most 65536; scale finite and > 0.
+ * Statistics in FP32.  A logit of -infinity is a token of probability zero (log
+ * probability -infinity, nothing to the entropy); a row of nothing else has
+ * entropy 0.  +infinity or NaN among a row's logits make all its log probabilities
+ * and its entropy NaN; in the order a NaN stands above +infinity.
+ * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
+ * nwc_token_logprobs_workspace_size bytes; no initial content needed); calls that
+ * share it must not run concurrently.  Async.
+ * Errors: INVALID_ARG, BUFFER_TOO_SMALL (ws), ALIGNMENT, UNSUPPORTED, HIP. */
+nwc_status nwc_token_logprobs_workspace_size(uint32_t rows, uint32_t vocab, uint32_t k, size_t *bytes);
+nwc_status nwc_token_logprobs(const void *logits_dev, uint64_t ld, nwc_out_type type, uint32_t rows,
+                              uint32_t vocab, float scale, const int32_t *targets_dev, uint32_t n_targets,
+                              float *logprobs_dev, float *entropy_dev, uint32_t k, int32_t *top_ids_dev,
+                              float *top_logprobs_dev, void *ws, size_t ws_bytes, void *stream);
+
 /* Test hook for the bounded waits of nwc_gemm_skinny's matrix-core kernel
  * (batch >= 5, 8-row tiles), whose decoding and matrix-core wavefronts wait
  * for each other through flags in LDS.  Every such wait gives up after
