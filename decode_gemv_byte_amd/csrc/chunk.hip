@@ -38,13 +38,22 @@ typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 // both kinds touch all banks evenly.
 
 constexpr int kChunkThreads = 256;
-constexpr uint32_t kCols = 128, kWaveCols = 32, kUnit = 64;
+constexpr uint32_t kMaxWorkers = 4 * kCus;
+constexpr uint32_t kLeast = 64;     // positions of a worker's range at least
+constexpr uint32_t kItemCost = 256;  // what an item's begin and end take, in positions
 constexpr float kNoMax = -3.402823466e+38f;  // the maximum of nothing: finite, so that exp2(-inf - it) is 0
 constexpr float kFinite = 3.0e38f;
 // Scaled maxima up to which a weight's exponent, score * scale - maximum * scale
 // with the second product rounded, is off by a common 2^5 at most; beyond, a column
 // is computed by itself.
 constexpr float kFarMax = 0x1p29f;
+
+// An item that goes on behind the range of the worker that began it, in the ranges
+// of `more` others (0: there is none): its key-value head, table row, first token and
+// what that one sees, and its columns.
+struct Cut {
+  uint32_t more, head, cols, token, sees, row, worker, unused;
+};
 
 struct ChunkArgs {
   const uint16_t *k, *v, *q;
@@ -59,6 +68,7 @@ struct ChunkArgs {
   float scale, scale2;  // scale * log2(e)
   float* part_o;     // workspace: means over a part of a column's positions [part][column][D]
   float* part_ml;    // their scaled maxima and weight sums
+  Cut* cuts;         // one for each worker
 };
 
 // A row's tokens that see something: n tokens from token t0 of q on, the first of
@@ -79,14 +89,14 @@ struct RowPart {
     base = end - n;
   }
   __device__ uint32_t blocks(uint32_t tb) const { return (n + tb - 1) / tb; }
-  // positions that block b sees, and those of all blocks before it
+  // positions that block b sees, and what all blocks before it take
   __device__ uint32_t sees(uint32_t b, uint32_t tb) const { return base + min(n, (b + 1) * tb); }
   __device__ uint64_t before(uint32_t b, uint32_t tb) const {
-    return static_cast<uint64_t>(b) * base + static_cast<uint64_t>(tb) * (static_cast<uint64_t>(b) * (b + 1) / 2);
+    return static_cast<uint64_t>(b) * (base + kItemCost) + static_cast<uint64_t>(tb) * (static_cast<uint64_t>(b) * (b + 1) / 2);
   }
   __device__ uint64_t all(uint32_t tb) const {
     const uint32_t nb = blocks(tb);
-    return nb ? before(nb - 1, tb) + sees(nb - 1, tb) : 0;
+    return nb ? before(nb - 1, tb) + sees(nb - 1, tb) + kItemCost : 0;
   }
 };
 
@@ -94,10 +104,9 @@ struct RowPart {
 struct Item {
   uint64_t at;  // its first position in the stretch
   uint32_t head, row, block;
-  uint32_t units(uint32_t sees) const;
 };
 
-// The positions of all rows before each row, in LDS: pre[rows + 1].
+// The positions of all rows before each row, in LDS: pre[rows + 1]; carry: 4 more.
 __device__ __forceinline__ void make_prefix(const ChunkArgs& a, uint64_t* pre, uint64_t* carry) {
   const uint32_t rows = a.pages.rows, tid = threadIdx.x, lane = __lane_id(), wave = uniform(tid / kWave);
   uint64_t sum = 0;
@@ -113,7 +122,12 @@ __device__ __forceinline__ void make_prefix(const ChunkArgs& a, uint64_t* pre, u
       const uint32_t end = len < 0 ? 0 : min(static_cast<uint32_t>(len), a.pages.cols << a.pages.shift);
       const uint32_t n = min(all, end), b = end - n, nb = (n + a.tb - 1) / a.tb;
       if (nb)
-        x = static_cast<uint64_t>(nb - 1) * b + static_cast<uint64_t>(a.tb) * (static_cast<uint64_t>(nb - 1) * nb / 2) + b + n;
+        x = static_cast<uint64_t>(nb - 1) * (b + kItemCost) + static_cast<uint64_t>(a.tb) * (static_cast<uint64_t>(nb - 1) * nb / 2) + b + n + kItemCost;
+    }
+    if (rows == 1) {
+      if (tid == 0) pre[1] = x;
+      __syncthreads();
+      return;
     }
     for (int d = 1; d < kWave; d *= 2) {
       const uint64_t y = __shfl_up(x, d, kWave);
@@ -134,9 +148,9 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
   return static_cast<uint64_t>(uniform(static_cast<uint32_t>(v >> 32))) << 32 | uniform(static_cast<uint32_t>(v));
 }
 
-// Positions per worker: equal ranges, of at least two units.
+// Positions per worker: equal ranges.
 __device__ __forceinline__ uint64_t quota_of(const ChunkArgs& a, uint64_t total) {
-  return max((total + a.workers - 1) / a.workers, uint64_t{2 * kUnit});
+  return max((total + a.workers - 1) / a.workers, uint64_t{kLeast});
 }
 
 // The item that position x < hkv * pre[rows] of the stretch belongs to.
@@ -242,202 +256,286 @@ template <int D>
 struct ChunkShape {
   static constexpr int kKs = D / 16;   // steps of the K Q^T product
   static constexpr int kDt = D / 32;   // 32-row tiles of O^T
-  static constexpr uint32_t kTile = kUnit * D * 2;  // bytes of a unit's keys or values
-  static constexpr uint32_t kLds = 4 * kTile;       // two units
-  static constexpr int kWgs = D <= 128 ? 2 : 1;     // workgroups of a compute unit
+  static constexpr int kNt = 1;            // 32-column tiles of a wavefront
+  static constexpr uint32_t kUnit = D <= 128 ? 64 : 32;   // positions of a unit
+  static constexpr int kKt = kUnit / 32;                  // 32-position tiles of it
+  static constexpr uint32_t kCols = 4 * 32 * kNt;         // columns of an item
+  static constexpr uint32_t kTile = kUnit * D * 2;        // bytes of a unit's keys or values
+  static constexpr int kRing = D <= 64 ? 3 : D <= 128 ? 2 : D <= 192 ? 3 : 4;                         // units of each in LDS
+  static constexpr uint32_t kLds = 2 * kRing * kTile;
+  static constexpr int kWgs = D <= 96 ? 3 : D <= 192 ? 2 : 1;           // workgroups of a compute unit
+  static constexpr int kRows = kUnit / 4;                 // rows of a tile that a wavefront loads
+  static constexpr int kLoads = kRows * D * 2 / 1024;     // and its loads for them
 };
+
+// 16 bytes a lane from base + off (bytes) to 1024 bytes of LDS.  In assembly, since
+// the compiler lets every transposing LDS read wait for all of them; nothing is
+// returned to registers, and wait_vmem counts them.
+__device__ __forceinline__ void load_lds(const void* base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
+}
 
 template <int D>
 __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, const RowPart& p, uint32_t u0, uint32_t u1, uint32_t part,
-                         uint8_t* lds) {
+                                         uint8_t* lds) {
   using S = ChunkShape<D>;
-  constexpr uint32_t kPieces = D / 8;
-  constexpr int kLoads = D / 32;  // of a wavefront's 16 rows
+  constexpr uint32_t kPieces = D / 8, kUnit = S::kUnit;
+  constexpr int kNt = S::kNt, kKt = S::kKt, kKs = S::kKs, kDt = S::kDt;
   const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave), n = lane % 32, g = lane / 32;
   const uint32_t sees = p.sees(it.block, a.tb), units = (sees + kUnit - 1) / kUnit;
   const uint32_t tok0 = it.block * a.tb;
   const uint32_t cols = min(a.tb, p.n - tok0) * a.ratio;
   const int32_t* ids = a.pages.ids + static_cast<uint64_t>(it.row) * a.pages.ld;
-  // the lane's column
-  const uint32_t col = kWaveCols * wave + n, tok = tok0 + col / a.ratio;
-  const bool live = col < cols;
-  const uint32_t h = it.head * a.ratio + col % a.ratio;
-  const uint32_t reach = live ? p.base + tok + 1 : 0;  // positions that it sees
-  // what the wavefront's columns see: all of them, and any
-  const bool works = kWaveCols * wave < cols;
-  const uint32_t all_see = works ? p.base + tok0 + kWaveCols * wave / a.ratio + 1 : 0;
-  const uint32_t any_sees = works ? p.base + tok0 + (min(cols, kWaveCols * (wave + 1)) - 1) / a.ratio + 1 : 0;
-  const bool full = kWaveCols * (wave + 1) <= cols;
+  // the wavefront's columns and what they see: all of them, and any
+  const uint32_t col0 = 32 * kNt * wave;
+  const bool works = col0 < cols, full = col0 + 32 * kNt <= cols;
+  const uint32_t all_see = full ? p.base + tok0 + col0 / a.ratio + 1 : 0;
+  const uint32_t any_sees = works ? p.base + tok0 + (min(cols, col0 + 32 * kNt) - 1) / a.ratio + 1 : 0;
+  const uint32_t uw = min(u1, (any_sees + kUnit - 1) / kUnit);  // the wavefront's units end here
+  uint32_t reach[kNt];  // positions that the lane's columns see
 
-  u32x4_t qf[S::kKs];
-  {
+  u32x4_t qf[kNt][kKs];
+#pragma unroll
+  for (int c = 0; c < kNt; ++c) {
+    const uint32_t col = col0 + 32 * c + n, tok = tok0 + col / a.ratio, h = it.head * a.ratio + col % a.ratio;
+    const bool live = col < cols;
+    reach[c] = live ? p.base + tok + 1 : 0;
     const uint16_t* src = a.q + static_cast<uint64_t>(p.t0 + tok) * a.ldq + static_cast<uint64_t>(h) * D + 8 * g;
 #pragma unroll
-    for (int k = 0; k < S::kKs; ++k) {
-      qf[k] = u32x4_t{0, 0, 0, 0};
-      if (live) qf[k] = *reinterpret_cast<const u32x4_t*>(src + 16 * k);
+    for (int k = 0; k < kKs; ++k) {
+      qf[c][k] = u32x4_t{0, 0, 0, 0};
+      if (live) qf[c][k] = *reinterpret_cast<const u32x4_t*>(src + 16 * k);
     }
   }
-  f32x16_t o[S::kDt];
-#pragma unroll
-  for (int d = 0; d < S::kDt; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-  float m = kNoMax, mc = fmaxf(m * a.scale2, -kFinite), l = 0.f;
 
-  // page numbers of the 16-position quarters of unit u; a quarter past the last
-  // position reads that position's
-  auto quarter = [&](uint32_t u, uint32_t i) { return min(kUnit * u + 16 * i, (sees - 1) & ~15u); };
-  int32_t id[4];
-  auto read_ids = [&](uint32_t u) {
+  bool missing = false;  // a page of the range that does not exist
+  bool far = false;      // a maximum of the lane's columns passed kFarMax
+  f32x16_t o[kNt][kDt];
+  float m[kNt], mc[kNt], l[kNt];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) id[i] = sload(ids, quarter(u, i) >> a.pages.shift);
-  };
-  uint32_t known = 0;  // quarters of the unit that have a page
-  auto issue = [&](uint32_t u, uint32_t buf) {
-    known = 0;
+  for (int c = 0; c < kNt; ++c) {
+    m[c] = kNoMax;
+    mc[c] = fmaxf(kNoMax * a.scale2, -kFinite);
+    l[c] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) known |= (static_cast<uint32_t>(id[i]) < a.pages.n_pages ? 1u : 0u) << i;
-    const uint32_t q0 = quarter(u, wave), last = min(sees - 1 - q0, 15u);
-    const int32_t page = wave == 0 ? id[0] : wave == 1 ? id[1] : wave == 2 ? id[2] : id[3];
-    const uint32_t within = (it.head << a.pages.shift) + (q0 & ((1u << a.pages.shift) - 1));
-    const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(page) < a.pages.n_pages ? page : 0) * a.pages.stride8 * 8 +
-                         static_cast<uint64_t>(within) * D;
-    uint8_t* to = lds + buf * (2 * S::kTile) + wave * (16 * D * 2);
+    for (int d = 0; d < kDt; ++d)
 #pragma unroll
-    for (int y = 0; y < kLoads; ++y) {
-      const uint32_t piece = 64 * y + lane, row = piece / kPieces, c = piece % kPieces;
-      const uint32_t from = min(row, last) * D + 8 * (c ^ key_swap<D>(row));
-      __builtin_amdgcn_global_load_lds(a.k + off + from, to + 1024 * y, 16, 0, 0);
-    }
-#pragma unroll
-    for (int y = 0; y < kLoads; ++y) {
-      const uint32_t piece = 64 * y + lane, row = piece / kPieces, c = piece % kPieces;
-      const uint32_t from = min(row, last) * D + 8 * (c ^ value_swap<D>(row));
-      __builtin_amdgcn_global_load_lds(a.v + off + from, to + S::kTile + 1024 * y, 16, 0, 0);
-    }
-  };
+      for (int i = 0; i < 16; ++i) o[c][d][i] = 0.f;
+  }
 
-  read_ids(u0);
-  __syncthreads();  // the tiles are free (the plan or the item before lay there)
-  issue(u0, 0);
-  uint32_t buf = 0;
-  for (uint32_t u = u0; u < u1; ++u, buf ^= 1) {
-    const uint32_t here = known;
-    if (u + 1 < u1) read_ids(u + 1);
-    wait_vmem<0>();
-    __syncthreads();
-    if (u + 1 < u1) issue(u + 1, buf ^ 1);
-    if (kUnit * u >= any_sees) continue;
-    const uint8_t* kt = lds + buf * (2 * S::kTile);
-    f32x16_t sc[2];
+  typedef __attribute__((address_space(3))) uint8_t lds1;
+  typedef const __attribute__((address_space(3))) u32x4_t lds16;
+  typedef __attribute__((address_space(3))) s16x4_t lds8;
+  const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds1*)lds));
+  // The wavefront's rows of a tile come from one page; a row past the last position is
+  // that position's.
+  auto first_row = [&](uint32_t u) { return min(kUnit * u + S::kRows * wave, (sees - 1) & ~(S::kRows - 1u)); };
+  auto page_of = [&](uint32_t u) { return sload(ids, first_row(min(u, u1 - 1)) >> a.pages.shift); };
+  uint32_t from[2][S::kLoads];  // byte offsets of the lane's pieces
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+  for (int y = 0; y < S::kLoads; ++y) {
+    const uint32_t piece = 64 * y + lane, row = piece / kPieces, c = piece % kPieces, at = S::kRows * wave + row;
+    from[0][y] = 2 * (row * D + 8 * (c ^ key_swap<D>(at)));
+    from[1][y] = 2 * (row * D + 8 * (c ^ value_swap<D>(at)));
+  }
+  auto load_rows = [&](const uint16_t* pages, int which, uint32_t u, int32_t page, uint32_t to) {
+    const uint32_t r0 = first_row(u), last = sees - 1 - r0;
+    const uint32_t within = (it.head << a.pages.shift) + (r0 & ((1u << a.pages.shift) - 1));
+    const uint16_t* base = pages + static_cast<uint64_t>(static_cast<uint32_t>(page) < a.pages.n_pages ? page : 0) * a.pages.stride8 * 8 +
+                           static_cast<uint64_t>(within) * D;
+    to += S::kRows * wave * D * 2;
+    if (last >= S::kRows - 1u) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+      for (int y = 0; y < S::kLoads; ++y) load_lds(base, from[which][y], to + 1024 * y);
+    } else {
 #pragma unroll
-      for (int k = 0; k < S::kKs; ++k) {
-        const uint32_t row = 32 * t + n;
-        const u32x4_t kf = *reinterpret_cast<const u32x4_t*>(kt + 16 * (row * kPieces + ((2 * k + g) ^ key_swap<D>(row))));
-        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, kf), __builtin_bit_cast(bf16x8_t, qf[k]), sc[t], 0, 0, 0);
+      for (int y = 0; y < S::kLoads; ++y) {
+        const uint32_t row = (64 * y + lane) / kPieces;
+        load_lds(base, from[which][y] - (row - min(row, last)) * (2 * D), to + 1024 * y);
       }
     }
-    if (!full || kUnit * (u + 1) > all_see || here != 15) {
+  };
+  int32_t page = page_of(u0);  // of the next unit to be asked for
+  auto issue = [&](uint32_t i, uint32_t place) {
+    load_rows(a.k, 0, i, page, place);
+    load_rows(a.v, 1, i, page, place + S::kTile);
+    page = page_of(i + 1);
+  };
+  // Operand addresses in a tile: the swap makes the step k (or d) a bit pattern to
+  // be turned, kKx (kDx) of them, the rest an offset.
+  constexpr int kKx = D == 96 ? 2 : D == 192 ? 4 : kKs, kDx = D == 96 ? 1 : D == 192 ? 2 : kDt;
+  const uint32_t key_at = 16 * (n * kPieces + (g ^ key_swap<D>(n)));
+  // a lane's positions are 16 s + 4 g + j (and 8 more) of component 32 d + n; it reads 4
+  // components of the position that its place among 16 names
+  const uint32_t vr = 4 * g + (lane % 16) / 4;
+  const uint32_t value_at = 16 * (vr * kPieces + ((n / 16 * 2 + lane % 4 / 2) ^ value_swap<D>(vr))) + 8 * (lane % 2);
+  auto scores = [&](uint32_t kt, f32x16_t (&sc)[kKt][kNt]) {
+    const uint32_t at = kt + key_at;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < kKt; ++t) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t at = 32 * t + 8 * (i / 4) + 4 * g + i % 4;
-          if (kUnit * u + at >= reach || !(here >> (2 * t + i / 8) & 1)) sc[t][i] = -INFINITY;
+      for (int c = 0; c < kNt; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[t][c][i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kKs; ++k) {
+        const u32x4_t kf = *((lds16*)static_cast<uintptr_t>((at ^ (k % kKx * 32)) + (32 * t * D * 2 + k / kKx * (kKx * 32))));
+#pragma unroll
+        for (int c = 0; c < kNt; ++c)
+          sc[t][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, kf), __builtin_bit_cast(bf16x8_t, qf[c][k]),
+                                                             sc[t][c], 0, 0, 0);
+      }
+    }
+  };
+  // scores of unit u that are not seen, and the maximum, which weights are relative
+  // to: it moves where a score outgrows it by 2^11
+  auto settle = [&](uint32_t u, f32x16_t (&sc)[kKt][kNt]) {
+    if (kUnit * (u + 1) > all_see || missing) {
+      uint32_t known = 0;
+#pragma unroll
+      for (uint32_t i = 0; i < kUnit / 16; ++i) {
+        const uint32_t at = min((kUnit * u + 16 * i) >> a.pages.shift, a.pages.cols - 1);
+        known |= (static_cast<uint32_t>(sload(ids, at)) < a.pages.n_pages ? 1u : 0u) << i;
+      }
+#pragma unroll
+      for (int t = 0; t < kKt; ++t)
+#pragma unroll
+        for (int c = 0; c < kNt; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t at = 32 * t + 8 * (i / 4) + 4 * g + i % 4;
+            if (kUnit * u + at >= reach[c] || !(known >> (2 * t + i / 8) & 1)) sc[t][c][i] = -INFINITY;
+          }
+    }
+    float x[kNt];
+    bool grown = false;
+#pragma unroll
+    for (int c = 0; c < kNt; ++c) {
+      x[c] = sc[0][c][0];
+#pragma unroll
+      for (int t = 0; t < kKt; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[c] = fmaxf(x[c], sc[t][c][i]);
+      grown |= fmaf(x[c], a.scale2, -mc[c]) > 11.f;
+    }
+    if (__any(grown)) {
+#pragma unroll
+      for (int c = 0; c < kNt; ++c) {
+        m[c] = fmaxf(m[c], fmaxf(x[c], lane_xor(x[c], 32)));
+        const float to = fminf(fmaxf(m[c] * a.scale2, -kFinite), kFinite);
+        const float f = __builtin_amdgcn_exp2f(mc[c] - to);
+        far |= !(fabsf(to) < kFarMax) && m[c] != kNoMax;
+        mc[c] = to;
+        l[c] *= f;
+#pragma unroll
+        for (int d = 0; d < kDt; ++d) o[c][d] *= f;
+      }
+    }
+  };
+  // the weights of 16 positions at a time, and their products with the values
+  auto weigh = [&](uint32_t vt, const f32x16_t (&sc)[kKt][kNt]) {
+    const uint32_t at = vt + value_at;
+#pragma unroll
+    for (int s = 0; s < 2 * kKt; ++s) {
+      u32x4_t pf[kNt];
+#pragma unroll
+      for (int c = 0; c < kNt; ++c) {
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float x = __builtin_amdgcn_exp2f(fmaf(sc[s / 2][c][8 * (s % 2) + j], a.scale2, -mc[c]));
+          const float y = __builtin_amdgcn_exp2f(fmaf(sc[s / 2][c][8 * (s % 2) + j + 1], a.scale2, -mc[c]));
+          sum[0] += x;
+          sum[1] += y;
+          pf[c][j / 2] = pack_bf16(x, y);
         }
-    }
-    // weights relative to the maximum so far; it moves only where a lane's sum
-    // shows that they outgrew it by 2^11
-    float w[32], sum;
-    auto weigh = [&] {
+        l[c] += sum[0] + sum[1];
+      }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = __builtin_amdgcn_exp2f(fmaf(sc[i / 16][i % 16], a.scale2, -mc));
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < 32; ++i) s[i % 4] += w[i];
-      sum = (s[0] + s[1]) + (s[2] + s[3]);
-      return !(sum <= 2048.f);
-    };
-    if (__any(weigh())) {
-      float x = sc[0][0];
-#pragma unroll
-      for (int i = 1; i < 32; ++i) x = fmaxf(x, sc[i / 16][i % 16]);
-      x = fmaxf(x, lane_xor(x, 32));
-      m = fmaxf(m, x);
-      const float to = fminf(fmaxf(m * a.scale2, -kFinite), kFinite);
-      const float f = __builtin_amdgcn_exp2f(mc - to);
-      mc = to;
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < S::kDt; ++d) o[d] *= f;
-      weigh();
-    }
-    l += sum;
-    const uint8_t* vt = kt + S::kTile;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      u32x4_t pf;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) pf[j] = pack_bf16(w[8 * s + 2 * j], w[8 * s + 2 * j + 1]);
-#pragma unroll
-      for (int d = 0; d < S::kDt; ++d) {
-        // lane: positions 16 s + 4 g + j (and 8 more) of component 32 d + n; it reads
-        // 4 components of the position that its place among 16 names
-        const uint32_t r0 = 16 * s + 4 * g + (lane % 16) / 4, c = 4 * d + (n / 16) * 2 + (lane % 4) / 2;
-        const uint32_t half = 8 * (lane % 2);
-        typedef __attribute__((address_space(3))) s16x4_t lds4;
-        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds4*)(vt + 16 * (r0 * kPieces + (c ^ value_swap<D>(r0))) + half));
-        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds4*)(vt + 16 * ((r0 + 8) * kPieces + (c ^ value_swap<D>(r0 + 8))) + half));
-        const u32x2_t a0 = __builtin_bit_cast(u32x2_t, lo), a1 = __builtin_bit_cast(u32x2_t, hi);
+      for (int d = 0; d < kDt; ++d) {
+        const uint32_t to = (at ^ (d % kDx * 64)) + (16 * s * D * 2 + d / kDx * (kDx * 64));
+        const u32x2_t a0 = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds8*)static_cast<uintptr_t>(to)));
+        const u32x2_t a1 = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds8*)static_cast<uintptr_t>(to + 8 * D * 2)));
         const u32x4_t vf = {a0[0], a0[1], a1[0], a1[1]};
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, vf), __builtin_bit_cast(bf16x8_t, pf), o[d], 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < kNt; ++c)
+          o[c][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, vf), __builtin_bit_cast(bf16x8_t, pf[c]),
+                                                            o[c][d], 0, 0, 0);
       }
     }
+  };
+  __syncthreads();  // the ring is free (the plan or the item before lay there)
+#pragma unroll
+  for (uint32_t i = 0; i < S::kRing - 1; ++i)
+    if (u0 + i < u1) issue(u0 + i, ring + i * (2 * S::kTile));
+  // pages that do not exist are looked for once
+  for (uint32_t at = kUnit * u0 >> a.pages.shift, end = (min(kUnit * u1, sees) - 1) >> a.pages.shift; at <= end; at += kWave)
+    missing |= static_cast<uint32_t>(ids[min(at + lane, end)]) >= a.pages.n_pages;
+  missing = __any(missing);
+  // the queries have to be there before the loads in flight are counted
+#pragma unroll
+  for (int c = 0; c < kNt; ++c)
+#pragma unroll
+    for (int k = 0; k < kKs; ++k) asm volatile("" : "+v"(qf[c][k]));
+  uint32_t place = ring;  // of unit u
+  for (uint32_t u = u0; u < u1; ++u) {
+    if (u + S::kRing - 2 < u1)
+      wait_vmem<2 * S::kLoads*(S::kRing - 2)>();
+    else
+      wait_vmem<0>();
+    __syncthreads();
+    if (u + S::kRing - 1 < u1) issue(u + S::kRing - 1, place == ring ? ring + (S::kRing - 1) * (2 * S::kTile) : place - 2 * S::kTile);
+    if (u < uw) {
+      f32x16_t sc[kKt][kNt];
+      scores(place, sc);
+      settle(u, sc);
+      weigh(place + S::kTile, sc);
+    }
+    place = place == ring + (S::kRing - 1) * (2 * S::kTile) ? ring : place + 2 * S::kTile;
   }
   if (!works) return;
-  l += lane_xor(l, 32);
-  float zero = 0.f;
-#pragma unroll
-  for (int d = 0; d < S::kDt; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) zero = fmaf(o[d][i], 0.f, zero);
-  // columns whose weights are NaN keep it: so does every component
-  const bool lost = live && l == l && (!(zero + lane_xor(zero, 32) + l * 0.f == 0.f) || !(fabsf(mc) < kFarMax || m == kNoMax));
-  const float r = l == 0.f ? 0.f : 1.f / l;
   const bool direct = u0 == 0 && u1 == units;
-  if (live && direct && !lost) {
-    uint16_t* dst = a.out + static_cast<uint64_t>(p.t0 + tok) * a.ldo + static_cast<uint64_t>(h) * D + 4 * g;
 #pragma unroll
-    for (int d = 0; d < S::kDt; ++d)
+  for (int c = 0; c < kNt; ++c) {
+    const uint32_t col = col0 + 32 * c + n, tok = tok0 + col / a.ratio, h = it.head * a.ratio + col % a.ratio;
+    const bool live = col < cols;
+    l[c] += lane_xor(l[c], 32);
+    float zero = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const u32x2_t x = {pack_bf16(o[d][i] * r, o[d][i + 1] * r), pack_bf16(o[d][i + 2] * r, o[d][i + 3] * r)};
-        *reinterpret_cast<u32x2_t*>(dst + 32 * d + 2 * i) = x;
+    for (int d = 0; d < kDt; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) zero = fmaf(o[c][d][i], 0.f, zero);
+    // columns whose weights are NaN keep it: so does every component
+    const bool lost = live && (far || (l[c] == l[c] && !(zero + lane_xor(zero, 32) + l[c] * 0.f == 0.f)));
+    const float r = l[c] == 0.f ? 0.f : 1.f / l[c];
+    if (live && direct && !lost) {
+      uint16_t* dst = a.out + static_cast<uint64_t>(p.t0 + tok) * a.ldo + static_cast<uint64_t>(h) * D + 4 * g;
+#pragma unroll
+      for (int d = 0; d < kDt; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const u32x2_t x = {pack_bf16(o[c][d][i] * r, o[c][d][i + 1] * r), pack_bf16(o[c][d][i + 2] * r, o[c][d][i + 3] * r)};
+          *reinterpret_cast<u32x2_t*>(dst + 32 * d + 2 * i) = x;
+        }
+    } else if (live && !direct) {
+      const uint64_t at = static_cast<uint64_t>(part) * a.cap + col;
+      if (g == 0) {
+        a.part_ml[2 * at] = lost ? INFINITY : mc[c];  // an infinite maximum: the column is computed by itself
+        a.part_ml[2 * at + 1] = l[c];
       }
-  } else if (live && !direct) {
-    const uint64_t slot = static_cast<uint64_t>(part) * a.cap + col;
-    if (g == 0) {
-      a.part_ml[2 * slot] = lost ? INFINITY : mc;  // an infinite maximum: the column is computed by itself
-      a.part_ml[2 * slot + 1] = l;
+      float* dst = a.part_o + at * D + 4 * g;
+#pragma unroll
+      for (int d = 0; d < kDt; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<f32x4_t*>(dst + 32 * d + 2 * i) =
+              f32x4_t{o[c][d][i] * r, o[c][d][i + 1] * r, o[c][d][i + 2] * r, o[c][d][i + 3] * r};
     }
-    float* dst = a.part_o + slot * D + 4 * g;
-#pragma unroll
-    for (int d = 0; d < S::kDt; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<f32x4_t*>(dst + 32 * d + 2 * i) = f32x4_t{o[d][i] * r, o[d][i + 1] * r, o[d][i + 2] * r, o[d][i + 3] * r};
-  }
-  uint64_t again = __ballot(direct && lost) & 0xFFFFFFFFu;
-  for (; again; again &= again - 1) {
-    const uint32_t c = kWaveCols * wave + __builtin_ctzll(again), t = tok0 + c / a.ratio;
-    redo<D>(a, it.row, p.t0 + t, it.head * a.ratio + c % a.ratio, p.base + t + 1);
+    uint64_t again = __ballot(direct && lost) & 0xFFFFFFFFu;
+    for (; again; again &= again - 1) {
+      const uint32_t x = col0 + 32 * c + __builtin_ctzll(again), t = tok0 + x / a.ratio;
+      redo<D>(a, it.row, p.t0 + t, it.head * a.ratio + x % a.ratio, p.base + t + 1);
+    }
   }
 }
 
@@ -447,11 +545,11 @@ __device__ __forceinline__ uint32_t worker_of(uint32_t block, uint32_t workers) 
 
 template <int D>
 __global__ __launch_bounds__(kChunkThreads, ChunkShape<D>::kWgs) void k_chunk(const ChunkArgs a) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ uint64_t carry[4];
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];  // from LDS address 0 on: there is no other
   uint64_t* pre = reinterpret_cast<uint64_t*>(lds);  // until the first tile arrives
   const uint32_t rows = a.pages.rows;
-  make_prefix(a, pre, carry);
+  constexpr uint32_t kUnit = ChunkShape<D>::kUnit;
+  make_prefix(a, pre, pre + rows + 1);
   // tokens that see nothing
   for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const RowPart p(a, r);
@@ -462,88 +560,183 @@ __global__ __launch_bounds__(kChunkThreads, ChunkShape<D>::kWgs) void k_chunk(co
   const uint64_t total = uniform64(pre[rows]) * a.hkv, quota = quota_of(a, total);
   const uint32_t w = worker_of(blockIdx.x, a.workers);
   const uint64_t x0 = w * quota, x1 = min(x0 + quota, total);
-  if (x0 >= total) return;
-  Item it = find(a, pre, x0);
-  RowPart p(a, it.row);
-  for (;;) {
-    const uint32_t sees = p.sees(it.block, a.tb), units = (sees + kUnit - 1) / kUnit;
-    const uint32_t u0 = x0 > it.at ? static_cast<uint32_t>((x0 - it.at + kUnit - 1) / kUnit) : 0;
-    const uint32_t u1 = static_cast<uint32_t>(min(static_cast<uint64_t>(units), (x1 - it.at + kUnit - 1) / kUnit));
-    if (u0 < u1) run_item<D>(a, it, p, u0, u1, 2 * w + (x0 > it.at ? 0 : 1), lds);
-    it.at += sees;
-    if (it.at >= x1) return;
-    if (++it.block == p.blocks(a.tb)) {
-      it.block = 0;
-      do {
-        if (++it.row == rows) {
-          it.row = 0;
-          ++it.head;
-        }
-        p = RowPart(a, it.row);
-      } while (p.n == 0);
+  Cut cut = {};
+  if (x0 < total) {
+    Item it = find(a, pre, x0);
+    RowPart p(a, it.row);
+    for (;;) {
+      const uint32_t sees = p.sees(it.block, a.tb), units = (sees + kUnit - 1) / kUnit;
+      const uint32_t u0 = x0 > it.at ? static_cast<uint32_t>((x0 - it.at + kUnit - 1) / kUnit) : 0;
+      const uint32_t u1 = static_cast<uint32_t>(min(static_cast<uint64_t>(units), (x1 - it.at + kUnit - 1) / kUnit));
+      if (x0 <= it.at && u1 < units) {  // the last one, which goes on in the next workers' ranges
+        const uint64_t last = it.at + static_cast<uint64_t>(units - 1) * kUnit;
+        const uint32_t tok0 = it.block * a.tb;
+        cut = Cut{static_cast<uint32_t>(last / quota) - w, it.head, min(a.tb, p.n - tok0) * a.ratio, p.t0 + tok0, p.base + tok0 + 1, it.row, w, 0};
+      }
+      if (u0 < u1) run_item<D>(a, it, p, u0, u1, 2 * w + (x0 > it.at ? 0 : 1), lds);
+      it.at += sees + kItemCost;
+      if (it.at >= x1) break;
+      if (++it.block == p.blocks(a.tb)) {
+        it.block = 0;
+        do {
+          if (++it.row == rows) {
+            it.row = 0;
+            ++it.head;
+          }
+          p = RowPart(a, it.row);
+        } while (p.n == 0);
+      }
     }
   }
+  if (threadIdx.x == 0) a.cuts[w] = cut;
 }
 
-// The item that the end of worker blockIdx.x's range cuts first: 8 columns of its
-// parts a workgroup, 32 lanes each.
-constexpr uint32_t kJoinCols = 8;
+// Items that several workers had.  The cuts are few beside the workers, so every
+// workgroup lists them, and all take (cut, some of its columns) in turn.  A group of
+// 32 lanes adds the parts of a column four at a time, relative to their maximum so
+// far.  Cuts of up to kJoinFew parts, the ends of most ranges, go by kJoinWide columns a
+// workgroup, a group each; those of more by kJoinCols, a column by kJoinSplit groups,
+// each with every kJoinSplit-th part, whose sums meet in LDS.
+constexpr uint32_t kJoinCols = 2, kJoinSplit = 4, kJoinGroups = 1024, kJoinFew = 16, kJoinWide = 16;
+static_assert(kJoinCols * kJoinSplit * 32 == kChunkThreads, "lanes");
 template <int D>
 __global__ __launch_bounds__(kChunkThreads) void k_chunk_join(const ChunkArgs a) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ uint64_t carry[4];
-  uint64_t* pre = reinterpret_cast<uint64_t*>(lds);
-  make_prefix(a, pre, carry);
-  const uint64_t total = uniform64(pre[a.pages.rows]) * a.hkv, quota = quota_of(a, total);
-  const uint32_t w = blockIdx.x;
-  const uint64_t x0 = w * quota, x = x0 + quota;
-  if (x >= total) return;
-  const Item it = find(a, pre, x);
-  const RowPart p(a, it.row);
-  const uint32_t sees = p.sees(it.block, a.tb), units = (sees + kUnit - 1) / kUnit;
-  // began in this range, and goes on behind it
-  if (it.at < x0 || it.at >= x || (x - it.at + kUnit - 1) / kUnit >= units) return;
-  const uint32_t tok0 = it.block * a.tb, cols = min(a.tb, p.n - tok0) * a.ratio;
-  const uint32_t sub = threadIdx.x / 32, lane = threadIdx.x % 32, col = blockIdx.y * kJoinCols + sub;
-  if (col - sub % 2 >= cols) return;  // both columns of the wavefront
-  const bool live = col < cols;
-  // workers after this one that have units of the item
-  const uint64_t last = it.at + static_cast<uint64_t>(units - 1) * kUnit;
-  const uint32_t more = static_cast<uint32_t>(last / quota) - w;
-  auto slot = [&](uint32_t i) { return static_cast<uint64_t>(i ? 2 * (w + i) : 2 * w + 1) * a.cap + (live ? col : cols - 1); };
-  float best = -INFINITY, sum = 0.f;
-  bool odd = false;
-  for (uint32_t i = lane; i <= more; i += 32) {
-    const float m = a.part_ml[2 * slot(i)];
-    odd |= m == INFINITY;
-    best = fmaxf(best, m);
-  }
-  for (int d = 16; d; d /= 2) best = fmaxf(best, lane_xor(best, d));
-  for (uint32_t i = lane; i <= more; i += 32) sum += a.part_ml[2 * slot(i) + 1] * __builtin_amdgcn_exp2f(a.part_ml[2 * slot(i)] - best);
-  for (int d = 16; d; d /= 2) sum += lane_xor(sum, d);
-  const uint64_t which = __ballot(odd && live);
-  const float r = sum == 0.f ? 0.f : 1.f / sum;
   constexpr int kPer = D / 32;
-  float o[kPer];
+  __shared__ uint32_t list[kMaxWorkers];  // cuts of few parts from its begin on, of many from its end
+  __shared__ uint32_t counts[kMaxWorkers / kChunkThreads][kChunkThreads / kWave];
+  __shared__ float sums[kJoinCols][kJoinSplit][D], maxima[kJoinCols][kJoinSplit], totals[kJoinCols][kJoinSplit];
+  const uint32_t wave = uniform(threadIdx.x / kWave);
+  constexpr int kSteps = kMaxWorkers / kChunkThreads;
+  uint32_t more[kSteps];
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (uint32_t i = 0; i <= more; ++i) {
-    const uint64_t s = slot(i);
-    const float f = a.part_ml[2 * s + 1] * __builtin_amdgcn_exp2f(a.part_ml[2 * s] - best) * r;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = fmaf(f, a.part_o[s * D + lane + 32 * e], o[e]);
+  for (int i = 0; i < kSteps; ++i) {
+    const uint32_t w = i * kChunkThreads + threadIdx.x;
+    more[i] = w < a.workers ? a.cuts[w].more : 0;
   }
-  const uint32_t tok = tok0 + col / a.ratio, h = it.head * a.ratio + col % a.ratio;
-  if (live && !(which >> (__lane_id() & 32) & 0xFFFFFFFFu)) {
-    uint16_t* dst = a.out + static_cast<uint64_t>(p.t0 + tok) * a.ldo + static_cast<uint64_t>(h) * D + lane;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) dst[32 * e] = static_cast<uint16_t>(pack_bf16(o[e], 0.f));
+  for (int i = 0; i < kSteps; ++i) {
+    const uint64_t any = __ballot(more[i] != 0), many = __ballot(more[i] >= kJoinFew);
+    if (__lane_id() == 0) counts[i][wave] = __popcll(any & ~many) | __popcll(many) << 16;
   }
-  for (uint32_t side = 0; side < 2; ++side) {
-    if (!(which >> (32 * side) & 0xFFFFFFFFu)) continue;
-    const uint32_t c = uniform(col - sub % 2) + side, t = tok0 + c / a.ratio;
-    redo<D>(a, it.row, p.t0 + t, it.head * a.ratio + c % a.ratio, p.base + t + 1);
+  __syncthreads();
+  uint32_t n[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const bool kind = more[i] >= kJoinFew;
+    const uint64_t many = __ballot(kind), which = kind ? many : __ballot(more[i] != 0) & ~many;
+    uint32_t at = __popcll(which & ((uint64_t{1} << __lane_id()) - 1));
+#pragma unroll
+    for (uint32_t v = 0; v < kChunkThreads / kWave; ++v) {
+      const uint32_t x = counts[i][v];
+      if (v == wave) at += kind ? n[1] : n[0];
+      n[0] += x & 0xFFFF;
+      n[1] += x >> 16;
+    }
+    if (more[i]) list[kind ? kMaxWorkers - 1 - at : at] = i * kChunkThreads + threadIdx.x;
+  }
+  __syncthreads();
+  const uint32_t lane = threadIdx.x % 32, group = threadIdx.x / 32;
+  float m, l, o[kPer];  // of a group's parts: maximum, weight sum, weighted sum of means; m infinite where one is computed by itself
+  auto add = [&](const Cut& cut, uint32_t col, bool live, uint32_t first, uint32_t step) __attribute__((always_inline)) {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+    for (uint32_t i0 = first; i0 <= cut.more; i0 += 4 * step) {
+      float mi[4], li[4], x[4][kPer];
+#pragma unroll
+      for (uint32_t y = 0; y < 4; ++y) {
+        const uint32_t i = i0 + y * step;
+        const uint64_t s = static_cast<uint64_t>(i ? 2 * (cut.worker + i) : 2 * cut.worker + 1) * a.cap + col;
+        mi[y] = -INFINITY;
+        li[y] = 0.f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) x[y][e] = 0.f;
+        if (i <= cut.more && live) {
+          mi[y] = a.part_ml[2 * s];
+          li[y] = a.part_ml[2 * s + 1];
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) x[y][e] = a.part_o[s * D + lane + 32 * e];
+        }
+      }
+      const float to = fmaxf(m, fmaxf(fmaxf(mi[0], mi[1]), fmaxf(mi[2], mi[3])));
+      // weights of 0 relative to a maximum that is none yet
+      const float f = m == to ? 1.f : __builtin_amdgcn_exp2f(m - to);
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] *= f;
+#pragma unroll
+      for (uint32_t y = 0; y < 4; ++y) {
+        const float w = mi[y] == -INFINITY ? 0.f : li[y] * __builtin_amdgcn_exp2f(mi[y] - to);
+        l += w;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] = fmaf(w, x[y][e], o[e]);
+      }
+      m = to;
+    }
+  };
+  auto once_more = [&](const Cut& cut, uint32_t col) __attribute__((always_inline)) {
+    const uint32_t t = col / a.ratio;
+    redo<D>(a, uniform(cut.row), uniform(cut.token) + t, uniform(cut.head) * a.ratio + col % a.ratio, uniform(cut.sees) + t);
+  };
+  auto row_of = [&](const Cut& cut, uint32_t col) {
+    return a.out + static_cast<uint64_t>(cut.token + col / a.ratio) * a.ldo + static_cast<uint64_t>(cut.head * a.ratio + col % a.ratio) * D;
+  };
+  const uint32_t wide = (a.cap + kJoinWide - 1) / kJoinWide, narrow = (a.cap + kJoinCols - 1) / kJoinCols;
+  const uint32_t few = uniform(n[0]) * wide, tasks = few + uniform(n[1]) * narrow;
+  for (uint32_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    if (task < few) {
+      const Cut cut = a.cuts[uniform(list[task / wide])];
+#pragma unroll
+      for (uint32_t y = 0; y < kJoinWide / 8; ++y) {
+        const uint32_t col = task % wide * kJoinWide + 8 * y + group;
+        const bool live = col < cut.cols;
+        add(cut, col, live, 0, 1);
+        const bool odd = m == INFINITY;
+        const float r = l == 0.f ? 0.f : 1.f / l;
+        if (live && !odd) {
+          uint16_t* dst = row_of(cut, col) + lane;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) dst[32 * e] = static_cast<uint16_t>(pack_bf16(o[e] * r, 0.f));
+        }
+        const uint64_t again = __ballot(live && odd);
+        for (uint32_t side = 0; side < 2; ++side)
+          if (again >> (32 * side) & 0xFFFFFFFFu) once_more(cut, uniform(col) + side);
+      }
+    } else {
+      const Cut cut = a.cuts[uniform(list[kMaxWorkers - 1 - (task - few) / narrow])];
+      const uint32_t c = group / kJoinSplit, split = group % kJoinSplit, col = (task - few) % narrow * kJoinCols + c;
+      const bool live = col < cut.cols;
+      add(cut, col, live, split, kJoinSplit);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) sums[c][split][lane + 32 * e] = o[e];
+      if (lane == 0) {
+        maxima[c][split] = m;
+        totals[c][split] = l;
+      }
+      __syncthreads();
+      float best = -INFINITY, total = 0.f, f[kJoinSplit];
+#pragma unroll
+      for (uint32_t i = 0; i < kJoinSplit; ++i) best = fmaxf(best, maxima[c][i]);
+#pragma unroll
+      for (uint32_t i = 0; i < kJoinSplit; ++i) {
+        f[i] = maxima[c][i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(maxima[c][i] - best);
+        total = fmaf(f[i], totals[c][i], total);
+      }
+      const bool odd = best == INFINITY;
+      const float r = total == 0.f ? 0.f : 1.f / total;
+      if (live && !odd) {
+        uint16_t* dst = row_of(cut, col);
+        for (uint32_t e = threadIdx.x % (32 * kJoinSplit); e < D; e += 32 * kJoinSplit) {
+          float x = 0.f;
+#pragma unroll
+          for (uint32_t i = 0; i < kJoinSplit; ++i) x = fmaf(f[i] * r, sums[c][i][e], x);
+          dst[e] = static_cast<uint16_t>(pack_bf16(x, 0.f));
+        }
+      }
+      if (wave % (kJoinSplit / 2) == 0 && __any(live && odd)) once_more(cut, uniform(col));
+      __syncthreads();  // the sums are read
+    }
   }
 }
 
@@ -553,17 +746,18 @@ constexpr uint32_t kChunkMaxRows = 4096, kChunkMaxTokens = 1u << 22, kChunkMaxRa
 
 struct ChunkLayout {
   uint32_t workers, tb, cap;
-  uint64_t ml, bytes;
+  uint64_t ml, cuts, bytes;
 };
 ChunkLayout chunk_layout(uint32_t tokens, uint32_t ratio, uint32_t d) {
   ChunkLayout L;
-  L.workers = kCus * (d <= 128 ? 2 : 1);
-  L.tb = kCols / ratio;
+  L.workers = kCus * (d <= 96 ? 3 : d <= 192 ? 2 : 1);  // ChunkShape's workgroups
+  L.tb = 128 / ratio;                                   // ChunkShape's columns
   L.cap = std::min(tokens, L.tb) * ratio;
   const uint64_t slots = 2ull * L.workers * L.cap;
   auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
   L.ml = up(slots * d * 4);
-  L.bytes = L.ml + up(slots * 8);
+  L.cuts = L.ml + up(slots * 8);
+  L.bytes = L.cuts + up(L.workers * sizeof(Cut));
   return L;
 }
 
@@ -579,13 +773,14 @@ nwc_status chunk_shape(const nwc_cache* c, uint32_t rows, uint32_t tokens, uint3
 
 template <int D>
 nwc_status launch_chunk(const ChunkArgs& a, hipStream_t s) {
-  constexpr size_t lds = std::max<size_t>(ChunkShape<D>::kLds, (kChunkMaxRows + 1) * 8);
-  static_assert(lds + 64 <= kMaxLds, "LDS");
+  if (a.tb != ChunkShape<D>::kCols / a.ratio) return NWC_ERR_UNSUPPORTED;  // never: the layout's columns are the kernel's
+  constexpr size_t lds = std::max<size_t>(ChunkShape<D>::kLds, (kChunkMaxRows + 5) * 8);
+  static_assert(lds <= kMaxLds, "LDS");
   if (lds > 65536 && !allow_lds<k_chunk<D>, lds>()) return NWC_ERR_HIP;
   const nwc_status st = launch(k_chunk<D>, dim3(a.workers), dim3(kChunkThreads), lds, s, a);
   if (st) return st;
-  return launch(k_chunk_join<D>, dim3(a.workers, (a.cap + kJoinCols - 1) / kJoinCols), dim3(kChunkThreads),
-                (static_cast<size_t>(a.pages.rows) + 1) * 8, s, a);
+  const uint32_t groups = (a.cap + kJoinCols - 1) / kJoinCols;
+  return launch(k_chunk_join<D>, dim3(std::min(kJoinGroups, a.workers * groups)), dim3(kChunkThreads), 0, s, a);
 }
 
 }  // namespace
@@ -634,11 +829,15 @@ nwc_status nwc_attend_chunk(const nwc_cache* cache, const nwc_page_table* table,
   a.hkv = cache->kv_heads;
   a.tb = L.tb;
   a.cap = L.cap;
-  a.workers = L.workers;
+  // no more workers than a call of full tables has work for
+  const uint64_t items = std::min<uint64_t>(tokens, table->rows + tokens / L.tb) * a.hkv;
+  const uint64_t most = items * ((static_cast<uint64_t>(table->cols) << a.pages.shift) + kItemCost) / kLeast + 1;
+  a.workers = static_cast<uint32_t>(std::min<uint64_t>(L.workers, (most + 7) / 8 * 8));
   a.scale = scale;
   a.scale2 = scale * kLog2e;
   a.part_o = reinterpret_cast<float*>(w);
   a.part_ml = reinterpret_cast<float*>(w + L.ml);
+  a.cuts = reinterpret_cast<Cut*>(w + L.cuts);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (d) {
     case 64: return launch_chunk<64>(a, s);

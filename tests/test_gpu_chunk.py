@@ -190,19 +190,20 @@ def test_rows_that_see_nothing_and_padding():
 def test_starts_that_are_out_of_range_or_descend():
     # device data of any content: nothing outside the tensors is touched, and rows of sound numbers keep their results
     c = Case([6, 5, 7], [20, 30, 40], 4, 2, 64, 16, seed=5)
-    good = c.call()
-    nwc.nwc_attend_chunk(good)
-    torch.cuda.synchronize()
-    want = c.out.clone()
+    ref, size = c.ref()
+    # where positions are cut between workgroups follows from all rows, and with it the order of sums: the bits are
+    # not those of other starts, but every result is within the tolerance of one
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -10) * size
     for start in ([-5, 6, 11, 18], [0, 6, 11, 10 ** 9], [18, 6, 11, 18]):
         _say("starts %s" % start)
         c.out_all.fill_(7.0)
         c.start = np.asarray(start)
         nwc.nwc_attend_chunk(c.call())
         torch.cuda.synchronize()
-        assert torch.equal(c.out[6:18], want[6:18])
+        near = ((c.out.double() - ref).abs() <= tol).all(-1).all(-1)
+        assert bool(near[6:18].all())
         if start[0] <= 0:
-            assert torch.equal(c.out[:6], want[:6])
+            assert bool(near[:6].all())
         else:
             assert bool((c.out[:6] == 7.0).all())
 
