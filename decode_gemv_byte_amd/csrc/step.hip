@@ -15,6 +15,8 @@
 
 namespace {
 
+typedef __attribute__((ext_vector_type(8))) float f32x8_t;
+
 // Sum over the wavefront, in every lane.
 __device__ __forceinline__ float wave_sum(float v) {
   for (int x = 32; x; x /= 2) v += lane_xor(v, x);
@@ -213,8 +215,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void k_residual(const Residu
 // below the last one take its place.
 
 constexpr int kLpThreads = 512, kLpWaves = kLpThreads / kWave;
-constexpr uint32_t kLpMaxK = 64, kLpMaxSplit = 64, kLpFound = 2048;
-constexpr float kLowest = -3.402823466e+38f;
+constexpr uint32_t kLpMaxK = 64, kLpMaxSplit = 32, kLpFound = 2048;
+constexpr float kLowest = -3.402823466e+38f, kLowestC = -3e38f;
+constexpr float kFar = 0x1p20f;   // maxima, times c, whose product's rounding is off by 2^-4 at most
 constexpr float kGrow = 8.f;     // log2 of how far a logit may outgrow its lane's maximum
 constexpr float kNoWeight = -16384.f;  // a power of two that is 0 in FP32, and finite: 0 times it is 0
 
@@ -242,6 +245,14 @@ __device__ __forceinline__ float value_of(uint32_t o) {
 }
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
   return static_cast<uint64_t>(ordered(x)) << 32 | (0xFFFFFFFFu - index);
+}
+
+// The largest of three, as fmaxf, which asks for one instruction more a value (a
+// signalling NaN made quiet first).
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+  return r;
 }
 
 struct Stats {
@@ -304,10 +315,11 @@ __device__ __forceinline__ float kth_of_wave(float v, uint32_t k) {
 
 template <bool F32>
 __global__ __launch_bounds__(kLpThreads) void k_logprobs(const LogprobsArgs a) {
-  __shared__ float groups[kWave];
+  __shared__ float groups[kWave], shared_bound;
   __shared__ Stats waves[kLpWaves];
   __shared__ uint64_t found[kLpFound];
-  __shared__ uint32_t n_found;
+  __shared__ uint32_t n_found, n_lanes, counts[kLpWaves];
+  __shared__ uint16_t lanes[kLpThreads];
   __shared__ uint64_t best[2][kLpWaves];
   const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave);
   const uint64_t row = blockIdx.x / a.split;
@@ -315,70 +327,109 @@ __global__ __launch_bounds__(kLpThreads) void k_logprobs(const LogprobsArgs a) {
   const uint32_t v0 = part * a.chunk, v1 = min(v0 + a.chunk, a.vocab);  // this workgroup's logits
   const uint8_t* base = static_cast<const uint8_t*>(a.logits) + (row * a.ld + v0) * (F32 ? 4 : 2);
   const uint32_t n = v1 - v0, pieces = (n + 7) / 8;
-  if (threadIdx.x == 0) n_found = 0;
+  if (threadIdx.x == 0) n_found = n_lanes = 0;
 
-  // piece p of the part; past its end -infinity
-  auto load = [&](uint32_t p, float (&x)[8]) {
-    if (8 * p + 8 <= n) {
-      if constexpr (F32) {
-        const f32x4_t lo = reinterpret_cast<const f32x4_t*>(base)[2 * p], hi = reinterpret_cast<const f32x4_t*>(base)[2 * p + 1];
+  // pieces of 8, the last of which may be short and is filled with -infinity
+  const uint32_t full = n / 8;
+  typedef std::conditional_t<F32, f32x8_t, u32x4_t> Raw;
+  auto values = [&](const Raw& r, float (&x)[8]) {
+    if constexpr (F32) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = lo[j];
-          x[4 + j] = hi[j];
-        }
-      } else {
-        const u32x4_t v = reinterpret_cast<const u32x4_t*>(base)[p];
-        unpack8(v, x);
-      }
+      for (int j = 0; j < 8; ++j) x[j] = r[j];
     } else {
+      unpack8(r, x);
+    }
+  };
+  auto short_piece = [&](float (&x)[8]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 8 * p + j < n ? logit<F32>(a, row, v0 + 8 * p + j) : -INFINITY;
+    for (int j = 0; j < 8; ++j) x[j] = 8 * full + j < n ? logit<F32>(a, row, v0 + 8 * full + j) : -INFINITY;
+  };
+  // f(piece, whether there is one, its values) for the lane's pieces in order
+  auto walk = [&](auto f) {
+    const Raw* at = reinterpret_cast<const Raw*>(base);
+    uint32_t p = threadIdx.x;
+    float x[8];
+    for (; uniform(p - lane) + kWave <= full; p += kLpThreads) {
+      values(at[p], x);
+      f(p, true, x);
+    }
+    if (uniform(p - lane) < full) {
+      const bool on = p < full;
+      Raw r = {};
+      if (on) r = at[p];
+      values(r, x);
+      f(p, on, x);
+    }
+    if (full != pieces && wave == full % kLpThreads / kWave) {
+      const bool on = threadIdx.x == full % kLpThreads;
+      if (on) short_piece(x);
+      f(full, on, x);
     }
   };
 
-  Stats t = {kLowest, 0.f, 0.f};
+  // mc: a lane's maximum times c, rounded.  A weight's exponent is x c - mc with one
+  // rounding: what mc's rounding moved it by is the same for all, and comes off below
+  float mc = kLowestC, sum = 0.f, weighted = 0.f;
   float most = -INFINITY;  // the lane's largest
-  for (uint32_t p = threadIdx.x; p < pieces; p += kLpThreads) {
-    float x[8];
-    load(p, x);
-    const float pm = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    most = fmaxf(most, pm);
-    if (__any((pm - t.m) * a.c > kGrow)) t.move(fmaxf(t.m, pm), a.c);
+  walk([&](uint32_t, bool on, const float (&x)[8]) {
+    if (!on) return;
+    const float pm = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max3(x[6], x[7], x[7]));
+    most = max3(most, pm, pm);
+    if (__any(fmaf(pm, a.c, -mc) > kGrow)) {
+      const float to = fminf(fmaxf(mc, pm * a.c), -kLowestC), d = mc - to, f = __builtin_amdgcn_exp2f(d);
+      weighted = f * fmaf(sum, fmaxf(d, kNoWeight), weighted);
+      sum *= f;
+      mc = to;
+    }
     float s = 0.f, w = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float d = (x[j] - t.m) * a.c, e = __builtin_amdgcn_exp2f(d);
+      const float d = fmaf(x[j], a.c, -mc), e = __builtin_amdgcn_exp2f(d);
       s += e;
       w = fmaf(e, fmaxf(d, kNoWeight), w);
     }
-    t.s += s;
-    t.a += w;
-  }
+    sum += s;
+    weighted += w;
+  });
   // the workgroup's statistics, relative to its largest logit
   {
-    float m = fmaxf(most, kLowest), g = most;
-    for (int x = 32; x; x /= 2) {
-      m = fmaxf(m, lane_xor(m, x));
-      if (x < 8) g = fmaxf(g, lane_xor(g, x));
-    }
+    float g = most;
+    for (int x = 1; x < 8; x *= 2) g = fmaxf(g, lane_xor(g, x));
     if (lane % 8 == 0) groups[wave * 8 + lane / 8] = g;
-    t.move(m, a.c);
-    t.s = wave_sum(t.s);
-    t.a = wave_sum(t.a);
-    if (lane == 0) waves[wave] = t;
   }
   __syncthreads();
-  float m = kLowest;
-#pragma unroll
-  for (int w = 0; w < kLpWaves; ++w) m = fmaxf(m, waves[w].m);
-  t = Stats{m, 0.f, 0.f};
+  float largest = groups[lane];
+  for (int x = 32; x; x /= 2) largest = fmaxf(largest, lane_xor(largest, x));
+  Stats t = {fmaxf(largest, kLowest), 0.f, 0.f};
+  const float top = t.m * a.c;
+  if (fabsf(top) <= kFar || largest == -INFINITY) {
+    const float to = largest == -INFINITY ? mc : top;  // then all sums are 0
+    const float d = mc - to, f = __builtin_amdgcn_exp2f(d);
+    t.a = f * fmaf(sum, fmaxf(d, kNoWeight), weighted);
+    t.s = sum * f;
+  } else {
+    // a maximum whose product with c is too coarse: differences first
+#pragma unroll 1
+    for (uint32_t v = threadIdx.x; v < n; v += kLpThreads) {
+      const float d = (logit<F32>(a, row, v0 + v) - t.m) * a.c, e = __builtin_amdgcn_exp2f(d);
+      t.s += e;
+      t.a = fmaf(e, fmaxf(d, kNoWeight), t.a);
+    }
+  }
+  t.s = wave_sum(t.s);
+  t.a = wave_sum(t.a);
+  if (lane == 0) waves[wave] = t;
+  __syncthreads();
+  t.s = t.a = 0.f;
 #pragma unroll
   for (int w = 0; w < kLpWaves; ++w) {
-    Stats x = waves[w];
-    x.move(m, a.c);
-    t.s += x.s;
-    t.a += x.a;
+    t.s += waves[w].s;
+    t.a += waves[w].a;
+  }
+  if (fabsf(top) <= kFar) {
+    const float off = fmaf(t.m, a.c, -top), f = __builtin_amdgcn_exp2f(-off);
+    t.a = f * fmaf(t.s, -off, t.a);
+    t.s *= f;
   }
   const RowOut out(t);
   const bool whole = a.split == 1;
@@ -402,63 +453,80 @@ __global__ __launch_bounds__(kLpThreads) void k_logprobs(const LogprobsArgs a) {
     }
   };
   const bool odd = !(t.s < INFINITY);  // NaN or +infinity among them
-  if (!odd) {
-    const float bound = kth_of_wave(groups[lane], k);
-    const bool mine = most >= bound;
-    uint32_t equal = 0;  // of the wavefront so far
-    if (__any(mine))
-      for (uint32_t p0 = wave * kWave; p0 < pieces; p0 += kLpThreads) {
-        const uint32_t p = p0 + lane;
-        float x[8];
-        uint32_t above = 0, same = 0;
-        if (mine && p < pieces) {
-          load(p, x);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const bool here = 8 * p + j < n;
-            above |= (here && x[j] > bound) << j;
-            same |= (here && x[j] == bound) << j;
-          }
-        }
-        if (!__any(above | same)) continue;
-        // of the equal ones those that are among the wavefront's k lowest
-        const uint32_t count = __popc(same);
-        uint32_t upto = count;
-        for (int d = 1; d < kWave; d *= 2) {
-          const uint32_t y = __shfl_up(upto, d, kWave);
-          if (static_cast<int>(lane) >= d) upto += y;
-        }
-        uint32_t before = equal + upto - count;
-        equal += __shfl(upto, kWave - 1, kWave);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const bool eq = same >> j & 1;
-          if ((above >> j & 1) || (eq && before < k)) {
-            const uint32_t i = atomicAdd(&n_found, 1u);
-            if (i < kLpFound) found[i] = key_of(x[j], v0 + 8 * p + j);
-          }
-          before += eq;
-        }
-      }
+  if (wave == 0) {
+    const float x = kth_of_wave(groups[lane], k);
+    if (lane == 0) shared_bound = x;
+  }
+  __syncthreads();
+  const float bound = shared_bound;
+  // The logits that reach the bound, then, where there are too many of them for LDS,
+  // those above it.  The lanes that have some are listed, and their pieces go round
+  // all lanes.
+  const uint32_t each = (pieces + kLpThreads - 1) / kLpThreads;  // pieces of a lane at most
+  for (uint32_t strict = 0; strict < 2 && !odd; ++strict) {
+    if (strict ? most > bound : most >= bound) lanes[atomicAdd(&n_lanes, 1u)] = static_cast<uint16_t>(threadIdx.x);
     __syncthreads();
-    if (n_found <= kLpFound) {
-      rank_keys(found, n_found, k, kLpThreads, put);
-      // a last part with fewer logits than k
-      for (uint32_t r = n_found + threadIdx.x; r < k; r += kLpThreads) put(r, 0);
-      return;
+    const uint32_t listed = n_lanes;
+    if (strict || listed <= kLpThreads / 2)  // more: most logits are equal
+      for (uint32_t i = threadIdx.x; i < listed * each; i += kLpThreads) {
+        const uint32_t p = lanes[i / each] + i % each * kLpThreads;
+        if (p >= pieces || *const_cast<volatile uint32_t*>(&n_found) > kLpFound) continue;
+        float x[8];
+        if (p < full)
+          values(reinterpret_cast<const Raw*>(base)[p], x);
+        else
+          short_piece(x);
+        uint32_t hits = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) hits |= ((strict ? x[j] > bound : x[j] >= bound) && 8 * p + j < n ? 1u : 0u) << j;
+        if (!hits) continue;
+        uint32_t at = atomicAdd(&n_found, static_cast<uint32_t>(__popc(hits)));
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (hits >> j & 1) {
+            if (at < kLpFound) found[at] = key_of(x[j], v0 + 8 * p + j);
+            ++at;
+          }
+      }
+    else if (threadIdx.x == 0)
+      n_found = kLpFound + 1;
+    __syncthreads();
+    uint32_t have = n_found;
+    if (have > kLpFound) {
+      __syncthreads();  // n_found and the list are read
+      if (threadIdx.x == 0) n_found = n_lanes = 0;
+      __syncthreads();
+      continue;
     }
+    // those equal to the bound, from the lowest index on, until there are k
+#pragma unroll 1
+    for (uint32_t v = 0; strict && have < k && v < n; v += kLpThreads) {
+      const uint32_t index = v0 + v + threadIdx.x;
+      const bool hit = index < v1 && logit<F32>(a, row, index) == bound;
+      const uint64_t which = __ballot(hit);
+      if (lane == 0) counts[wave] = __popcll(which);
+      __syncthreads();
+      uint32_t at = have + __popcll(which & ((uint64_t{1} << lane) - 1));
+      for (uint32_t w = 0; w < kLpWaves; ++w) {
+        if (w < wave) at += counts[w];
+        have += counts[w];
+      }
+      if (hit && at < k) found[at] = key_of(bound, index);
+      __syncthreads();
+    }
+    have = strict ? min(have, max(k, n_found)) : have;
+    rank_keys(found, have, k, kLpThreads, put);
+    // a last part with fewer logits than k
+    for (uint32_t r = have + threadIdx.x; r < k; r += kLpThreads) put(r, 0);
+    return;
   }
   uint64_t last = ~uint64_t{0};
   for (uint32_t r = 0; r < k; ++r) {
     uint64_t top = 0;
-    for (uint32_t p = threadIdx.x; p < pieces; p += kLpThreads) {
-      float x[8];
-      load(p, x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint64_t key = 8 * p + j < n ? key_of(x[j], v0 + 8 * p + j) : 0;
-        if (key < last && key > top) top = key;
-      }
+#pragma unroll 1
+    for (uint32_t v = v0 + threadIdx.x; v < v1; v += kLpThreads) {
+      const uint64_t key = key_of(logit<F32>(a, row, v), v);
+      if (key < last && key > top) top = key;
     }
     for (int x = 32; x; x /= 2) {
       const uint64_t y = __shfl_xor(top, x, kWave);
@@ -473,51 +541,55 @@ __global__ __launch_bounds__(kLpThreads) void k_logprobs(const LogprobsArgs a) {
   }
 }
 
-// The parts of a row, a workgroup each.  The first few of every part's sorted
-// keys, 64 or more together, give the bound.
+// The parts of a row, a workgroup each: all that they left is asked for at once.  The
+// first few of every part's sorted keys, 64 or more together, give the bound.
+constexpr int kJoinThreads = 256;
 template <bool F32>
-__global__ __launch_bounds__(256) void k_logprobs_join(const LogprobsArgs a) {
-  __shared__ uint64_t heads[2 * kWave];
-  __shared__ uint64_t found[kLpMaxSplit * kLpMaxK];
+__global__ __launch_bounds__(kJoinThreads) void k_logprobs_join(const LogprobsArgs a) {
+  __shared__ uint64_t keys[kLpMaxSplit * kLpMaxK], heads[2 * kWave];
   __shared__ uint64_t bound;
   __shared__ uint32_t n_found;
+  __shared__ uint64_t found[kLpMaxSplit * kLpMaxK];
   const uint64_t row = blockIdx.x;
-  const float* st = a.stats + 4 * row * a.split;
+  const uint32_t k = a.k, lane = __lane_id();
+  const uint64_t* tops = a.tops + row * a.split * k;
+  const f32x4_t* st = reinterpret_cast<const f32x4_t*>(a.stats) + row * a.split;
   if (threadIdx.x == 0) {
     n_found = 0;
     bound = 0;
   }
-  Stats t = {kLowest, 0.f, 0.f};
-  for (uint32_t i = 0; i < a.split; ++i) t.m = fmaxf(t.m, st[4 * i]);
-  for (uint32_t i = 0; i < a.split; ++i) {
-    Stats x = {st[4 * i], st[4 * i + 1], st[4 * i + 2]};
-    x.move(t.m, a.c);
-    t.s += x.s;
-    t.a += x.a;
-  }
+  f32x4_t part = {kLowest, 0.f, 0.f, 0.f};
+  if (lane < a.split) part = st[lane];  // a lane each
+#pragma unroll 4
+  for (uint32_t i = threadIdx.x; i < a.split * k; i += kJoinThreads) keys[i] = tops[i];
+  Stats t = {part[0], part[1], part[2]};
+  float m = t.m;
+  for (int x = 32; x; x /= 2) m = fmaxf(m, lane_xor(m, x));
+  t.move(m, a.c);
+  t.s = wave_sum(t.s);
+  t.a = wave_sum(t.a);
   const RowOut out(t);
-  store_targets<F32>(a, row, out, blockDim.x);
+  store_targets<F32>(a, row, out, kJoinThreads);
   if (threadIdx.x == 0 && a.entropy) a.entropy[row] = out.none ? 0.f : fmaf(-0.69314718055994530942f, t.a / t.s, out.log_s);
-  const uint32_t k = a.k;
   if (k == 0) return;
-  const uint64_t* keys = a.tops + row * a.split * k;
+  __syncthreads();
   const uint32_t each = min(k, (kWave + a.split - 1) / a.split), n_heads = each * a.split;  // at most 64 + split - 1
-  for (uint32_t i = threadIdx.x; i < n_heads; i += blockDim.x) heads[i] = keys[i / each * k + i % each];
+  for (uint32_t i = threadIdx.x; i < n_heads; i += kJoinThreads) heads[i] = keys[i / each * k + i % each];
   __syncthreads();
   // fewer heads than k: no bound
-  for (uint32_t i = threadIdx.x; i < n_heads; i += blockDim.x) {
+  for (uint32_t i = threadIdx.x; i < n_heads; i += kJoinThreads) {
     uint32_t rank = 0;
     for (uint32_t j = 0; j < n_heads; ++j) rank += heads[j] > heads[i] || (heads[j] == heads[i] && j < i);
     if (rank == k - 1) bound = heads[i];
   }
   __syncthreads();
   const uint64_t least = max(bound, uint64_t{1});  // a key of 0 is none
-  for (uint32_t i = threadIdx.x; i < a.split * k; i += blockDim.x) {
+  for (uint32_t i = threadIdx.x; i < a.split * k; i += kJoinThreads) {
     const uint64_t key = keys[i];
     if (key >= least) found[atomicAdd(&n_found, 1u)] = key;
   }
   __syncthreads();
-  rank_keys(found, n_found, k, blockDim.x, [&](uint32_t rank, uint64_t key) {
+  rank_keys(found, n_found, k, kJoinThreads, [&](uint32_t rank, uint64_t key) {
     a.top_ids[row * k + rank] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
     a.top_logprobs[row * k + rank] = out.logprob(value_of(static_cast<uint32_t>(key >> 32)), a.scale);
   });
@@ -642,8 +714,8 @@ nwc_status nwc_token_logprobs(const void* logits_dev, uint64_t ld, nwc_out_type 
   const dim3 grid(rows * L.split), block(kLpThreads);
   const nwc_status first = type == NWC_OUT_F32 ? launch(k_logprobs<true>, grid, block, 0, s, a) : launch(k_logprobs<false>, grid, block, 0, s, a);
   if (first || L.split == 1) return first;
-  return type == NWC_OUT_F32 ? launch(k_logprobs_join<true>, dim3(rows), dim3(256), 0, s, a)
-                             : launch(k_logprobs_join<false>, dim3(rows), dim3(256), 0, s, a);
+  return type == NWC_OUT_F32 ? launch(k_logprobs_join<true>, dim3(rows), dim3(kJoinThreads), 0, s, a)
+                             : launch(k_logprobs_join<false>, dim3(rows), dim3(kJoinThreads), 0, s, a);
 }
 
 }  // extern "C"
