@@ -106,12 +106,13 @@ struct Item {
   uint32_t head, row, block;
 };
 
-// The positions of all rows before each row, in LDS: pre[rows + 1]; carry: 4 more.
+// The positions of all rows before each row, in LDS: pre[rows + 1]; carry: W more.
+template <int W>
 __device__ __forceinline__ void make_prefix(const ChunkArgs& a, uint64_t* pre, uint64_t* carry) {
   const uint32_t rows = a.pages.rows, tid = threadIdx.x, lane = __lane_id(), wave = uniform(tid / kWave);
   uint64_t sum = 0;
   if (tid == 0) pre[0] = 0;
-  for (uint32_t base = 0; base < rows; base += kChunkThreads) {
+  for (uint32_t base = 0; base < rows; base += W * kWave) {
     const uint32_t r = base + tid;
     uint64_t x = 0;
     if (r < rows) {
@@ -135,11 +136,11 @@ __device__ __forceinline__ void make_prefix(const ChunkArgs& a, uint64_t* pre, u
     }
     if (lane == kWave - 1) carry[wave] = x;
     __syncthreads();
-    for (uint32_t w = 0; w < 4; ++w) {
+    for (uint32_t w = 0; w < W; ++w) {
       if (w < wave) x += carry[w];
     }
     if (r < rows) pre[r + 1] = sum + x;
-    for (uint32_t w = 0; w < 4; ++w) sum += carry[w];
+    for (uint32_t w = 0; w < W; ++w) sum += carry[w];
     __syncthreads();
   }
 }
@@ -252,20 +253,22 @@ __device__ void redo(const ChunkArgs& a, uint32_t row, uint32_t token, uint32_t 
   }
 }
 
-template <int D>
+template <int D, int W>
 struct ChunkShape {
   static constexpr int kKs = D / 16;   // steps of the K Q^T product
   static constexpr int kDt = D / 32;   // 32-row tiles of O^T
-  static constexpr int kNt = 1;            // 32-column tiles of a wavefront
-  static constexpr uint32_t kUnit = D <= 128 ? 64 : 32;   // positions of a unit
+  static constexpr uint32_t kCols = 32 * W;               // columns of an item
+  static constexpr uint32_t kUnit = D <= 128 ? 64 : 32;  // positions of a unit
   static constexpr int kKt = kUnit / 32;                  // 32-position tiles of it
-  static constexpr uint32_t kCols = 4 * 32 * kNt;         // columns of an item
   static constexpr uint32_t kTile = kUnit * D * 2;        // bytes of a unit's keys or values
-  static constexpr int kRing = D <= 64 ? 3 : D <= 128 ? 2 : D <= 192 ? 3 : 4;                         // units of each in LDS
+  static constexpr int kRing = W == 8 ? 4 : D <= 64 ? 3 : D <= 128 ? 2 : D <= 192 ? 3 : 4;  // units of each in LDS
   static constexpr uint32_t kLds = 2 * kRing * kTile;
-  static constexpr int kWgs = D <= 96 ? 3 : D <= 192 ? 2 : 1;           // workgroups of a compute unit
-  static constexpr int kRows = kUnit / 4;                 // rows of a tile that a wavefront loads
+  static constexpr int kLag = W == 8;                     // turns that the slower half is behind
+  static constexpr int kAhead = kRing - 1 - kLag;         // units asked for before their turn
+  static constexpr int kWgs = W == 8 ? 1 : D <= 96 ? 3 : D <= 192 ? 2 : 1;  // workgroups of a compute unit
+  static constexpr int kRows = kUnit / W;                 // rows of a tile that a wavefront loads
   static constexpr int kLoads = kRows * D * 2 / 1024;     // and its loads for them
+  static_assert(kRows * D * 2 % 1024 == 0 && 16 % kRows == 0 && kAhead > 0, "rows of a wavefront");
 };
 
 // 16 bytes a lane from base + off (bytes) to 1024 bytes of LDS.  In assembly, since
@@ -275,12 +278,12 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t off, uint32_
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
 }
 
-template <int D>
+template <int D, int W>
 __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, const RowPart& p, uint32_t u0, uint32_t u1, uint32_t part,
                                          uint8_t* lds) {
-  using S = ChunkShape<D>;
+  using S = ChunkShape<D, W>;
   constexpr uint32_t kPieces = D / 8, kUnit = S::kUnit;
-  constexpr int kNt = S::kNt, kKt = S::kKt, kKs = S::kKs, kDt = S::kDt;
+  constexpr int kNt = 1, kKt = S::kKt, kKs = S::kKs, kDt = S::kDt;
   const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave), n = lane % 32, g = lane / 32;
   const uint32_t sees = p.sees(it.block, a.tb), units = (sees + kUnit - 1) / kUnit;
   const uint32_t tok0 = it.block * a.tb;
@@ -466,7 +469,7 @@ __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, con
   };
   __syncthreads();  // the ring is free (the plan or the item before lay there)
 #pragma unroll
-  for (uint32_t i = 0; i < S::kRing - 1; ++i)
+  for (uint32_t i = 0; i < S::kAhead; ++i)
     if (u0 + i < u1) issue(u0 + i, ring + i * (2 * S::kTile));
   // pages that do not exist are looked for once
   for (uint32_t at = kUnit * u0 >> a.pages.shift, end = (min(kUnit * u1, sees) - 1) >> a.pages.shift; at <= end; at += kWave)
@@ -477,22 +480,38 @@ __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, con
   for (int c = 0; c < kNt; ++c)
 #pragma unroll
     for (int k = 0; k < kKs; ++k) asm volatile("" : "+v"(qf[c][k]));
-  uint32_t place = ring;  // of unit u
-  for (uint32_t u = u0; u < u1; ++u) {
-    if (u + S::kRing - 2 < u1)
-      wait_vmem<2 * S::kLoads*(S::kRing - 2)>();
+  // Of 8 wavefronts those that share a SIMD with an earlier one are a barrier, half a
+  // turn, behind: one's first product runs beside the other's weights.
+  const bool behind = W == 8 && wave >= 4;
+  constexpr uint32_t kGroup = 2 * S::kTile, kEnd = S::kRing * kGroup;
+  auto arrived = [&](uint32_t u) {  // the wavefront's rows of unit u, kAhead of which are on their way at most
+    if (u + S::kAhead - 1 < u1)
+      wait_vmem<2 * S::kLoads*(S::kAhead - 1)>();
     else
       wait_vmem<0>();
+  };
+  uint32_t place = 0;  // of unit u in the ring
+  if (behind) {
+    arrived(u0);
     __syncthreads();
-    if (u + S::kRing - 1 < u1) issue(u + S::kRing - 1, place == ring ? ring + (S::kRing - 1) * (2 * S::kTile) : place - 2 * S::kTile);
-    if (u < uw) {
-      f32x16_t sc[kKt][kNt];
-      scores(place, sc);
-      settle(u, sc);
-      weigh(place + S::kTile, sc);
-    }
-    place = place == ring + (S::kRing - 1) * (2 * S::kTile) ? ring : place + 2 * S::kTile;
   }
+  for (uint32_t u = u0; u < u1; ++u) {
+    if (!behind) arrived(u);
+    __syncthreads();
+    if (u + S::kAhead < u1) issue(u + S::kAhead, ring + (place + S::kAhead * kGroup) % kEnd);
+    f32x16_t sc[kKt][kNt];
+    if (u < uw) {
+      scores(ring + place, sc);
+      settle(u, sc);
+    }
+    if constexpr (W == 8) {
+      if (behind && u + 1 < u1) arrived(u + 1);
+      __syncthreads();
+    }
+    if (u < uw) weigh(ring + place + S::kTile, sc);
+    place = (place + kGroup) % kEnd;
+  }
+  if (W == 8 && !behind) __syncthreads();
   if (!works) return;
   const bool direct = u0 == 0 && u1 == units;
 #pragma unroll
@@ -543,18 +562,18 @@ __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, con
 // on one XCD (blocks go round the 8 of them).
 __device__ __forceinline__ uint32_t worker_of(uint32_t block, uint32_t workers) { return block % 8 * (workers / 8) + block / 8; }
 
-template <int D>
-__global__ __launch_bounds__(kChunkThreads, ChunkShape<D>::kWgs) void k_chunk(const ChunkArgs a) {
+template <int D, int W>
+__global__ __launch_bounds__(W * kWave, (ChunkShape<D, W>::kWgs * W / 4)) void k_chunk(const ChunkArgs a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];  // from LDS address 0 on: there is no other
   uint64_t* pre = reinterpret_cast<uint64_t*>(lds);  // until the first tile arrives
   const uint32_t rows = a.pages.rows;
-  constexpr uint32_t kUnit = ChunkShape<D>::kUnit;
-  make_prefix(a, pre, pre + rows + 1);
+  constexpr uint32_t kUnit = ChunkShape<D, W>::kUnit;
+  make_prefix<W>(a, pre, pre + rows + 1);
   // tokens that see nothing
   for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const RowPart p(a, r);
     const uint32_t per = a.hq * (D / 8);
-    for (uint64_t i = threadIdx.x; i < static_cast<uint64_t>(p.skipped) * per; i += kChunkThreads)
+    for (uint64_t i = threadIdx.x; i < static_cast<uint64_t>(p.skipped) * per; i += W * kWave)
       *reinterpret_cast<u32x4_t*>(a.out + (p.t0 - p.skipped + i / per) * a.ldo + i % per * 8) = u32x4_t{0, 0, 0, 0};
   }
   const uint64_t total = uniform64(pre[rows]) * a.hkv, quota = quota_of(a, total);
@@ -573,7 +592,7 @@ __global__ __launch_bounds__(kChunkThreads, ChunkShape<D>::kWgs) void k_chunk(co
         const uint32_t tok0 = it.block * a.tb;
         cut = Cut{static_cast<uint32_t>(last / quota) - w, it.head, min(a.tb, p.n - tok0) * a.ratio, p.t0 + tok0, p.base + tok0 + 1, it.row, w, 0};
       }
-      if (u0 < u1) run_item<D>(a, it, p, u0, u1, 2 * w + (x0 > it.at ? 0 : 1), lds);
+      if (u0 < u1) run_item<D, W>(a, it, p, u0, u1, 2 * w + (x0 > it.at ? 0 : 1), lds);
       it.at += sees + kItemCost;
       if (it.at >= x1) break;
       if (++it.block == p.blocks(a.tb)) {
@@ -745,13 +764,15 @@ __global__ __launch_bounds__(kChunkThreads) void k_chunk_join(const ChunkArgs a)
 constexpr uint32_t kChunkMaxRows = 4096, kChunkMaxTokens = 1u << 22, kChunkMaxRatio = 64, kChunkMaxLen = 1u << 22;
 
 struct ChunkLayout {
-  uint32_t workers, tb, cap;
+  uint32_t waves, workers, tb, cap;
   uint64_t ml, cuts, bytes;
 };
-ChunkLayout chunk_layout(uint32_t tokens, uint32_t ratio, uint32_t d) {
+ChunkLayout chunk_layout(uint32_t rows, uint32_t tokens, uint32_t ratio, uint32_t d) {
   ChunkLayout L;
-  L.workers = kCus * (d <= 96 ? 3 : d <= 192 ? 2 : 1);  // ChunkShape's workgroups
-  L.tb = 128 / ratio;                                   // ChunkShape's columns
+  const bool wide = (d == 64 || d == 128) && static_cast<uint64_t>(tokens) * ratio >= 192ull * rows;
+  L.waves = wide ? 8 : 4;
+  L.workers = kCus * (wide ? 1 : d <= 96 ? 3 : d <= 192 ? 2 : 1);  // ChunkShape's workgroups
+  L.tb = 32 * L.waves / ratio;
   L.cap = std::min(tokens, L.tb) * ratio;
   const uint64_t slots = 2ull * L.workers * L.cap;
   auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
@@ -771,13 +792,14 @@ nwc_status chunk_shape(const nwc_cache* c, uint32_t rows, uint32_t tokens, uint3
   return NWC_OK;
 }
 
-template <int D>
+template <int D, int W>
 nwc_status launch_chunk(const ChunkArgs& a, hipStream_t s) {
-  if (a.tb != ChunkShape<D>::kCols / a.ratio) return NWC_ERR_UNSUPPORTED;  // never: the layout's columns are the kernel's
-  constexpr size_t lds = std::max<size_t>(ChunkShape<D>::kLds, (kChunkMaxRows + 5) * 8);
+  using S = ChunkShape<D, W>;
+  constexpr size_t lds = std::max<size_t>(S::kLds, (kChunkMaxRows + 1 + W) * 8);
   static_assert(lds <= kMaxLds, "LDS");
-  if (lds > 65536 && !allow_lds<k_chunk<D>, lds>()) return NWC_ERR_HIP;
-  const nwc_status st = launch(k_chunk<D>, dim3(a.workers), dim3(kChunkThreads), lds, s, a);
+  if (a.tb != S::kCols / a.ratio) return NWC_ERR_UNSUPPORTED;  // never: the layout's columns are the kernel's
+  if (lds > 65536 && !allow_lds<k_chunk<D, W>, lds>()) return NWC_ERR_HIP;
+  const nwc_status st = launch(k_chunk<D, W>, dim3(a.workers), dim3(W * kWave), lds, s, a);
   if (st) return st;
   const uint32_t groups = (a.cap + kJoinCols - 1) / kJoinCols;
   return launch(k_chunk_join<D>, dim3(std::min(kJoinGroups, a.workers * groups)), dim3(kChunkThreads), 0, s, a);
@@ -791,7 +813,7 @@ nwc_status nwc_attend_chunk_workspace_size(const nwc_cache* cache, uint32_t rows
   if (!bytes) return NWC_ERR_INVALID_ARG;
   const nwc_status st = chunk_shape(cache, rows, tokens, q_heads);
   if (st) return st;
-  *bytes = chunk_layout(tokens, q_heads / cache->kv_heads, cache->head_dim).bytes;
+  *bytes = chunk_layout(rows, tokens, q_heads / cache->kv_heads, cache->head_dim).bytes;
   return NWC_OK;
 }
 
@@ -812,7 +834,7 @@ nwc_status nwc_attend_chunk(const nwc_cache* cache, const nwc_page_table* table,
       !aligned(ws, 256))
     return NWC_ERR_ALIGNMENT;
   a.ratio = q_heads / cache->kv_heads;
-  const ChunkLayout L = chunk_layout(tokens, a.ratio, d);
+  const ChunkLayout L = chunk_layout(table->rows, tokens, a.ratio, d);
   if (ws_bytes < L.bytes) return NWC_ERR_BUFFER_TOO_SMALL;
   if (out_dev == q_dev) return NWC_ERR_INVALID_ARG;  // workgroups read queries that others have answered
   uint8_t* w = static_cast<uint8_t*>(ws);
@@ -840,11 +862,11 @@ nwc_status nwc_attend_chunk(const nwc_cache* cache, const nwc_page_table* table,
   a.cuts = reinterpret_cast<Cut*>(w + L.cuts);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (d) {
-    case 64: return launch_chunk<64>(a, s);
-    case 96: return launch_chunk<96>(a, s);
-    case 128: return launch_chunk<128>(a, s);
-    case 192: return launch_chunk<192>(a, s);
-    default: return launch_chunk<256>(a, s);
+    case 64: return L.waves == 8 ? launch_chunk<64, 8>(a, s) : launch_chunk<64, 4>(a, s);
+    case 96: return launch_chunk<96, 4>(a, s);
+    case 128: return L.waves == 8 ? launch_chunk<128, 8>(a, s) : launch_chunk<128, 4>(a, s);
+    case 192: return launch_chunk<192, 4>(a, s);
+    default: return launch_chunk<256, 4>(a, s);
   }
 }
 
