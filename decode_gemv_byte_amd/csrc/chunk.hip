@@ -13,7 +13,6 @@
 
 namespace {
 
-typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4_t;
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 
@@ -65,7 +64,7 @@ struct ChunkArgs {
   uint32_t tb;       // tokens of an item
   uint32_t cap;      // column slots of a part
   uint32_t workers;  // workgroups that positions are cut for
-  float scale, scale2;  // scale * log2(e)
+  float scale2;      // scale * log2(e)
   float* part_o;     // workspace: means over a part of a column's positions [part][column][D]
   float* part_ml;    // their scaled maxima and weight sums
   Cut* cuts;         // one for each worker
@@ -93,10 +92,6 @@ struct RowPart {
   __device__ uint32_t sees(uint32_t b, uint32_t tb) const { return base + min(n, (b + 1) * tb); }
   __device__ uint64_t before(uint32_t b, uint32_t tb) const {
     return static_cast<uint64_t>(b) * (base + kItemCost) + static_cast<uint64_t>(tb) * (static_cast<uint64_t>(b) * (b + 1) / 2);
-  }
-  __device__ uint64_t all(uint32_t tb) const {
-    const uint32_t nb = blocks(tb);
-    return nb ? before(nb - 1, tb) + sees(nb - 1, tb) + kItemCost : 0;
   }
 };
 
@@ -261,11 +256,11 @@ struct ChunkShape {
   static constexpr uint32_t kUnit = D <= 128 ? 64 : 32;  // positions of a unit
   static constexpr int kKt = kUnit / 32;                  // 32-position tiles of it
   static constexpr uint32_t kTile = kUnit * D * 2;        // bytes of a unit's keys or values
-  static constexpr int kRing = W == 8 ? 4 : D <= 64 ? 3 : D <= 128 ? 2 : D <= 192 ? 3 : 4;  // units of each in LDS
+  static constexpr int kRing = W == 8 ? 4 : D <= 96 ? 3 : D <= 128 ? 2 : D <= 192 ? 3 : 4;  // units of each in LDS
   static constexpr uint32_t kLds = 2 * kRing * kTile;
   static constexpr int kLag = W == 8;                     // turns that the slower half is behind
   static constexpr int kAhead = kRing - 1 - kLag;         // units asked for before their turn
-  static constexpr int kWgs = W == 8 ? 1 : D <= 96 ? 3 : D <= 192 ? 2 : 1;  // workgroups of a compute unit
+  static constexpr int kWgs = W == 8 ? 1 : D <= 64 ? 3 : D <= 192 ? 2 : 1;  // workgroups of a compute unit
   static constexpr int kRows = kUnit / W;                 // rows of a tile that a wavefront loads
   static constexpr int kLoads = kRows * D * 2 / 1024;     // and its loads for them
   static_assert(kRows * D * 2 % 1024 == 0 && 16 % kRows == 0 && kAhead > 0, "rows of a wavefront");
@@ -275,7 +270,9 @@ struct ChunkShape {
 // the compiler lets every transposing LDS read wait for all of them; nothing is
 // returned to registers, and wait_vmem counts them.
 __device__ __forceinline__ void load_lds(const void* base, uint32_t off, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
+  // five wait states: base may come from a vector instruction, as a scalar register
+  // restored from a lane does
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
 }
 
 template <int D, int W>
@@ -283,48 +280,40 @@ __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, con
                                          uint8_t* lds) {
   using S = ChunkShape<D, W>;
   constexpr uint32_t kPieces = D / 8, kUnit = S::kUnit;
-  constexpr int kNt = 1, kKt = S::kKt, kKs = S::kKs, kDt = S::kDt;
+  constexpr int kKt = S::kKt, kKs = S::kKs, kDt = S::kDt;
   const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x / kWave), n = lane % 32, g = lane / 32;
   const uint32_t sees = p.sees(it.block, a.tb), units = (sees + kUnit - 1) / kUnit;
   const uint32_t tok0 = it.block * a.tb;
   const uint32_t cols = min(a.tb, p.n - tok0) * a.ratio;
   const int32_t* ids = a.pages.ids + static_cast<uint64_t>(it.row) * a.pages.ld;
   // the wavefront's columns and what they see: all of them, and any
-  const uint32_t col0 = 32 * kNt * wave;
-  const bool works = col0 < cols, full = col0 + 32 * kNt <= cols;
+  const uint32_t col0 = 32 * wave;
+  const bool works = col0 < cols, full = col0 + 32 <= cols;
   const uint32_t all_see = full ? p.base + tok0 + col0 / a.ratio + 1 : 0;
-  const uint32_t any_sees = works ? p.base + tok0 + (min(cols, col0 + 32 * kNt) - 1) / a.ratio + 1 : 0;
+  const uint32_t any_sees = works ? p.base + tok0 + (min(cols, col0 + 32) - 1) / a.ratio + 1 : 0;
   const uint32_t uw = min(u1, (any_sees + kUnit - 1) / kUnit);  // the wavefront's units end here
-  uint32_t reach[kNt];  // positions that the lane's columns see
+  // the lane's column
+  const uint32_t col = col0 + n, tok = tok0 + col / a.ratio, h = it.head * a.ratio + col % a.ratio;
+  const bool live = col < cols;
+  const uint32_t reach = live ? p.base + tok + 1 : 0;  // positions that it sees
 
-  u32x4_t qf[kNt][kKs];
+  u32x4_t qf[kKs];
+  const uint16_t* src = a.q + static_cast<uint64_t>(p.t0 + tok) * a.ldq + static_cast<uint64_t>(h) * D + 8 * g;
 #pragma unroll
-  for (int c = 0; c < kNt; ++c) {
-    const uint32_t col = col0 + 32 * c + n, tok = tok0 + col / a.ratio, h = it.head * a.ratio + col % a.ratio;
-    const bool live = col < cols;
-    reach[c] = live ? p.base + tok + 1 : 0;
-    const uint16_t* src = a.q + static_cast<uint64_t>(p.t0 + tok) * a.ldq + static_cast<uint64_t>(h) * D + 8 * g;
-#pragma unroll
-    for (int k = 0; k < kKs; ++k) {
-      qf[c][k] = u32x4_t{0, 0, 0, 0};
-      if (live) qf[c][k] = *reinterpret_cast<const u32x4_t*>(src + 16 * k);
-    }
+  for (int k = 0; k < kKs; ++k) {
+    qf[k] = u32x4_t{0, 0, 0, 0};
+    if (live) qf[k] = *reinterpret_cast<const u32x4_t*>(src + 16 * k);
   }
 
   bool missing = false;  // a page of the range that does not exist
-  bool far = false;      // a maximum of the lane's columns passed kFarMax
-  f32x16_t o[kNt][kDt];
-  float m[kNt], mc[kNt], l[kNt];
+  bool far = false;      // a maximum of the column passed kFarMax
+  f32x16_t o[kDt];
+  // the maximum so far, and times scale2, which weights are relative to; their sum
+  float m = kNoMax, mc = fmaxf(kNoMax * a.scale2, -kFinite), l = 0.f;
 #pragma unroll
-  for (int c = 0; c < kNt; ++c) {
-    m[c] = kNoMax;
-    mc[c] = fmaxf(kNoMax * a.scale2, -kFinite);
-    l[c] = 0.f;
+  for (int d = 0; d < kDt; ++d)
 #pragma unroll
-    for (int d = 0; d < kDt; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[c][d][i] = 0.f;
-  }
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
 
   typedef __attribute__((address_space(3))) uint8_t lds1;
   typedef const __attribute__((address_space(3))) u32x4_t lds16;
@@ -372,27 +361,36 @@ __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, con
   // components of the position that its place among 16 names
   const uint32_t vr = 4 * g + (lane % 16) / 4;
   const uint32_t value_at = 16 * (vr * kPieces + ((n / 16 * 2 + lane % 4 / 2) ^ value_swap<D>(vr))) + 8 * (lane % 2);
-  auto scores = [&](uint32_t kt, f32x16_t (&sc)[kKt][kNt]) {
+  auto scores = [&](uint32_t kt, f32x16_t (&sc)[kKt]) {
     const uint32_t at = kt + key_at;
+    constexpr int kReads = kKt * kKs, kHeld = kReads < (D == 192 ? 3 : 6) ? kReads : D == 192 ? 3 : 6;
+    u32x4_t kf[kReads];
+    auto read = [&](int i) {
+      const int k = i / kKt, t = i % kKt;
+      kf[i] = *((lds16*)static_cast<uintptr_t>((at ^ (k % kKx * 32)) + (32 * t * D * 2 + k / kKx * (kKx * 32))));
+    };
+    // kHeld keys on their way from LDS before the first product, one more with each: left
+    // alone, the compiler waits for every key by itself
 #pragma unroll
-    for (int t = 0; t < kKt; ++t) {
+    for (int i = 0; i < kHeld; ++i) read(i);
 #pragma unroll
-      for (int c = 0; c < kNt; ++c)
+    for (int t = 0; t < kKt; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sc[t][c][i] = 0.f;
+      for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int k = 0; k < kKs; ++k) {
-        const u32x4_t kf = *((lds16*)static_cast<uintptr_t>((at ^ (k % kKx * 32)) + (32 * t * D * 2 + k / kKx * (kKx * 32))));
-#pragma unroll
-        for (int c = 0; c < kNt; ++c)
-          sc[t][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, kf), __builtin_bit_cast(bf16x8_t, qf[c][k]),
-                                                             sc[t][c], 0, 0, 0);
+    for (int i = 0; i < kReads; ++i) {
+      sc[i % kKt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, kf[i]),
+                                                            __builtin_bit_cast(bf16x8_t, qf[i / kKt]), sc[i % kKt], 0, 0, 0);
+      if (i + kHeld < kReads) {
+        read(i + kHeld);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
   // scores of unit u that are not seen, and the maximum, which weights are relative
   // to: it moves where a score outgrows it by 2^11
-  auto settle = [&](uint32_t u, f32x16_t (&sc)[kKt][kNt]) {
+  auto settle = [&](uint32_t u, f32x16_t (&sc)[kKt]) {
     if (kUnit * (u + 1) > all_see || missing) {
       uint32_t known = 0;
 #pragma unroll
@@ -403,70 +401,76 @@ __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, con
 #pragma unroll
       for (int t = 0; t < kKt; ++t)
 #pragma unroll
-        for (int c = 0; c < kNt; ++c)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t at = 32 * t + 8 * (i / 4) + 4 * g + i % 4;
-            if (kUnit * u + at >= reach[c] || !(known >> (2 * t + i / 8) & 1)) sc[t][c][i] = -INFINITY;
-          }
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t at = 32 * t + 8 * (i / 4) + 4 * g + i % 4;
+          if (kUnit * u + at >= reach || !(known >> (2 * t + i / 8) & 1)) sc[t][i] = -INFINITY;
+        }
     }
-    float x[kNt];
-    bool grown = false;
+    float x = sc[0][0];
 #pragma unroll
-    for (int c = 0; c < kNt; ++c) {
-      x[c] = sc[0][c][0];
+    for (int t = 0; t < kKt; ++t)
 #pragma unroll
-      for (int t = 0; t < kKt; ++t)
+      for (int i = 0; i < 16; ++i) x = fmaxf(x, sc[t][i]);
+    if (__any(fmaf(x, a.scale2, -mc) > 11.f)) {
+      m = fmaxf(m, fmaxf(x, lane_xor(x, 32)));
+      const float to = fminf(fmaxf(m * a.scale2, -kFinite), kFinite);
+      const float f = __builtin_amdgcn_exp2f(mc - to);
+      far |= !(fabsf(to) < kFarMax) && m != kNoMax;
+      mc = to;
+      l *= f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[c] = fmaxf(x[c], sc[t][c][i]);
-      grown |= fmaf(x[c], a.scale2, -mc[c]) > 11.f;
-    }
-    if (__any(grown)) {
-#pragma unroll
-      for (int c = 0; c < kNt; ++c) {
-        m[c] = fmaxf(m[c], fmaxf(x[c], lane_xor(x[c], 32)));
-        const float to = fminf(fmaxf(m[c] * a.scale2, -kFinite), kFinite);
-        const float f = __builtin_amdgcn_exp2f(mc[c] - to);
-        far |= !(fabsf(to) < kFarMax) && m[c] != kNoMax;
-        mc[c] = to;
-        l[c] *= f;
-#pragma unroll
-        for (int d = 0; d < kDt; ++d) o[c][d] *= f;
-      }
+      for (int d = 0; d < kDt; ++d) o[d] *= f;
     }
   };
   // the weights of 16 positions at a time, and their products with the values
-  auto weigh = [&](uint32_t vt, const f32x16_t (&sc)[kKt][kNt]) {
+  auto weigh = [&](uint32_t vt, const f32x16_t (&sc)[kKt]) {
     const uint32_t at = vt + value_at;
-#pragma unroll
-    for (int s = 0; s < 2 * kKt; ++s) {
-      u32x4_t pf[kNt];
-#pragma unroll
-      for (int c = 0; c < kNt; ++c) {
-        float sum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float x = __builtin_amdgcn_exp2f(fmaf(sc[s / 2][c][8 * (s % 2) + j], a.scale2, -mc[c]));
-          const float y = __builtin_amdgcn_exp2f(fmaf(sc[s / 2][c][8 * (s % 2) + j + 1], a.scale2, -mc[c]));
-          sum[0] += x;
-          sum[1] += y;
-          pf[c][j / 2] = pack_bf16(x, y);
-        }
-        l[c] += sum[0] + sum[1];
-      }
+    constexpr int kSteps = 2 * kKt, kSets = D == 192 ? 1 : 2;  // a second set of values there would spill
+    u32x2_t vf[kSets][kDt][2];
+    auto read = [&](int s) {
 #pragma unroll
       for (int d = 0; d < kDt; ++d) {
         const uint32_t to = (at ^ (d % kDx * 64)) + (16 * s * D * 2 + d / kDx * (kDx * 64));
-        const u32x2_t a0 = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds8*)static_cast<uintptr_t>(to)));
-        const u32x2_t a1 = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds8*)static_cast<uintptr_t>(to + 8 * D * 2)));
-        const u32x4_t vf = {a0[0], a0[1], a1[0], a1[1]};
-#pragma unroll
-        for (int c = 0; c < kNt; ++c)
-          o[c][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, vf), __builtin_bit_cast(bf16x8_t, pf[c]),
-                                                            o[c][d], 0, 0, 0);
+        vf[s % kSets][d][0] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds8*)static_cast<uintptr_t>(to)));
+        vf[s % kSets][d][1] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds8*)static_cast<uintptr_t>(to + 8 * D * 2)));
       }
+    };
+    float sum[2] = {0.f, 0.f};
+    u32x4_t pf[2];
+    auto two = [&](int s, int j) {  // weights 2 j and 2 j + 1 of step s
+      const float x = __builtin_amdgcn_exp2f(fmaf(sc[s / 2][8 * (s % 2) + 2 * j], a.scale2, -mc));
+      const float y = __builtin_amdgcn_exp2f(fmaf(sc[s / 2][8 * (s % 2) + 2 * j + 1], a.scale2, -mc));
+      sum[0] += x;
+      sum[1] += y;
+      pf[s % 2][j] = pack_bf16(x, y);
+    };
+    // the next step's values come from LDS, and its weights are made, beside the
+    // products of this one, in this order
+    read(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) two(0, j);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      if (kSets == 2 && s + 1 < kSteps) read(s + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int d = 0; d < kDt; ++d) {
+        const u32x4_t v = {vf[s % kSets][d][0][0], vf[s % kSets][d][0][1], vf[s % kSets][d][1][0], vf[s % kSets][d][1][1]};
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, pf[s % 2]), o[d],
+                                                       0, 0, 0);
+        if (s + 1 < kSteps) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j * kDt / 4 == d) two(s + 1, j);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if (kSets == 1 && s + 1 < kSteps) read(s + 1);
     }
+    l += sum[0] + sum[1];
   };
+
   __syncthreads();  // the ring is free (the plan or the item before lay there)
 #pragma unroll
   for (uint32_t i = 0; i < S::kAhead; ++i)
@@ -477,9 +481,7 @@ __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, con
   missing = __any(missing);
   // the queries have to be there before the loads in flight are counted
 #pragma unroll
-  for (int c = 0; c < kNt; ++c)
-#pragma unroll
-    for (int k = 0; k < kKs; ++k) asm volatile("" : "+v"(qf[c][k]));
+  for (int k = 0; k < kKs; ++k) asm volatile("" : "+v"(qf[k]));
   // Of 8 wavefronts those that share a SIMD with an earlier one are a barrier, half a
   // turn, behind: one's first product runs beside the other's weights.
   const bool behind = W == 8 && wave >= 4;
@@ -499,7 +501,7 @@ __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, con
     if (!behind) arrived(u);
     __syncthreads();
     if (u + S::kAhead < u1) issue(u + S::kAhead, ring + (place + S::kAhead * kGroup) % kEnd);
-    f32x16_t sc[kKt][kNt];
+    f32x16_t sc[kKt];
     if (u < uw) {
       scores(ring + place, sc);
       settle(u, sc);
@@ -514,47 +516,39 @@ __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, con
   if (W == 8 && !behind) __syncthreads();
   if (!works) return;
   const bool direct = u0 == 0 && u1 == units;
+  l += lane_xor(l, 32);
+  float zero = 0.f;
 #pragma unroll
-  for (int c = 0; c < kNt; ++c) {
-    const uint32_t col = col0 + 32 * c + n, tok = tok0 + col / a.ratio, h = it.head * a.ratio + col % a.ratio;
-    const bool live = col < cols;
-    l[c] += lane_xor(l[c], 32);
-    float zero = 0.f;
+  for (int d = 0; d < kDt; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) zero = fmaf(o[d][i], 0.f, zero);
+  // a column whose weights are NaN keeps it: so does every component
+  const bool lost = live && (far || (l == l && !(zero + lane_xor(zero, 32) + l * 0.f == 0.f)));
+  const float r = l == 0.f ? 0.f : 1.f / l;
+  if (live && direct && !lost) {
+    uint16_t* dst = a.out + static_cast<uint64_t>(p.t0 + tok) * a.ldo + static_cast<uint64_t>(h) * D + 4 * g;
 #pragma unroll
     for (int d = 0; d < kDt; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) zero = fmaf(o[c][d][i], 0.f, zero);
-    // columns whose weights are NaN keep it: so does every component
-    const bool lost = live && (far || (l[c] == l[c] && !(zero + lane_xor(zero, 32) + l[c] * 0.f == 0.f)));
-    const float r = l[c] == 0.f ? 0.f : 1.f / l[c];
-    if (live && direct && !lost) {
-      uint16_t* dst = a.out + static_cast<uint64_t>(p.t0 + tok) * a.ldo + static_cast<uint64_t>(h) * D + 4 * g;
-#pragma unroll
-      for (int d = 0; d < kDt; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const u32x2_t x = {pack_bf16(o[c][d][i] * r, o[c][d][i + 1] * r), pack_bf16(o[c][d][i + 2] * r, o[c][d][i + 3] * r)};
-          *reinterpret_cast<u32x2_t*>(dst + 32 * d + 2 * i) = x;
-        }
-    } else if (live && !direct) {
-      const uint64_t at = static_cast<uint64_t>(part) * a.cap + col;
-      if (g == 0) {
-        a.part_ml[2 * at] = lost ? INFINITY : mc[c];  // an infinite maximum: the column is computed by itself
-        a.part_ml[2 * at + 1] = l[c];
-      }
-      float* dst = a.part_o + at * D + 4 * g;
-#pragma unroll
-      for (int d = 0; d < kDt; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<f32x4_t*>(dst + 32 * d + 2 * i) =
-              f32x4_t{o[c][d][i] * r, o[c][d][i + 1] * r, o[c][d][i + 2] * r, o[c][d][i + 3] * r};
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<u32x2_t*>(dst + 32 * d + 2 * i) =
+            u32x2_t{pack_bf16(o[d][i] * r, o[d][i + 1] * r), pack_bf16(o[d][i + 2] * r, o[d][i + 3] * r)};
+  } else if (live && !direct) {
+    const uint64_t at = static_cast<uint64_t>(part) * a.cap + col;
+    if (g == 0) {
+      a.part_ml[2 * at] = lost ? INFINITY : mc;  // an infinite maximum: the column is computed by itself
+      a.part_ml[2 * at + 1] = l;
     }
-    uint64_t again = __ballot(direct && lost) & 0xFFFFFFFFu;
-    for (; again; again &= again - 1) {
-      const uint32_t x = col0 + 32 * c + __builtin_ctzll(again), t = tok0 + x / a.ratio;
-      redo<D>(a, it.row, p.t0 + t, it.head * a.ratio + x % a.ratio, p.base + t + 1);
-    }
+    float* dst = a.part_o + at * D + 4 * g;
+#pragma unroll
+    for (int d = 0; d < kDt; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<f32x4_t*>(dst + 32 * d + 2 * i) = f32x4_t{o[d][i] * r, o[d][i + 1] * r, o[d][i + 2] * r, o[d][i + 3] * r};
+  }
+  for (uint64_t again = __ballot(direct && lost) & 0xFFFFFFFFu; again; again &= again - 1) {
+    const uint32_t x = col0 + __builtin_ctzll(again), t = tok0 + x / a.ratio;
+    redo<D>(a, it.row, p.t0 + t, it.head * a.ratio + x % a.ratio, p.base + t + 1);
   }
 }
 
@@ -769,9 +763,9 @@ struct ChunkLayout {
 };
 ChunkLayout chunk_layout(uint32_t rows, uint32_t tokens, uint32_t ratio, uint32_t d) {
   ChunkLayout L;
-  const bool wide = (d == 64 || d == 128) && static_cast<uint64_t>(tokens) * ratio >= 192ull * rows;
+  const bool wide = d == 128 && static_cast<uint64_t>(tokens) * ratio >= 192ull * rows;
   L.waves = wide ? 8 : 4;
-  L.workers = kCus * (wide ? 1 : d <= 96 ? 3 : d <= 192 ? 2 : 1);  // ChunkShape's workgroups
+  L.workers = kCus * (wide ? 1 : d <= 64 ? 3 : d <= 192 ? 2 : 1);  // ChunkShape's workgroups
   L.tb = 32 * L.waves / ratio;
   L.cap = std::min(tokens, L.tb) * ratio;
   const uint64_t slots = 2ull * L.workers * L.cap;
@@ -855,14 +849,13 @@ nwc_status nwc_attend_chunk(const nwc_cache* cache, const nwc_page_table* table,
   const uint64_t items = std::min<uint64_t>(tokens, table->rows + tokens / L.tb) * a.hkv;
   const uint64_t most = items * ((static_cast<uint64_t>(table->cols) << a.pages.shift) + kItemCost) / kLeast + 1;
   a.workers = static_cast<uint32_t>(std::min<uint64_t>(L.workers, (most + 7) / 8 * 8));
-  a.scale = scale;
   a.scale2 = scale * kLog2e;
   a.part_o = reinterpret_cast<float*>(w);
   a.part_ml = reinterpret_cast<float*>(w + L.ml);
   a.cuts = reinterpret_cast<Cut*>(w + L.cuts);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (d) {
-    case 64: return L.waves == 8 ? launch_chunk<64, 8>(a, s) : launch_chunk<64, 4>(a, s);
+    case 64: return launch_chunk<64, 4>(a, s);
     case 96: return launch_chunk<96, 4>(a, s);
     case 128: return L.waves == 8 ? launch_chunk<128, 8>(a, s) : launch_chunk<128, 4>(a, s);
     case 192: return launch_chunk<192, 4>(a, s);
