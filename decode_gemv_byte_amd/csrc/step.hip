@@ -597,29 +597,32 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprobs_join(const LogprobsAr
 
 // ------------------------------------------------------------------- host ---
 
-constexpr uint32_t kMaxCols = 32768;  // 16 wavefronts of 4 pieces a lane
+constexpr uint32_t kMaxCols = 32768;  // 8 wavefronts of 8 pieces a lane
 
 template <bool F32>
 nwc_status launch_residual(const ResidualArgs& a, hipStream_t s) {
-  // as few wavefronts a token as hold it in 8 pieces a lane where tokens fill the
-  // GPU, else as many as have a piece for each lane
+  // As few wavefronts a token as hold it in 8 pieces a lane where tokens fill the
+  // GPU, else as many as have a piece for each lane; past 16384 columns 8, the most
+  // whose registers hold 8 pieces.
   const bool many = a.tokens >= 4 * kCus;
-  const uint32_t wide = many ? 8 : 1;
-  const uint32_t w = a.cols8 <= 64 * wide ? 1 : a.cols8 <= 256 * wide ? 4 : 16;
-  const uint32_t p = (a.cols8 + 64 * w - 1) / (64 * w);
-  auto go = [&](auto waves) {
-    constexpr int W = decltype(waves)::value;
-    const uint64_t groups = (static_cast<uint64_t>(a.tokens) + (W == 1 ? 3 : 0)) / (W == 1 ? 4 : 1);
-    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(groups, 1u << 20))), block(W == 1 ? 256 : W * 64);
-    if (p == 1) return launch(k_residual<W, 1, F32>, grid, block, 0, s, a);
-    if (p == 2) return launch(k_residual<W, 2, F32>, grid, block, 0, s, a);
-    if constexpr (W < 16)
-      if (p > 4) return launch(k_residual<W, 8, F32>, grid, block, 0, s, a);
-    return launch(k_residual<W, 4, F32>, grid, block, 0, s, a);
+  const auto go = [&](auto kernel, uint32_t w) {
+    const uint64_t groups = w == 1 ? (static_cast<uint64_t>(a.tokens) + 3) / 4 : a.tokens;
+    return launch(kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>(groups, 1u << 20))), dim3(w == 1 ? 256 : w * 64), 0, s, a);
   };
-  if (w == 1) return go(std::integral_constant<int, 1>{});
-  if (w == 4) return go(std::integral_constant<int, 4>{});
-  return go(std::integral_constant<int, 16>{});
+  const uint32_t c = a.cols8;
+  if (c > 2048) return go(k_residual<8, 8, F32>, 8);
+  if (many) {
+    if (c > 1024) return go(k_residual<4, 8, F32>, 4);
+    if (c > 512) return go(k_residual<4, 4, F32>, 4);
+    if (c > 256) return go(k_residual<1, 8, F32>, 1);
+    if (c > 128) return go(k_residual<1, 4, F32>, 1);
+    if (c > 64) return go(k_residual<1, 2, F32>, 1);
+    return go(k_residual<1, 1, F32>, 1);
+  }
+  if (c > 1024) return go(k_residual<16, 2, F32>, 16);
+  if (c > 256) return go(k_residual<16, 1, F32>, 16);
+  if (c > 64) return go(k_residual<4, 1, F32>, 4);
+  return go(k_residual<1, 1, F32>, 1);
 }
 
 struct LogprobsLayout {
