@@ -32,9 +32,25 @@ typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 // products: a lane's scores are those of one column at positions 8 a + 4 g + j (g =
 // lane / 32, a and j = 0 .. 3), which is the order in which the second product
 // takes its weights from the lane's own registers, if the values come in the same
-// order: two transposing LDS reads of 4 positions each.  Keys and values pass
-// through LDS, two units deep, in pieces of 16 bytes placed so that the reads of
-// both kinds touch all banks evenly.
+// order: two transposing LDS reads of 4 positions each.  The weights are rounded to
+// BF16 for that product, their sum is not: an output is off by half a step of BF16
+// (its own rounding) and, from the weights' roundings, which are independent, by less
+// than that again, where keeping their other 16 bits takes a second product, half as
+// much again of all matrix work.
+//
+// Keys and values go straight to a ring of units in LDS, kAhead units before their
+// turn, in pieces of 16 bytes placed so that the reads of both kinds touch all banks
+// evenly.  Of 8 wavefronts (heads of 128) the two that share a SIMD are half a turn
+// apart, so that one's weights are made beside the other's products; 4 wavefronts and
+// two or three workgroups a compute unit leave that to chance.
+//
+// Bound by the matrix cores, whose clock falls under this load: 4096 tokens behind
+// 28672 positions, 32 / 8 heads of 128, 1930 us, 1070 TFLOP/s, where an 8192^3 product
+// reaches 1250 (by 4 wavefronts 2130); 8192 tokens of a new prompt 570 us, 960 TFLOP/s
+// (by 4 wavefronts 588).  With few columns by what an item leaves for the join (64
+// tokens behind 131007 positions: 156 us and 10 for the join, 3.1 TB/s), with single
+// tokens by HBM (31 rows of up to 4001 positions 71 us, 4.5 TB/s), with little work by
+// one chain of dependent loads (5 tokens behind 507 positions: 6.3 us).
 
 constexpr int kChunkThreads = 256;
 constexpr uint32_t kMaxWorkers = 4 * kCus;
@@ -763,6 +779,10 @@ struct ChunkLayout {
 };
 ChunkLayout chunk_layout(uint32_t rows, uint32_t tokens, uint32_t ratio, uint32_t d) {
   ChunkLayout L;
+  // 8 wavefronts a workgroup where a row has columns for 6 of them.  Us by 4 and by 8, 32
+  // / 8 heads: rows of one token 71 and 86, of 64 tokens (256 columns) behind 3000
+  // positions 38.4 and 38.8, of 128 51 and 50, of 512 142 and 137; 64 tokens behind 131007
+  // positions 199 and 182
   const bool wide = d == 128 && static_cast<uint64_t>(tokens) * ratio >= 192ull * rows;
   L.waves = wide ? 8 : 4;
   L.workers = kCus * (wide ? 1 : d <= 64 ? 3 : d <= 192 ? 2 : 1);  // ChunkShape's workgroups

@@ -48,7 +48,11 @@ __device__ __forceinline__ u32x4_t pack8(const float (&f)[8]) {
 
 // A token by W wavefronts, P pieces of 8 values a lane, all of a row's values in
 // registers between its loads and its stores: each is read once, before any of
-// its lane's pieces is written.
+// its lane's pieces is written.  Sums of squares are FP32; x', where it is BF16, is
+// rounded when it is stored, and the norm takes it as it was before.
+// Bound by HBM for a prompt: 16384 tokens of 4096, 537 MB, 102 us, 5.2 TB/s, what a large
+// copy and read reach together; by one chain of loads, a sum and a store for a token:
+// 2.8 us, of which an empty launch takes 2.5.
 template <int W, int P, bool F32>
 __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void k_residual(const ResidualArgs a) {
   constexpr int kRows = W == 1 ? 4 : 1;  // tokens that a workgroup has at a time
@@ -213,6 +217,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void k_residual(const Residu
 // wavefront's k lowest) is ranked by counting, each against all.  Where more is
 // found than LDS has room for, or NaN stands in the row, k rounds of a largest
 // below the last one take its place.
+//
+// 2048 rows of 128256 BF16 logits, 525 MB, k = 20: 123 us, 4.3 TB/s, bound by vector
+// instructions (85 us of them: an exponential, two products and a maximum a logit) beside
+// loads that take 85 by themselves; one row of 128256: 8.4 us and 5.4 for the join, both
+// one chain of loads, sums over the workgroup and a ranking.
 
 constexpr int kLpThreads = 512, kLpWaves = kLpThreads / kWave;
 constexpr uint32_t kLpMaxK = 64, kLpMaxSplit = 32, kLpFound = 2048;
@@ -603,7 +612,9 @@ template <bool F32>
 nwc_status launch_residual(const ResidualArgs& a, hipStream_t s) {
   // As few wavefronts a token as hold it in 8 pieces a lane where tokens fill the
   // GPU, else as many as have a piece for each lane; past 16384 columns 8, the most
-  // whose registers hold 8 pieces.
+  // whose registers hold 8 pieces.  Us for 4096 columns, few and many wavefronts a token:
+  // 256 tokens 6.3 and 3.9, 512 tokens 6.8 and 6.2, 1024 tokens 8.3 and 10.1, 16384 tokens
+  // 104 and 169
   const bool many = a.tokens >= 4 * kCus;
   const auto go = [&](auto kernel, uint32_t w) {
     const uint64_t groups = w == 1 ? (static_cast<uint64_t>(a.tokens) + 3) / 4 : a.tokens;
@@ -631,7 +642,8 @@ struct LogprobsLayout {
 };
 LogprobsLayout logprobs_layout(uint32_t rows, uint32_t vocab, uint32_t k) {
   LogprobsLayout L;
-  // two workgroups a compute unit, of 4096 logits at least
+  // Two workgroups a compute unit, of 4096 logits at least: us by 2048, 4096 and 8192 at
+  // least, 1 row of 32003: 13.6, 13.0, 13.0; 8 rows 14.2, 13.4, 13.9; 16 rows 12.3, 11.6, 11.6
   const uint32_t want = std::min<uint32_t>({(2 * kCus + rows - 1) / rows, (vocab + 4095) / 4096, kLpMaxSplit});
   L.chunk = ((vocab + want - 1) / want + 7) / 8 * 8;
   L.split = (vocab + L.chunk - 1) / L.chunk;

@@ -380,3 +380,41 @@ def test_offsets_past_32_bits():
     nwc.nwc_attend_chunk(c.call())
     torch.cuda.synchronize()
     c.check("far page")
+
+
+def test_wide_items_and_what_they_do_not_see():
+    # rows of more than 192 columns with heads of 128: slots behind the lengths, an inner unit's missing page, tokens that are
+    # more than the positions, a padding row, and rows of a token beside them
+    for value in (float("nan"), -float("inf"), 3.3e38):
+        c = Case([90, 70, 150, 60, 1], [500, 64, 150, 300, 777], 32, 8, 128, 32, seed=21)
+        for r in range(5):
+            n = int(c.lengths[r])
+            if n % 32:
+                pg = int(c.table[r, n // 32])
+                c.k[pg, :, n % 32:] = value
+                c.v[pg, :, n % 32:] = value
+        c.table[0, 4] = -1
+        c.table[0, 15] = 2 ** 31 - 1
+        c.lengths[3] = -1
+        call = c.call()
+        nwc.nwc_attend_chunk(call)
+        torch.cuda.synchronize()
+        c.check("wide items, %g behind the lengths" % value)
+        first = c.out.clone()
+        for _ in range(3):
+            nwc.nwc_attend_chunk(call)
+            torch.cuda.synchronize()
+            assert torch.equal(c.out, first)
+
+
+def test_wide_items_of_large_values_and_nan_queries():
+    c = Case([64, 70], [300, 2000], 32, 8, 128, 64, seed=22)
+    c.v.fill_(3.0e38)
+    c.q[3, 5, 7] = float("nan")
+    c.q[100, 31, 0] = float("inf")
+    nwc.nwc_attend_chunk(c.call())
+    torch.cuda.synchronize()
+    want = torch.full_like(c.out, 3.0e38)
+    want[3, 5] = float("nan")
+    want[100, 31] = float("nan")
+    assert torch.equal(c.out.nan_to_num(1234.0), want.nan_to_num(1234.0))
