@@ -104,17 +104,29 @@ struct RowPart {
     base = end - n;
   }
   __device__ uint32_t blocks(uint32_t tb) const { return (n + tb - 1) / tb; }
-  // positions that block b sees, and what all blocks before it take
+  // positions that block b sees, and what the first b < blocks take
   __device__ uint32_t sees(uint32_t b, uint32_t tb) const { return base + min(n, (b + 1) * tb); }
-  __device__ uint64_t before(uint32_t b, uint32_t tb) const {
+  __device__ uint64_t first(uint32_t b, uint32_t tb) const {
     return static_cast<uint64_t>(b) * (base + kItemCost) + static_cast<uint64_t>(tb) * (static_cast<uint64_t>(b) * (b + 1) / 2);
+  }
+  // A row's blocks in order: the first, the last, the second, the last but one, ..: two
+  // together take the same, so the ranges of a long prompt end where items do.  The i-th
+  // of them, and what all before it take.
+  __device__ static uint32_t block(uint32_t i, uint32_t blocks) { return i % 2 ? blocks - 1 - i / 2 : i / 2; }
+  __device__ uint64_t before(uint32_t i, uint32_t tb) const {
+    uint64_t x = first((i + 1) / 2, tb);
+    if (i >= 2) {
+      const uint32_t nb = blocks(tb);
+      x += first(nb - 1, tb) + base + n + kItemCost - first(nb - i / 2, tb);
+    }
+    return x;
   }
 };
 
 // An item, and where it lies in the stretch of all positions; wave-uniform.
 struct Item {
   uint64_t at;  // its first position in the stretch
-  uint32_t head, row, block;
+  uint32_t head, row, order, block;  // order: among the row's blocks
 };
 
 // The positions of all rows before each row, in LDS: pre[rows + 1]; carry: W more.
@@ -160,10 +172,29 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
   return static_cast<uint64_t>(uniform(static_cast<uint32_t>(v >> 32))) << 32 | uniform(static_cast<uint32_t>(v));
 }
 
-// Positions per worker: equal ranges.
-__device__ __forceinline__ uint64_t quota_of(const ChunkArgs& a, uint64_t total) {
-  return max((total + a.workers - 1) / a.workers, uint64_t{kLeast});
-}
+// Equal ranges of the stretch for the first n workers: worker w's begins at begin(w).
+struct Ranges {
+  uint64_t total, each;
+  uint32_t n, rest, near;  // near: see unit_of
+  __device__ Ranges(const ChunkArgs& a, uint64_t all) : total(all) {
+    n = static_cast<uint32_t>(min(static_cast<uint64_t>(a.workers), max(all / kLeast, uint64_t{1})));
+    each = all / n;
+    rest = static_cast<uint32_t>(all - each * n);
+    near = static_cast<uint32_t>(min(each / 8, static_cast<uint64_t>(kItemCost)));
+  }
+  __device__ uint64_t begin(uint32_t w) const {  // total w / n
+    w = min(w, n);
+    return each * w + rest * w / n;
+  }
+  __device__ uint32_t worker(uint64_t x) const { return static_cast<uint32_t>(((x + 1) * n - 1) / total); }  // of position x
+  // The unit of an item that a range's bound falls on: none of it where it is that near to
+  // its begin, since a cut takes what kItemCost positions take (and near its end, where
+  // kItemCost lies).
+  template <uint32_t kUnit>
+  __device__ uint32_t unit_of(uint64_t x, uint64_t at, uint32_t units) const {
+    return x <= at + near ? 0 : static_cast<uint32_t>(min(static_cast<uint64_t>(units), (x - at + kUnit - 1) / kUnit));
+  }
+};
 
 // The item that position x < hkv * pre[rows] of the stretch belongs to.
 __device__ __forceinline__ Item find(const ChunkArgs& a, const uint64_t* pre, uint64_t x) {
@@ -180,12 +211,12 @@ __device__ __forceinline__ Item find(const ChunkArgs& a, const uint64_t* pre, ui
   it.row = lo;
   const uint64_t first = uniform64(pre[lo]);
   const RowPart p(a, lo);
-  uint32_t b = 0, end = p.blocks(a.tb);  // the last block with before(b) <= rem - first
+  uint32_t b = 0, end = p.blocks(a.tb);  // the last one with before(b) <= rem - first
   while (b + 1 < end) {
     const uint32_t mid = (b + end) / 2;
     if (p.before(mid, a.tb) <= rem - first) b = mid; else end = mid;
   }
-  it.block = b;
+  it.order = b;
   it.at = it.head * each + first + p.before(b, a.tb);
   return it;
 }
@@ -586,27 +617,28 @@ __global__ __launch_bounds__(W * kWave, (ChunkShape<D, W>::kWgs * W / 4)) void k
     for (uint64_t i = threadIdx.x; i < static_cast<uint64_t>(p.skipped) * per; i += W * kWave)
       *reinterpret_cast<u32x4_t*>(a.out + (p.t0 - p.skipped + i / per) * a.ldo + i % per * 8) = u32x4_t{0, 0, 0, 0};
   }
-  const uint64_t total = uniform64(pre[rows]) * a.hkv, quota = quota_of(a, total);
+  const uint64_t total = uniform64(pre[rows]) * a.hkv;
+  const Ranges ranges(a, total);
   const uint32_t w = worker_of(blockIdx.x, a.workers);
-  const uint64_t x0 = w * quota, x1 = min(x0 + quota, total);
+  const uint64_t x0 = ranges.begin(w), x1 = ranges.begin(w + 1);
   Cut cut = {};
-  if (x0 < total) {
+  if (x0 < x1) {
     Item it = find(a, pre, x0);
     RowPart p(a, it.row);
     for (;;) {
+      it.block = RowPart::block(it.order, p.blocks(a.tb));
       const uint32_t sees = p.sees(it.block, a.tb), units = (sees + kUnit - 1) / kUnit;
-      const uint32_t u0 = x0 > it.at ? static_cast<uint32_t>((x0 - it.at + kUnit - 1) / kUnit) : 0;
-      const uint32_t u1 = static_cast<uint32_t>(min(static_cast<uint64_t>(units), (x1 - it.at + kUnit - 1) / kUnit));
-      if (x0 <= it.at && u1 < units) {  // the last one, which goes on in the next workers' ranges
+      const uint32_t u0 = ranges.unit_of<kUnit>(x0, it.at, units), u1 = ranges.unit_of<kUnit>(x1, it.at, units);
+      if (u0 == 0 && u1 != 0 && u1 < units) {  // the last one, which goes on in the next workers' ranges
         const uint64_t last = it.at + static_cast<uint64_t>(units - 1) * kUnit;
         const uint32_t tok0 = it.block * a.tb;
-        cut = Cut{static_cast<uint32_t>(last / quota) - w, it.head, min(a.tb, p.n - tok0) * a.ratio, p.t0 + tok0, p.base + tok0 + 1, it.row, w, 0};
+        cut = Cut{ranges.worker(last) - w, it.head, min(a.tb, p.n - tok0) * a.ratio, p.t0 + tok0, p.base + tok0 + 1, it.row, w, 0};
       }
-      if (u0 < u1) run_item<D, W>(a, it, p, u0, u1, 2 * w + (x0 > it.at ? 0 : 1), lds);
+      if (u0 < u1) run_item<D, W>(a, it, p, u0, u1, 2 * w + (u0 ? 0 : 1), lds);
       it.at += sees + kItemCost;
       if (it.at >= x1) break;
-      if (++it.block == p.blocks(a.tb)) {
-        it.block = 0;
+      if (++it.order == p.blocks(a.tb)) {
+        it.order = 0;
         do {
           if (++it.row == rows) {
             it.row = 0;
