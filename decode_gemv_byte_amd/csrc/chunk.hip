@@ -45,12 +45,12 @@ typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 // two or three workgroups a compute unit leave that to chance.
 //
 // Bound by the matrix cores, whose clock falls under this load: 4096 tokens behind
-// 28672 positions, 32 / 8 heads of 128, 1930 us, 1070 TFLOP/s, where an 8192^3 product
-// reaches 1250 (by 4 wavefronts 2130); 8192 tokens of a new prompt 570 us, 960 TFLOP/s
-// (by 4 wavefronts 588).  With few columns by what an item leaves for the join (64
-// tokens behind 131007 positions: 156 us and 10 for the join, 3.1 TB/s), with single
-// tokens by HBM (31 rows of up to 4001 positions 71 us, 4.5 TB/s), with little work by
-// one chain of dependent loads (5 tokens behind 507 positions: 6.3 us).
+// 28672 positions, 32 / 8 heads of 128, 1820 us, 1130 TFLOP/s, where an 8192^3 product
+// reaches 1250; 8192 tokens of a new prompt 526 us, 1045 TFLOP/s.  With few columns by
+// what an item leaves for the join (64 tokens behind 131007 positions: 155 us and 10 for
+// the join, 3.4 TB/s), with single tokens by HBM (31 rows of up to 4001 positions 73 us,
+// 4.4 TB/s), with little work by one chain of dependent loads (5 tokens behind 507
+// positions: 6.4 us).
 
 constexpr int kChunkThreads = 256;
 constexpr uint32_t kMaxWorkers = 4 * kCus;
@@ -110,8 +110,9 @@ struct RowPart {
     return static_cast<uint64_t>(b) * (base + kItemCost) + static_cast<uint64_t>(tb) * (static_cast<uint64_t>(b) * (b + 1) / 2);
   }
   // A row's blocks in order: the first, the last, the second, the last but one, ..: two
-  // together take the same, so the ranges of a long prompt end where items do.  The i-th
-  // of them, and what all before it take.
+  // together take the same, so the ranges of a long prompt end where items do (in plain
+  // order 4096 tokens behind 28672 positions took 1905 us, so 1790; 8192 tokens 558 and
+  // 526; seven short prompts 124 and 126).  The i-th of them, and what all before it take.
   __device__ static uint32_t block(uint32_t i, uint32_t blocks) { return i % 2 ? blocks - 1 - i / 2 : i / 2; }
   __device__ uint64_t before(uint32_t i, uint32_t tb) const {
     uint64_t x = first((i + 1) / 2, tb);
@@ -189,7 +190,8 @@ struct Ranges {
   __device__ uint32_t worker(uint64_t x) const { return static_cast<uint32_t>(((x + 1) * n - 1) / total); }  // of position x
   // The unit of an item that a range's bound falls on: none of it where it is that near to
   // its begin, since a cut takes what kItemCost positions take (and near its end, where
-  // kItemCost lies).
+  // kItemCost lies).  With it 4 rows of 512 tokens behind 3000 positions take 116 us,
+  // without 126; two of 1024 with heads of 256 64.5 and 62.7.
   template <uint32_t kUnit>
   __device__ uint32_t unit_of(uint64_t x, uint64_t at, uint32_t units) const {
     return x <= at + near ? 0 : static_cast<uint32_t>(min(static_cast<uint64_t>(units), (x - at + kUnit - 1) / kUnit));
@@ -809,13 +811,18 @@ struct ChunkLayout {
   uint32_t waves, workers, tb, cap;
   uint64_t ml, cuts, bytes;
 };
-ChunkLayout chunk_layout(uint32_t rows, uint32_t tokens, uint32_t ratio, uint32_t d) {
+ChunkLayout chunk_layout(uint32_t rows, uint32_t tokens, uint32_t ratio, uint32_t kv_heads, uint32_t d) {
   ChunkLayout L;
-  // 8 wavefronts a workgroup where a row has columns for 6 of them.  Us by 4 and by 8, 32
-  // / 8 heads: rows of one token 71 and 86, of 64 tokens (256 columns) behind 3000
-  // positions 38.4 and 38.8, of 128 51 and 50, of 512 142 and 137; 64 tokens behind 131007
-  // positions 199 and 182
-  const bool wide = d == 128 && static_cast<uint64_t>(tokens) * ratio >= 192ull * rows;
+  // 8 wavefronts a workgroup for long prompts, whose tiles then serve twice as many
+  // columns, and where items are so few that all are cut, into half as many parts then.  Us
+  // by 4 and by 8, 32 / 8 heads: 1 row of 4096 tokens behind 28672 positions 1874 and 1792, 16
+  // rows of 512 behind 3000 455 and 430, of 256 222 and 226, 9 rows with a prompt of 1000
+  // among them 109 and 114, 20 prompts of 400 at most 45 and 48, 64 rows of 32 114 and 122; 4
+  // rows of 16 behind 3000 33 and 28, of 32 36 and 30, 1 row of 32 behind 100000 105 and 92,
+  // of 8 86 and 84, of 4 (16 columns) 87 and 95; 31 rows of one 73 and 88.
+  const uint64_t columns = static_cast<uint64_t>(tokens) * ratio;
+  const bool few = (rows + columns / 128) * kv_heads < kCus && columns >= 32ull * rows;
+  const bool wide = d == 128 && (few || columns >= 1536ull * rows);
   L.waves = wide ? 8 : 4;
   L.workers = kCus * (wide ? 1 : d <= 64 ? 3 : d <= 192 ? 2 : 1);  // ChunkShape's workgroups
   L.tb = 32 * L.waves / ratio;
@@ -859,7 +866,7 @@ nwc_status nwc_attend_chunk_workspace_size(const nwc_cache* cache, uint32_t rows
   if (!bytes) return NWC_ERR_INVALID_ARG;
   const nwc_status st = chunk_shape(cache, rows, tokens, q_heads);
   if (st) return st;
-  *bytes = chunk_layout(rows, tokens, q_heads / cache->kv_heads, cache->head_dim).bytes;
+  *bytes = chunk_layout(rows, tokens, q_heads / cache->kv_heads, cache->kv_heads, cache->head_dim).bytes;
   return NWC_OK;
 }
 
@@ -880,7 +887,7 @@ nwc_status nwc_attend_chunk(const nwc_cache* cache, const nwc_page_table* table,
       !aligned(ws, 256))
     return NWC_ERR_ALIGNMENT;
   a.ratio = q_heads / cache->kv_heads;
-  const ChunkLayout L = chunk_layout(table->rows, tokens, a.ratio, d);
+  const ChunkLayout L = chunk_layout(table->rows, tokens, a.ratio, cache->kv_heads, d);
   if (ws_bytes < L.bytes) return NWC_ERR_BUFFER_TOO_SMALL;
   if (out_dev == q_dev) return NWC_ERR_INVALID_ARG;  // workgroups read queries that others have answered
   uint8_t* w = static_cast<uint8_t*>(ws);

@@ -418,3 +418,23 @@ def test_wide_items_of_large_values_and_nan_queries():
     want[3, 5] = float("nan")
     want[100, 31] = float("nan")
     assert torch.equal(c.out.nan_to_num(1234.0), want.nan_to_num(1234.0))
+
+
+def test_many_rows_of_some_tokens():
+    # heads of 128, more items than are all cut, no long prompt among them
+    rnd = np.random.default_rng(23)
+    new = rnd.integers(0, 60, 40)
+    lengths = new + rnd.integers(1, 300, 40)
+    lengths[7] = new[7] // 2                                    # fewer positions than tokens
+    c = Case(list(new), list(lengths), 32, 8, 128, 16, seed=24, gap=64)
+    for r in range(40):
+        n = int(c.lengths[r])
+        if n % 16:
+            pg = int(c.table[r, n // 16])
+            c.k[pg, :, n % 16:] = float("nan")
+            c.v[pg, :, n % 16:] = float("inf")
+    c.table[3, 0] = -5
+    c.lengths[11] = -2
+    nwc.nwc_attend_chunk(c.call())
+    torch.cuda.synchronize()
+    c.check("many rows of some tokens")
