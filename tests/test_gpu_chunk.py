@@ -438,3 +438,29 @@ def test_many_rows_of_some_tokens():
     nwc.nwc_attend_chunk(c.call())
     torch.cuda.synchronize()
     c.check("many rows of some tokens")
+
+
+def test_refusals_of_device_tensors():
+    c = Case([3, 2], [40, 9], 8, 2, 64, 16, seed=25)
+    good = c.call()
+    cache, (table, start, lengths) = nwc.PagedCache(c.k, c.v), c.dev
+    ws = torch.zeros(nwc.nwc_attend_chunk_workspace_size(cache, 2, 5, 8), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(c.q)
+    for args in ((table, start[:2], lengths, c.q, out, ws), (table, start, lengths[:1], c.q, out, ws), (table, start.long(), lengths, c.q, out, ws),
+                 (table, start, lengths, c.q.float(), out, ws), (table, start, lengths, c.q, out[:4], ws), (table, start, lengths, c.q, out, ws.float()),
+                 (table, start, lengths, c.q[..., :32], out[..., :32], ws), (table.long(), start, lengths, c.q, out, ws)):
+        with pytest.raises(ValueError):
+            nwc.AttendChunk(cache, *args)
+    odd = torch.zeros((5, 3, 64), dtype=torch.bfloat16, device="cuda")                   # 3 heads for 2 key-value heads
+    for bad in (nwc.AttendChunk(cache, table, start, lengths, c.q, c.q, ws), nwc.AttendChunk(cache, table, start, lengths, c.q, out, ws[:256]),
+                nwc.AttendChunk(cache, table, start, lengths, odd, odd.clone(), ws),
+                nwc.AttendChunk(cache, table, start, lengths, c.q, out, ws, scale=0.0),
+                nwc.AttendChunk(cache, table, start, lengths, c.q, out, ws, scale=float("nan")),
+                nwc.AttendChunk(cache, table, start, lengths, c.q, out, ws[1:])):
+        with pytest.raises(nwc.NwcError):
+            nwc.nwc_attend_chunk(bad)
+    torch.cuda.synchronize()
+    assert bool((c.out == 7.0).all())                           # nothing ran
+    nwc.nwc_attend_chunk(good)
+    torch.cuda.synchronize()
+    c.check("after refusals")

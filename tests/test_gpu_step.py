@@ -330,3 +330,32 @@ def test_residual_captured():
             graph.replay()
         torch.cuda.synchronize()
         _check_residual(_ref_residual(x, y, w, None, 1.0, w), x_out, out, w, "replay", True)
+
+
+def test_refusals_of_device_tensors():
+    bf, f, i = torch.bfloat16, torch.float32, torch.int32
+    z = lambda shape, dtype: torch.zeros(shape, dtype=dtype, device="cuda")
+    x, y, w, out = z((4, 64), bf), z((4, 64), bf), z(64, bf), z((4, 64), bf)
+    for kw in (dict(y=z((4, 64), f)), dict(y=z((3, 64), bf)), dict(y=y, gate=z((4, 32), bf)), dict(y=y, gate=w, y_weight=z(63, bf)),
+               dict(out=out), dict(weight=w), dict(y=y, x_out=z((4, 64), f)), dict(out=out.T, weight=w), dict(gate=w, out=out, weight=w),
+               dict(y=y, x_out=x.clone(), keep=False)):
+        with pytest.raises((ValueError, TypeError)):
+            nwc.ResidualNorm(x, **kw)
+    for bad in (nwc.ResidualNorm(x, y, eps=-1.0), nwc.ResidualNorm(x, y, scale=float("inf")), nwc.ResidualNorm(x, out=w.view(1, 64).expand(4, 64), weight=w),
+                nwc.ResidualNorm(z((4, 60), bf), z((4, 60), bf))):
+        with pytest.raises(nwc.NwcError):
+            nwc.nwc_residual_norm(bad)
+    logits, ws = z((4, 1000), bf), z(nwc.nwc_token_logprobs_workspace_size(4, 1000, 5), torch.uint8)
+    t, lp, ent, ids, top = z((4, 2), i), z((4, 2), f), z(4, f), z((4, 5), i), z((4, 5), f)
+    for kw in (dict(targets=t), dict(logprobs=lp), dict(targets=t.long(), logprobs=lp), dict(targets=t, logprobs=lp[:, :1]),
+               dict(entropy=ent[:3]), dict(top_ids=ids), dict(top_ids=ids, top_logprobs=top.to(bf)), dict(top_ids=ids[:, ::2], top_logprobs=top[:, ::2])):
+        with pytest.raises((ValueError, TypeError)):
+            nwc.TokenLogprobs(logits, ws, **kw)
+    with pytest.raises((ValueError, TypeError)):
+        nwc.TokenLogprobs(logits.half(), ws, entropy=ent)
+    for bad in (nwc.TokenLogprobs(logits, ws), nwc.TokenLogprobs(logits, ws, entropy=ent, scale=0.0),
+                nwc.TokenLogprobs(logits[:, 1:], ws, entropy=ent), nwc.TokenLogprobs(logits, ws[:128], entropy=ent),
+                nwc.TokenLogprobs(z((4, 1001), bf), ws, entropy=ent),
+                nwc.TokenLogprobs(logits, ws, top_ids=z((4, 65), i), top_logprobs=z((4, 65), f))):
+        with pytest.raises(nwc.NwcError):
+            nwc.nwc_token_logprobs(bad)
