@@ -46,7 +46,8 @@ typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 //
 // Bound by the matrix cores, whose clock falls under this load: 4096 tokens behind
 // 28672 positions, 32 / 8 heads of 128, 1820 us, 1130 TFLOP/s, where an 8192^3 product
-// reaches 1250; 8192 tokens of a new prompt 526 us, 1045 TFLOP/s.  With few columns by
+// reaches 1250; 8192 tokens of a new prompt 526 us, 1045 TFLOP/s (1920 and 553 on a card
+// whose clock falls further).  With few columns by
 // what an item leaves for the join (64 tokens behind 131007 positions: 155 us and 10 for
 // the join, 3.4 TB/s), with single tokens by HBM (31 rows of up to 4001 positions 73 us,
 // 4.4 TB/s), with little work by one chain of dependent loads (5 tokens behind 507
@@ -823,15 +824,21 @@ ChunkLayout chunk_layout(uint32_t rows, uint32_t tokens, uint32_t ratio, uint32_
   const uint64_t columns = static_cast<uint64_t>(tokens) * ratio;
   const bool few = (rows + columns / 128) * kv_heads < kCus && columns >= 32ull * rows;
   const bool wide = d == 128 && (few || columns >= 1536ull * rows);
-  L.waves = wide ? 8 : 4;
-  L.workers = kCus * (wide ? 1 : d <= 64 ? 3 : d <= 192 ? 2 : 1);  // ChunkShape's workgroups
-  L.tb = 32 * L.waves / ratio;
-  L.cap = std::min(tokens, L.tb) * ratio;
-  const uint64_t slots = 2ull * L.workers * L.cap;
   auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
-  L.ml = up(slots * d * 4);
-  L.cuts = L.ml + up(slots * 8);
-  L.bytes = L.cuts + up(L.workers * sizeof(Cut));
+  auto by = [&](bool w8) {
+    L.waves = w8 ? 8 : 4;
+    L.workers = kCus * (w8 ? 1 : d <= 64 ? 3 : d <= 192 ? 2 : 1);  // ChunkShape's workgroups
+    L.tb = 32 * L.waves / ratio;
+    L.cap = std::min(tokens, L.tb) * ratio;
+    const uint64_t slots = 2ull * L.workers * L.cap;
+    L.ml = up(slots * d * 4);
+    L.cuts = L.ml + up(slots * 8);
+    return L.cuts + up(L.workers * sizeof(Cut));
+  };
+  // what either takes: a workspace for more tokens serves fewer, by however many wavefronts
+  const uint64_t other = d == 128 ? by(!wide) : 0;
+  L.bytes = by(wide);
+  L.bytes = std::max(L.bytes, other);
   return L;
 }
 

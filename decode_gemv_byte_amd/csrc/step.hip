@@ -648,7 +648,10 @@ LogprobsLayout logprobs_layout(uint32_t rows, uint32_t vocab, uint32_t k) {
   L.chunk = ((vocab + want - 1) / want + 7) / 8 * 8;
   L.split = (vocab + L.chunk - 1) / L.chunk;
   auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
-  const uint64_t parts = L.split == 1 ? 0 : static_cast<uint64_t>(rows) * L.split;
+  // the most parts that as many rows or fewer have, of rows * split < 2 kCus + rows: a
+  // workspace for more rows serves fewer
+  const uint64_t most = std::min<uint32_t>((vocab + 4095) / 4096, kLpMaxSplit);
+  const uint64_t parts = most == 1 ? 0 : std::min<uint64_t>(rows * most, 4 * kCus - 1);
   L.tops = up(parts * 16);
   L.bytes = std::max<uint64_t>(256, L.tops + up(parts * k * 8));
   return L;

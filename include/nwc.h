@@ -516,8 +516,9 @@ nwc_status nwc_attend(const nwc_cache *cache, const nwc_page_table *table, const
  * infinity or a NaN on the way, seen or not, takes longer: it is computed once
  * more, by itself.
  * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
- * nwc_attend_chunk_workspace_size bytes; no initial content needed); calls that
- * share it must not run concurrently.  Async.
+ * nwc_attend_chunk_workspace_size bytes; no initial content needed; what serves
+ * more tokens serves fewer, of any number of rows); calls that share it must not
+ * run concurrently.  Async.
  * Errors: INVALID_ARG, BUFFER_TOO_SMALL (ws), ALIGNMENT, UNSUPPORTED, HIP. */
 nwc_status nwc_attend_chunk_workspace_size(const nwc_cache *cache, uint32_t rows, uint32_t tokens,
                                            uint32_t q_heads, size_t *bytes);
@@ -573,8 +574,9 @@ nwc_status nwc_residual_norm(const nwc_residual *args, uint32_t tokens, uint32_t
  * entropy 0.  +infinity or NaN among a row's logits make all its log probabilities
  * and its entropy NaN; in the order a NaN stands above +infinity.
  * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
- * nwc_token_logprobs_workspace_size bytes; no initial content needed); calls that
- * share it must not run concurrently.  Async.
+ * nwc_token_logprobs_workspace_size bytes; no initial content needed; what serves
+ * more rows, a larger vocab or k serves less of each); calls that share it must
+ * not run concurrently.  Async.
  * Errors: INVALID_ARG, BUFFER_TOO_SMALL (ws), ALIGNMENT, UNSUPPORTED, HIP. */
 nwc_status nwc_token_logprobs_workspace_size(uint32_t rows, uint32_t vocab, uint32_t k, size_t *bytes);
 nwc_status nwc_token_logprobs(const void *logits_dev, uint64_t ld, nwc_out_type type, uint32_t rows,

@@ -160,3 +160,28 @@ def test_chunk_kernels_spill_nothing(tmp_path):
     assert sum("k_chunk" in k[".name"] for k in ours) == 11 and sum("k_logprobs" in k[".name"] for k in ours) == 4
     for k in ours:
         assert k[".vgpr_spill_count"] == 0 and k[".private_segment_fixed_size"] == 0, k[".name"]
+
+
+def test_a_workspace_for_more_serves_less():
+    size = ctypes.c_size_t()
+
+    def chunk(rows, tokens, ratio, hkv, d):
+        c = _cache(head_dim=d, kv_heads=hkv, page_stride=hkv * d * 1024)
+        assert L.nwc_attend_chunk_workspace_size(_ref(c), rows, tokens, ratio * hkv, ctypes.byref(size)) == nwc.NWC_OK
+        return size.value
+    for d in (64, 96, 128, 192, 256):
+        for ratio, hkv in ((1, 8), (4, 8), (7, 4), (64, 1)):
+            last = 0
+            for tokens in list(range(1, 300)) + [500, 1000, 4096, 70000]:
+                sizes = {chunk(rows, tokens, ratio, hkv, d) for rows in (1, 2, 5, 33, 700)}
+                assert len(sizes) == 1 and sizes.pop() >= last, (d, ratio, tokens)
+                last = chunk(1, tokens, ratio, hkv, d)
+
+    def logprobs(rows, vocab, k):
+        assert L.nwc_token_logprobs_workspace_size(rows, vocab, k, ctypes.byref(size)) == nwc.NWC_OK
+        return size.value
+    for vocab in (100, 4096, 4097, 32003, 128256, 1 << 20):
+        for k in (0, 1, 20, 64):
+            sizes = [logprobs(rows, vocab, k) for rows in list(range(1, 600)) + [1024, 4096]]
+            assert sizes == sorted(sizes), (vocab, k)
+            assert all(logprobs(rows, vocab, k) <= logprobs(rows, vocab + 5000, k) for rows in (1, 7, 300, 600))
