@@ -243,14 +243,15 @@ struct LogprobsArgs {
   uint64_t* tops;         // k keys of each part, descending
 };
 
-// The order of logits: value, the lower index first, NaN above all, -0 as 0.
+// The order of logits: value, the lower index first, NaN above all, -0 as 0.  Every NaN
+// counts as the positive quiet one, above +infinity, so that a key is neither 0 nor all
+// ones: 0 stands for none, and all ones is above every key.
 __device__ __forceinline__ uint32_t ordered(float x) {
-  if (x != x) return 0xFFFFFFFFu;
-  const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.f);
+  const uint32_t b = x != x ? 0x7FC00000u : __builtin_bit_cast(uint32_t, x + 0.f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t o) {
-  return __builtin_bit_cast(float, o & 0x80000000u ? (o == 0xFFFFFFFFu ? 0x7FC00000u : o & 0x7FFFFFFFu) : ~o);
+  return __builtin_bit_cast(float, o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
   return static_cast<uint64_t>(ordered(x)) << 32 | (0xFFFFFFFFu - index);
