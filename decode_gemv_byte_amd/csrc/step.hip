@@ -15,7 +15,12 @@
 
 namespace {
 
-typedef __attribute__((ext_vector_type(8))) float f32x8_t;
+// Eight logits as they are loaded: FP32 rows begin at any multiple of 16 bytes, which is
+// less than a vector of 8 floats asks for.
+struct F32x8 {
+  f32x4_t lo, hi;
+};
+static_assert(alignof(F32x8) == 16 && alignof(u32x4_t) == 16, "what nwc_token_logprobs checks");
 
 // Sum over the wavefront, in every lane.
 __device__ __forceinline__ float wave_sum(float v) {
@@ -341,11 +346,14 @@ __global__ __launch_bounds__(kLpThreads) void k_logprobs(const LogprobsArgs a) {
 
   // pieces of 8, the last of which may be short and is filled with -infinity
   const uint32_t full = n / 8;
-  typedef std::conditional_t<F32, f32x8_t, u32x4_t> Raw;
+  typedef std::conditional_t<F32, F32x8, u32x4_t> Raw;
   auto values = [&](const Raw& r, float (&x)[8]) {
     if constexpr (F32) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = r[j];
+      for (int j = 0; j < 4; ++j) {
+        x[j] = r.lo[j];
+        x[4 + j] = r.hi[j];
+      }
     } else {
       unpack8(r, x);
     }
