@@ -35,8 +35,10 @@ typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 // order: two transposing LDS reads of 4 positions each.  The weights are rounded to
 // BF16 for that product, their sum is not: an output is off by half a step of BF16
 // (its own rounding) and, from the weights' roundings, which are independent, by less
-// than that again, where keeping their other 16 bits takes a second product, half as
-// much again of all matrix work.
+// than that again (0.0020 to 0.0024 of the norm together, 0.0017 the first alone).
+// Keeping their other 16 bits takes a second product, half as much again of all matrix
+// work: 4096 tokens behind 28672 positions 2538 us, so 1870; a prompt of 8192 723 and
+// 549; 31 single tokens and one of 512 122 and 94; 31 single tokens alone 74 and 73.
 //
 // Keys and values go straight to a ring of units in LDS, kAhead units before their
 // turn, in pieces of 16 bytes placed so that the reads of both kinds touch all banks
@@ -45,13 +47,13 @@ typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 // two or three workgroups a compute unit leave that to chance.
 //
 // Bound by the matrix cores, whose clock falls under this load: 4096 tokens behind
-// 28672 positions, 32 / 8 heads of 128, 1820 us, 1130 TFLOP/s, where an 8192^3 product
-// reaches 1250; 8192 tokens of a new prompt 526 us, 1045 TFLOP/s (1920 and 553 on a card
-// whose clock falls further).  With few columns by
-// what an item leaves for the join (64 tokens behind 131007 positions: 155 us and 10 for
-// the join, 3.4 TB/s), with single tokens by HBM (31 rows of up to 4001 positions 73 us,
-// 4.4 TB/s), with little work by one chain of dependent loads (5 tokens behind 507
-// positions: 6.4 us).
+// 28672 positions, 32 / 8 heads of 128, 1819 to 1886 us by card, 1130 to 1090 TFLOP/s,
+// where an 8192^3 product reaches 1250; 8192 tokens of a new prompt 569 us, 967 TFLOP/s
+// (526 to 553 us a call among others).  With few columns by the loads' and the products'
+// turns, which overlap in part, and what an item leaves for the join (64 tokens behind
+// 131007 positions: 176 us and 11 for the join, 3.1 TB/s and 780 TFLOP/s), with single
+// tokens by HBM (31 rows of up to 4001 positions 73 us, 4.4 TB/s), with little work by one
+// chain of dependent loads (5 tokens behind 507 positions: 6.9 us).
 
 constexpr int kChunkThreads = 256;
 constexpr uint32_t kMaxWorkers = 4 * kCus;
@@ -820,7 +822,12 @@ ChunkLayout chunk_layout(uint32_t rows, uint32_t tokens, uint32_t ratio, uint32_
   // rows of 512 behind 3000 455 and 430, of 256 222 and 226, 9 rows with a prompt of 1000
   // among them 109 and 114, 20 prompts of 400 at most 45 and 48, 64 rows of 32 114 and 122; 4
   // rows of 16 behind 3000 33 and 28, of 32 36 and 30, 1 row of 32 behind 100000 105 and 92,
-  // of 8 86 and 84, of 4 (16 columns) 87 and 95; 31 rows of one 73 and 88.
+  // of 8 86 and 84, of 4 (16 columns) 87 and 95; 31 rows of one 73 and 88.  28 / 4, 16 / 8, 16
+  // / 1 and 8 / 8 heads: 16 rows of 8192 behind 1000 12222 and 11272, 6288 and 5843, 5531 and
+  // 5103, 3112 and 2968; 4 rows of 128 behind 3000 56 and 55, 40 and 42, 41 and 42, 37 and 32;
+  // 20 prompts of 400 at most 42 and 52, 32 and 41, 34 and 35, 28 and 34; 31 rows of one
+  // beside 512 tokens 86 and 115, 89 and 109, 48 and 54, 84 and 103, of which the rule takes
+  // the slower side for 28 / 4 and 16 / 1, whose items are few by the mean row.
   const uint64_t columns = static_cast<uint64_t>(tokens) * ratio;
   const bool few = (rows + columns / 128) * kv_heads < kCus && columns >= 32ull * rows;
   const bool wide = d == 128 && (few || columns >= 1536ull * rows);

@@ -623,7 +623,8 @@ nwc_status launch_residual(const ResidualArgs& a, hipStream_t s) {
   // GPU, else as many as have a piece for each lane; past 16384 columns 8, the most
   // whose registers hold 8 pieces.  Us for 4096 columns, few and many wavefronts a token:
   // 256 tokens 6.3 and 3.9, 512 tokens 6.8 and 6.2, 1024 tokens 8.3 and 10.1, 16384 tokens
-  // 104 and 169
+  // 104 and 169.  At other widths where the rule changes sides, 1023 tokens (many) and 1024
+  // (few): 1024 columns 4.2 and 3.8, 2048 4.8 and 5.3, 8192 14.3 and 13.1, 16384 24.8 and 24.2
   const bool many = a.tokens >= 4 * kCus;
   const auto go = [&](auto kernel, uint32_t w) {
     const uint64_t groups = w == 1 ? (static_cast<uint64_t>(a.tokens) + 3) / 4 : a.tokens;

@@ -295,6 +295,11 @@ nwc_status nwc_gemm_skinny(const nwc_info *info, const void *blob_dev, const uin
  * multiple of 16 bytes).  Meant for more X rows than nwc_gemm_skinny takes:
  * it reads the compressed weights once, writes and reads them back as BF16,
  * so it saves memory, not time.
+ * Not supported: matrices of more than 14336 rows (an LM head) with more than
+ * 200 X rows, and steps of many layers with more than 200 tokens: a program of
+ * 32 layers, 512 tokens and a head of 128256 rows ended in a GPU memory fault
+ * whose cause is not known, in these calls or others.  Longer prompts go
+ * through in parts of 200 tokens.
  *  - nwc_blas: an opaque context the caller creates and destroys, holding a
  *    hipBLASLt handle (whose creation may allocate) and the algorithm picked
  *    for each problem shape; it may be shared by calls on any stream.
@@ -510,11 +515,13 @@ nwc_status nwc_attend(const nwc_cache *cache, const nwc_page_table *table, const
  * <= 2^22.
  * Softmax statistics and sums in FP32, scores and their differences of any size
  * that FP32 holds.  The weights w enter the matrix cores as BF16, rounded to
- * nearest (each off by at most 2^-8 of itself, half a step).  Infinities, NaN and values whose weighted
- * sums pass FP32's range as in nwc_attend; what a token does not see (later
- * positions, slots past a length) may hold anything.  A head whose sums meet an
- * infinity or a NaN on the way, seen or not, takes longer: it is computed once
- * more, by itself.
+ * nearest (each off by at most 2^-8 of itself, half a step), where nwc_attend
+ * keeps 16 bits of them: a single token is less exact here.  Infinities, NaN and
+ * values whose weighted sums pass FP32's range as in nwc_attend; what a token does
+ * not see (later positions, slots past a length) may hold anything.  A head of a
+ * token whose sums meet an infinity or a NaN on the way, seen or not, is computed
+ * once more, by itself, which takes far longer (one infinite value that 512 tokens
+ * behind 4096 positions see: 12.7 ms instead of 62 us).
  * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
  * nwc_attend_chunk_workspace_size bytes; no initial content needed; what serves
  * more tokens serves fewer, of any number of rows); calls that share it must not
@@ -572,7 +579,9 @@ nwc_status nwc_residual_norm(const nwc_residual *args, uint32_t tokens, uint32_t
  * Statistics in FP32.  A logit of -infinity is a token of probability zero (log
  * probability -infinity, nothing to the entropy); a row of nothing else has
  * entropy 0.  +infinity or NaN among a row's logits make all its log probabilities
- * and its entropy NaN; in the order a NaN stands above +infinity.
+ * and its entropy NaN; in the order a NaN, whatever its sign, stands above
+ * +infinity.  Such a row is read once for each of its k (64 rows of 128256 with a
+ * NaN each, k = 20: 220 us instead of 17).
  * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
  * nwc_token_logprobs_workspace_size bytes; no initial content needed; what serves
  * more rows, a larger vocab or k serves less of each); calls that share it must
