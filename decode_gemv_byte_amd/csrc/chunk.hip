@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "device_common.hpp"
 
@@ -38,7 +39,12 @@ typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 // than that again (0.0020 to 0.0024 of the norm together, 0.0017 the first alone).
 // Keeping their other 16 bits takes a second product, half as much again of all matrix
 // work: 4096 tokens behind 28672 positions 2538 us, so 1870; a prompt of 8192 723 and
-// 549; 31 single tokens and one of 512 122 and 94; 31 single tokens alone 74 and 73.
+// 549.  Items of up to 32 columns, which are not bound by the matrix cores, take it, so
+// that a token by itself or a few drafted ones come out as by nwc_attend, off by their
+// own rounding alone (us with and without: 31 rows of one with heads of 64 47.5 and 44.6,
+// of 128 76.7 and 74.7, of 192 70.5 and 69.9, of 256 107 and 92; 8 tokens behind 131007
+// positions 111 and 107; 5 behind 507 16.0 and 15.5; 31 of one and one of 512 with heads
+// of 64 101 and 96).
 //
 // Keys and values go straight to a ring of units in LDS, kAhead units before their
 // turn, in pieces of 16 bytes placed so that the reads of both kinds touch all banks
@@ -52,7 +58,7 @@ typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 // (526 to 553 us a call among others).  With few columns by the loads' and the products'
 // turns, which overlap in part, and what an item leaves for the join (64 tokens behind
 // 131007 positions: 176 us and 11 for the join, 3.1 TB/s and 780 TFLOP/s), with single
-// tokens by HBM (31 rows of up to 4001 positions 73 us, 4.4 TB/s), with little work by one
+// tokens by HBM (31 rows of up to 4001 positions 77 us, 4.2 TB/s), with little work by one
 // chain of dependent loads (5 tokens behind 507 positions: 6.9 us).
 
 constexpr int kChunkThreads = 256;
@@ -523,6 +529,45 @@ __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, con
     l += sum[0] + sum[1];
   };
 
+  // The same with the weights' lower 16 bits by a second product, one step's values on
+  // their way beside its weights: few registers, for items that one wavefront has alone.
+  auto weigh_fine = [&](uint32_t vt, const f32x16_t (&sc)[kKt]) {
+    const uint32_t at = vt + value_at;
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 2 * kKt; ++s) {
+      u32x4_t hi, lo;
+      u32x2_t vf[kDt][2];
+#pragma unroll
+      for (int d = 0; d < kDt; ++d) {
+        const uint32_t to = (at ^ (d % kDx * 64)) + (16 * s * D * 2 + d / kDx * (kDx * 64));
+        vf[d][0] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds8*)static_cast<uintptr_t>(to)));
+        vf[d][1] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds8*)static_cast<uintptr_t>(to + 8 * D * 2)));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(sc[s / 2][8 * (s % 2) + 2 * j], a.scale2, -mc));
+        const float y = __builtin_amdgcn_exp2f(fmaf(sc[s / 2][8 * (s % 2) + 2 * j + 1], a.scale2, -mc));
+        sum[0] += x;
+        sum[1] += y;
+        hi[j] = pack_bf16(x, y);
+        lo[j] = pack_bf16(x - bf16_lo(hi[j]), y - bf16_hi(hi[j]));
+      }
+#pragma unroll
+      for (int d = 0; d < kDt; ++d) {
+        const u32x4_t v = {vf[d][0][0], vf[d][0][1], vf[d][1][0], vf[d][1][1]};
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, hi), o[d], 0, 0, 0);
+      }
+#pragma unroll
+      for (int d = 0; d < kDt; ++d) {
+        const u32x4_t v = {vf[d][0][0], vf[d][0][1], vf[d][1][0], vf[d][1][1]};
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, lo), o[d], 0, 0, 0);
+      }
+    }
+    l += sum[0] + sum[1];
+  };
+
   __syncthreads();  // the ring is free (the plan or the item before lay there)
 #pragma unroll
   for (uint32_t i = 0; i < S::kAhead; ++i)
@@ -544,27 +589,38 @@ __device__ __forceinline__ void run_item(const ChunkArgs& a, const Item& it, con
     else
       wait_vmem<0>();
   };
-  uint32_t place = 0;  // of unit u in the ring
-  if (behind) {
-    arrived(u0);
-    __syncthreads();
-  }
-  for (uint32_t u = u0; u < u1; ++u) {
-    if (!behind) arrived(u);
-    __syncthreads();
-    if (u + S::kAhead < u1) issue(u + S::kAhead, ring + (place + S::kAhead * kGroup) % kEnd);
-    f32x16_t sc[kKt];
-    if (u < uw) {
-      scores(ring + place, sc);
-      settle(u, sc);
-    }
-    if constexpr (W == 8) {
-      if (behind && u + 1 < u1) arrived(u + 1);
+  auto walk = [&](auto fine) __attribute__((always_inline)) {
+    uint32_t place = 0;  // of unit u in the ring
+    if (behind) {
+      arrived(u0);
       __syncthreads();
     }
-    if (u < uw) weigh(ring + place + S::kTile, sc);
-    place = (place + kGroup) % kEnd;
-  }
+    for (uint32_t u = u0; u < u1; ++u) {
+      if (!behind) arrived(u);
+      __syncthreads();
+      if (u + S::kAhead < u1) issue(u + S::kAhead, ring + (place + S::kAhead * kGroup) % kEnd);
+      f32x16_t sc[kKt];
+      if (u < uw) {
+        scores(ring + place, sc);
+        settle(u, sc);
+      }
+      if constexpr (W == 8) {
+        if (behind && u + 1 < u1) arrived(u + 1);
+        __syncthreads();
+      }
+      if (u < uw) {
+        if constexpr (decltype(fine)::value)
+          weigh_fine(ring + place + S::kTile, sc);
+        else
+          weigh(ring + place + S::kTile, sc);
+      }
+      place = (place + kGroup) % kEnd;
+    }
+  };
+  if (cols <= 32)  // tokens by themselves or a few together: see above
+    walk(std::true_type{});
+  else
+    walk(std::false_type{});
   if (W == 8 && !behind) __syncthreads();
   if (!works) return;
   const bool direct = u0 == 0 && u1 == units;

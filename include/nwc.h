@@ -515,13 +515,14 @@ nwc_status nwc_attend(const nwc_cache *cache, const nwc_page_table *table, const
  * <= 2^22.
  * Softmax statistics and sums in FP32, scores and their differences of any size
  * that FP32 holds.  The weights w enter the matrix cores as BF16, rounded to
- * nearest (each off by at most 2^-8 of itself, half a step), where nwc_attend
- * keeps 16 bits of them: a single token is less exact here.  Infinities, NaN and
- * values whose weighted sums pass FP32's range as in nwc_attend; what a token does
- * not see (later positions, slots past a length) may hold anything.  A head of a
- * token whose sums meet an infinity or a NaN on the way, seen or not, is computed
- * once more, by itself, which takes far longer (one infinite value that 512 tokens
- * behind 4096 positions see: 12.7 ms instead of 62 us).
+ * nearest (each off by at most 2^-8 of itself, half a step), of rows whose tokens
+ * times q_heads / kv_heads are at most 32 with 16 bits, as in nwc_attend (2^-16).
+ * Infinities, NaN and values whose weighted sums pass FP32's range as in
+ * nwc_attend; what a token does not see (later positions, slots past a length) may
+ * hold anything.  A head of a token whose sums meet an infinity or a NaN on the
+ * way, seen or not, is computed once more, by itself, which takes far longer (one
+ * infinite value that 512 tokens behind 4096 positions see: 12.7 ms instead of
+ * 62 us).
  * Repeated calls give the same bits.  ws (device, 256-byte aligned, at least
  * nwc_attend_chunk_workspace_size bytes; no initial content needed; what serves
  * more tokens serves fewer, of any number of rows); calls that share it must not
