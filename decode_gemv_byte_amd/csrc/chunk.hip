@@ -54,12 +54,12 @@ typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 //
 // Bound by the matrix cores, whose clock falls under this load: 4096 tokens behind
 // 28672 positions, 32 / 8 heads of 128, 1819 to 1886 us by card, 1130 to 1090 TFLOP/s,
-// where an 8192^3 product reaches 1250; 8192 tokens of a new prompt 569 us, 967 TFLOP/s
-// (526 to 553 us a call among others).  With few columns by the loads' and the products'
+// where an 8192^3 product reaches 1250; 8192 tokens of a new prompt 569 to 593 us, 967 to
+// 927 TFLOP/s (526 to 553 us a call among others).  With few columns by the loads' and the products'
 // turns, which overlap in part, and what an item leaves for the join (64 tokens behind
-// 131007 positions: 176 us and 11 for the join, 3.1 TB/s and 780 TFLOP/s), with single
+// 131007 positions: 176 to 179 us and 11 for the join, 3 TB/s and 780 TFLOP/s), with single
 // tokens by HBM (31 rows of up to 4001 positions 77 us, 4.2 TB/s), with little work by one
-// chain of dependent loads (5 tokens behind 507 positions: 6.9 us).
+// chain of dependent loads (5 tokens behind 507 positions: 7.7 us).
 
 constexpr int kChunkThreads = 256;
 constexpr uint32_t kMaxWorkers = 4 * kCus;
