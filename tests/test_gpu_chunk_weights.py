@@ -84,3 +84,72 @@ def test_the_same_token_by_either_attention(hq, hkv, d):
     # a step, 2^-7.5 of the value between them: 2^-9.5 for values of that size, some times more for smaller ones.  Weights
     # rounded once would move it by 2^-9 of that
     assert float((a != b).double().mean()) < 0.05
+
+
+def _check_all(c, what):
+    """Every finite component within the tolerance, every other one the reference's."""
+    ref, size = c.ref()
+    got = c.out.double()
+    assert bool((got.isnan() == ref.isnan()).all()), "%s: NaN in other places" % what
+    assert bool(((got == ref) | ~ref.isinf()).all()), "%s: other infinities" % what
+    err, tol = (got - ref).abs(), 2.0 ** -8 * ref.abs() + (2.0 ** -16 + 2.0 ** -10) * size
+    bad = ref.isfinite() & ~(err <= tol)
+    assert not bool(bad.any()), "%s: %d outside, first %s" % (what, int(bad.sum()), bad.nonzero()[0].tolist())
+
+
+SOME = [(32, 8, 128), (64, 8, 64), (20, 5, 96), (10, 5, 192), (8, 2, 256)]
+
+
+@pytest.mark.parametrize("hq,hkv,d", SOME)
+def test_infinities_nan_and_large_values_before_few_columns(hq, hkv, d):
+    # by one workgroup, and by several whose parts are joined
+    new, lengths = [1, 4, 2, 1, 3], [75, 104, 9000, 1, 333]
+    most = torch.finfo(torch.bfloat16).max
+    for kind in ("infinite", "nan", "largest", "smallest"):
+        _say("%s values, %d / %d heads of %d" % (kind, hq, hkv, d))
+        c = Case(new, lengths, hq, hkv, d, 32, seed=d)
+        if kind in ("largest", "smallest"):
+            g = torch.Generator(device="cuda").manual_seed(d)
+            c.v.copy_((torch.rand(c.v.shape, generator=g, device="cuda") * 0.5 + 0.5) * (most if kind == "largest" else 2.0 ** -108))
+            c.v[..., 1::2] *= torch.randint(0, 2, c.v[..., 1::2].shape, generator=g, device="cuda").mul_(2).sub_(1).to(torch.bfloat16)
+        else:
+            for r, n in enumerate(lengths):
+                at = np.arange(n)
+                pg, slot = torch.from_numpy(c.table[r, at // c.page]).cuda(), torch.from_numpy(at % c.page).cuda()
+                for e, p, value in ((3, 0, float("inf")), (5, n // 2, -float("inf")), (7, 0, -float("inf")), (7, n // 3, float("inf")),
+                                    (d - 1, n - 1, float("inf"))) if kind == "infinite" else ((3, 0, float("nan")), (9, n - 1, float("nan"))):
+                    c.v[pg[p], :, slot[p], e] = value
+        nwc.nwc_attend_chunk(c.call())
+        torch.cuda.synchronize()
+        if kind in ("infinite", "nan"):
+            # what a token does not see may be infinite or NaN too; the reference multiplies it by zero: component by component
+            ref, size = c.ref()
+            for r, n in enumerate(lengths):
+                t0, own = int(c.start[r]), n - int(c.new[r])
+                for i in range(int(c.new[r])):
+                    seen = own + i + 1
+                    one = Case([1], [seen], hq, hkv, d, c.page)
+                    one.k, one.v, one.table, one.q = c.k, c.v, c.table[r:r + 1], c.q[t0 + i:t0 + i + 1]
+                    ref[t0 + i:t0 + i + 1], size[t0 + i:t0 + i + 1] = one.ref()
+            c.ref = lambda: (ref, size)
+        _check_all(c, kind)
+
+
+@pytest.mark.parametrize("hq,hkv,d", SOME)
+def test_scores_of_any_size_before_few_columns(hq, hkv, d):
+    # finite scores far from zero, all equal or so far apart that the largest takes all; keys and queries are powers of two times
+    # at most 8 bits, so that FP32 holds each score exactly
+    _say("scores of any size, %d / %d heads of %d" % (hq, hkv, d))
+    lengths = [300, 77, 300, 3000, 1]
+    c = Case([1, 2, 3, 1, 1], lengths, hq, hkv, d, 32, seed=d + 1)
+    rnd = np.random.default_rng(d)
+    for r, (q, k, steps) in enumerate(((2.0 ** 50, -2.0 ** 50, 0), (2.0 ** 50, 2.0 ** 50, 0), (2.0 ** 18, 2.0 ** 18, 127),
+                                       (2.0 ** 18, -2.0 ** 18, 127), (2.0 ** 20, -2.0 ** 20, 0))):
+        at = np.arange(lengths[r])
+        pg, slot = torch.from_numpy(c.table[r, at // c.page]).cuda(), torch.from_numpy(at % c.page).cuda()
+        c.q[int(c.start[r]):int(c.start[r + 1])] = q
+        key = torch.tensor(k * (1 + rnd.integers(0, steps + 1, lengths[r]) / 128), device="cuda").to(torch.bfloat16)
+        c.k[pg, :, slot] = key[:, None, None].expand(lengths[r], hkv, d)
+    nwc.nwc_attend_chunk(c.call())
+    torch.cuda.synchronize()
+    _check_all(c, "scores")
